@@ -1,0 +1,232 @@
+// One AdamW step over many tensors, moments in fp32 or in 8 bits.
+//
+// Mathematics, g' = grad_scale g:
+//   m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2,
+//   p = (1 - lr wd) p - (lr / c1) m / (sqrt(v) / sqrt(c2) + eps),  c = 1 - b^step.
+// In 8 bits m and sqrt(v) are e4m3 codes (the hardware's conversions) with an
+// fp32 unit per 256 elements, the largest magnitude / 448: the moments are
+// formed and used in fp32 and rounded once, to 4 significant bits (2^-4
+// relative), which the block's unit keeps within e4m3's range down to 2^-17
+// of the largest.
+//
+// Memory bound: per element 16 bytes in and 12 out in fp32 (14 with the bf16
+// copy), 10 + 6 in 8 bits.  One launch takes up to kMaxTensors tensors, whose
+// table travels by value in the kernel's arguments (no device copy of it to
+// keep), and cuts them into pieces of kPiece elements; a workgroup finds its
+// tensor from its number and streams one piece with 16-byte accesses, four
+// elements per lane.  A wave's 64 lanes then hold the 256 elements of one
+// 8-bit block, whose largest magnitude is a wave maximum.
+#include "launch.h"
+
+namespace occ {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kStep = kThreads * 4;  // elements per pass of the workgroup
+constexpr int kPasses = 4;
+constexpr int kPiece = kStep * kPasses;
+constexpr int kMaxTensors = 30;
+constexpr uint64_t kMaxBlocks = 0xffffffffull / kThreads;  // a launch holds fewer than 2^32 threads
+static_assert(kAdamwMaxElements / kPiece < kMaxBlocks, "one tensor fits a launch");
+constexpr int kQBlock = kWave * 4;  // OCC_ADAMW_BLOCK
+
+constexpr float kE4m3Max = 448.f, kE4m3Min = 0x1p-9f, kSmallest = 0x1p-100f;
+
+struct Table {
+    AdamwTensor t[kMaxTensors];
+    uint32_t first[kMaxTensors];  // first workgroup of each tensor
+    int count;
+};
+static_assert(sizeof(Table) + sizeof(AdamwStep) <= 4096, "kernel arguments");
+
+// Four consecutive values from element i of n; whole when they may be moved
+// as one vector.
+template <typename V, typename E>
+__device__ __forceinline__ void load4(const void *p, int64_t i, int64_t n, bool whole, E (&v)[4]) {
+    const E *q = static_cast<const E *>(p) + i;
+    if (whole) {
+        const V x = *reinterpret_cast<const V *>(q);
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = reinterpret_cast<const E *>(&x)[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = i + j < n ? q[j] : static_cast<E>(0);
+    }
+}
+template <typename V, typename E>
+__device__ __forceinline__ void store4(void *p, int64_t i, int64_t n, bool whole, const E (&v)[4]) {
+    E *q = static_cast<E *>(p) + i;
+    if (whole) {
+        V x;
+#pragma unroll
+        for (int j = 0; j < 4; j++) reinterpret_cast<E *>(&x)[j] = v[j];
+        *reinterpret_cast<V *>(q) = x;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (i + j < n) q[j] = v[j];
+    }
+}
+
+__device__ __forceinline__ void from_e4m3(uint32_t codes, float unit, float (&v)[4]) {
+    v[0] = unit * __builtin_amdgcn_cvt_f32_fp8(codes, 0);
+    v[1] = unit * __builtin_amdgcn_cvt_f32_fp8(codes, 1);
+    v[2] = unit * __builtin_amdgcn_cvt_f32_fp8(codes, 2);
+    v[3] = unit * __builtin_amdgcn_cvt_f32_fp8(codes, 3);
+}
+__device__ __forceinline__ uint32_t to_e4m3(const float (&v)[4]) {
+    int c = 0;
+    c = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], c, false);
+    c = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], c, true);
+    return static_cast<uint32_t>(c);
+}
+
+// The wave's 256 values as codes, and their unit.  SQUARED: v holds sqrt(v),
+// whose nonzero values keep a nonzero code.
+template <bool SQUARED>
+__device__ __forceinline__ uint32_t quantise(const float (&v)[4], float &unit) {
+    const float top = wave_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])),
+                                     fmaxf(fabsf(v[2]), fabsf(v[3]))));
+    unit = 0.f;
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
+    if (!(top < kSmallest)) {
+        unit = top / kE4m3Max;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            c[j] = v[j] / unit;
+            // NaN (from a gradient that is not finite) passes both
+            c[j] = c[j] > kE4m3Max ? kE4m3Max : c[j] < -kE4m3Max ? -kE4m3Max : c[j];
+            if (SQUARED && v[j] > 0.f && c[j] < kE4m3Min) c[j] = kE4m3Min;
+        }
+    }
+    return to_e4m3(c);
+}
+
+template <bool Q8, bool GBF16>
+__global__ __launch_bounds__(kThreads) void k_adamw(Table tab, AdamwStep st) {
+    int a = 0;
+    for (int hi = tab.count; hi - a > 1;) {  // the last tensor with first <= blockIdx.x
+        const int mid = (a + hi) >> 1;
+        if (tab.first[mid] <= blockIdx.x)
+            a = mid;
+        else
+            hi = mid;
+    }
+    const AdamwTensor &T = tab.t[a];
+    const int64_t n = T.n;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x - tab.first[a]) * kPiece;
+    float lr = st.lr, c1 = st.c1, c2_rsqrt = st.c2_rsqrt, gs = st.grad_scale;
+    if (st.dynamic) {
+        lr = st.dynamic[0];
+        const float step = st.dynamic[1];
+        gs = st.dynamic[2];
+        c1 = -expm1f(step * st.log_b1);
+        c2_rsqrt = 1.f / sqrtf(-expm1f(step * st.log_b2));
+    }
+    const float decay = fmaf(-lr, st.weight_decay, 1.f), rate = lr / c1;
+#pragma unroll
+    for (int u = 0; u < kPasses; u++) {
+        const int64_t i = i0 + u * kStep + threadIdx.x * 4;
+        // a wave whose elements all lie behind the tensor's end has nothing to do
+        if (i0 + u * kStep + (threadIdx.x & ~(kWave - 1)) * 4 >= n) break;
+        const bool whole = T.aligned && i + 4 <= n;
+        float p[4], g[4], m[4], v[4];
+        load4<f32x4, float>(T.p, i, n, whole, p);
+        if constexpr (GBF16) {
+            typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+            uint16_t gb[4];
+            load4<u16x4, uint16_t>(T.g, i, n, whole, gb);
+#pragma unroll
+            for (int j = 0; j < 4; j++) g[j] = bf16_bits_to_f32(gb[j]);
+        } else {
+            load4<f32x4, float>(T.g, i, n, whole, g);
+        }
+        const int64_t qb = i / kQBlock;
+        if constexpr (Q8) {
+            typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
+            uint8_t mc[4], vc[4];
+            load4<u8x4, uint8_t>(T.m, i, n, whole, mc);
+            load4<u8x4, uint8_t>(T.v, i, n, whole, vc);
+            // a lane behind the end holds zeros; its block exists (the wave's first lane's does)
+            from_e4m3(mc[0] | mc[1] << 8 | mc[2] << 16 | static_cast<uint32_t>(mc[3]) << 24,
+                      T.m_scale[qb], m);
+            from_e4m3(vc[0] | vc[1] << 8 | vc[2] << 16 | static_cast<uint32_t>(vc[3]) << 24,
+                      T.v_scale[qb], v);
+#pragma unroll
+            for (int j = 0; j < 4; j++) v[j] *= v[j];
+        } else {
+            load4<f32x4, float>(T.m, i, n, whole, m);
+            load4<f32x4, float>(T.v, i, n, whole, v);
+        }
+        float root[4];
+        uint16_t copy[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float gj = g[j] * gs;
+            m[j] = fmaf(st.beta1, m[j], st.one_b1 * gj);
+            v[j] = fmaf(st.beta2, v[j], st.one_b2 * gj * gj);
+            root[j] = sqrtf(v[j]);
+            p[j] = fmaf(decay, p[j], -rate * (m[j] / fmaf(root[j], c2_rsqrt, st.eps)));
+            copy[j] = f32_to_bf16_bits(p[j]);
+        }
+        store4<f32x4, float>(T.p_out, i, n, whole, p);
+        if (T.p_bf16) {
+            typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+            store4<u16x4, uint16_t>(T.p_bf16, i, n, whole, copy);
+        }
+        if constexpr (Q8) {
+            typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
+            float um, uv;
+            const uint32_t qm = quantise<false>(m, um), qv = quantise<true>(root, uv);
+            const uint8_t mc[4] = {static_cast<uint8_t>(qm), static_cast<uint8_t>(qm >> 8),
+                                   static_cast<uint8_t>(qm >> 16), static_cast<uint8_t>(qm >> 24)};
+            const uint8_t vc[4] = {static_cast<uint8_t>(qv), static_cast<uint8_t>(qv >> 8),
+                                   static_cast<uint8_t>(qv >> 16), static_cast<uint8_t>(qv >> 24)};
+            store4<u8x4, uint8_t>(T.m_out, i, n, whole, mc);
+            store4<u8x4, uint8_t>(T.v_out, i, n, whole, vc);
+            if (lane_id() == 0) {
+                T.m_scale_out[qb] = um;
+                T.v_scale_out[qb] = uv;
+            }
+        } else {
+            store4<f32x4, float>(T.m_out, i, n, whole, m);
+            store4<f32x4, float>(T.v_out, i, n, whole, v);
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamwTensor *tensors, int count, const AdamwStep &st, int q8,
+                        int grad_bf16, hipStream_t s) {
+    int i = 0;
+    while (i < count) {
+        Table tab;
+        tab.count = 0;
+        uint64_t blocks = 0;
+        for (; i < count && tab.count < kMaxTensors; i++) {
+            if (tensors[i].n == 0) continue;
+            const uint64_t need = static_cast<uint64_t>((tensors[i].n + kPiece - 1) / kPiece);
+            if (blocks && blocks + need > kMaxBlocks) break;
+            tab.t[tab.count] = tensors[i];
+            tab.first[tab.count] = static_cast<uint32_t>(blocks);
+            tab.count++;
+            blocks += need;
+        }
+        if (tab.count == 0) continue;
+        const unsigned grid = static_cast<unsigned>(blocks);
+        if (q8 && grad_bf16)
+            k_adamw<true, true><<<grid, kThreads, 0, s>>>(tab, st);
+        else if (q8)
+            k_adamw<true, false><<<grid, kThreads, 0, s>>>(tab, st);
+        else if (grad_bf16)
+            k_adamw<false, true><<<grid, kThreads, 0, s>>>(tab, st);
+        else
+            k_adamw<false, false><<<grid, kThreads, 0, s>>>(tab, st);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace occ

@@ -1,6 +1,7 @@
 // C ABI of the Occult MoE-layer library: argument checks, workspace layout,
 // and the stage sequence of the layer (declarations and contracts in occ.h).
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -313,6 +314,52 @@ occ_status noalloc_scratch(void **out) {
     } while (0)
 
 #define OCC_HIP(expr) OCC_TRY(hip_status(expr))
+
+bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Whether each of these arrays (NULL among them) starts on a 16-byte border.
+template <typename... P>
+bool rows_aligned(P... p) {
+    return (aligned_to(p, 16) && ...);
+}
+
+int row_chunks(const occ_layer_desc &D) { return static_cast<int>(D.d * elem_bytes(D) / 16); }
+
+// Scratch of the operators around the layer: the largest of their needs.
+size_t block_ws_bytes(const occ_layer_desc &D) {
+    const size_t d = D.d, bf16 = D.dtype == OCC_BF16;
+    return align_up(std::max<size_t>(
+        {norm_back_blocks(D.T, row_chunks(D)) * 3 * d * 4, balance_part_bytes(D.T, D.Ne),
+         static_cast<size_t>(gate_dw_shares(D.T, D.d, D.Ne, bf16)) * D.Ne * d * 4}));
+}
+
+occ_status check_norm(const occ_layer_desc *desc, const occ_norm_desc *opt) {
+    OCC_TRY(check_desc(desc));
+    if (!opt || !std::isfinite(opt->eps) || opt->eps <= 0.f || !std::isfinite(opt->scale) ||
+        opt->gate < OCC_GATE_NONE || opt->gate > OCC_GATE_TOKEN)
+        return OCC_ERR_INVALID_ARG;
+    return OCC_OK;
+}
+
+// The gate's pointer matches its kind: rows of 16-byte chunks or floats.
+bool gate_fits(const occ_norm_desc &opt, const void *gate) {
+    if (opt.gate == OCC_GATE_NONE) return !gate;
+    return gate && aligned_to(gate, opt.gate == OCC_GATE_CHANNEL ? 16 : 4);
+}
+
+// The placement table for the router's losses, which use it for the group
+// term alone: experts in order when there is none.
+occ_status balance_tab(const occ_layer_desc &D, const occ_balance_desc *opt, const int32_t *L,
+                       PlaceTab *tab) {
+    if (!opt || !std::isfinite(opt->balance) || !std::isfinite(opt->group) ||
+        !std::isfinite(opt->z))
+        return OCC_ERR_INVALID_ARG;
+    if (L) return make_tab(D, L, tab);
+    if (opt->group != 0.f) return OCC_ERR_INVALID_ARG;
+    int32_t order[kMaxNe];
+    for (int e = 0; e < D.Ne; e++) order[e] = e;
+    return make_tab(D, order, tab);
+}
 
 }  // namespace
 
@@ -637,6 +684,167 @@ occ_status occ_gate(const occ_layer_desc *desc, const void *x, const void *w_rou
     if (!x || !w_router || !logits) return OCC_ERR_INVALID_ARG;
     OCC_HIP(launch_gate(x, w_router, desc->T, desc->d, desc->Ne, desc->dtype == OCC_BF16, logits,
                         static_cast<hipStream_t>(stream)));
+    return OCC_OK;
+}
+
+occ_status occ_block_workspace_size(const occ_layer_desc *desc, size_t *bytes_host) {
+    OCC_TRY(check_desc(desc));
+    if (!bytes_host) return OCC_ERR_INVALID_ARG;
+    *bytes_host = block_ws_bytes(*desc);
+    return OCC_OK;
+}
+
+occ_status occ_block_norm(const occ_layer_desc *desc, const occ_norm_desc *opt, const void *x,
+                          const void *y, const void *w_post, const void *gate, const void *w_pre,
+                          void *r, void *h, void *stream) {
+    OCC_TRY(check_norm(desc, opt));
+    if (!x || !gate_fits(*opt, gate) || !w_pre != !h) return OCC_ERR_INVALID_ARG;
+    if (y ? !r : r || w_post || gate || !h) return OCC_ERR_INVALID_ARG;
+    if (!rows_aligned(x, y, w_post, w_pre, r, h)) return OCC_ERR_INVALID_ARG;
+    OCC_HIP(launch_block_norm(x, y, w_post, gate, w_pre, desc->T, desc->d,
+                              desc->dtype == OCC_BF16, opt->gate, opt->eps, opt->scale, r, h,
+                              static_cast<hipStream_t>(stream)));
+    return OCC_OK;
+}
+
+occ_status occ_block_norm_backward(const occ_layer_desc *desc, const occ_norm_desc *opt,
+                                   const void *dr, const void *dh, const void *r, const void *y,
+                                   const void *w_post, const void *gate, const void *w_pre,
+                                   void *dx, void *dy, float *dw_post, float *dgate,
+                                   float *dw_pre, void *workspace, size_t ws_bytes,
+                                   void *stream) {
+    OCC_TRY(check_norm(desc, opt));
+    if (!dx || !gate_fits(*opt, gate) || (!dr && !dh)) return OCC_ERR_INVALID_ARG;
+    if (!w_pre != !dh || !w_pre != !dw_pre || !w_post != !dw_post || !gate != !dgate)
+        return OCC_ERR_INVALID_ARG;
+    if ((w_pre && !r) || ((w_post || gate) && (!y || !dy)) || (y && !dy))
+        return OCC_ERR_INVALID_ARG;
+    if (!rows_aligned(dr, dh, r, y, w_post, w_pre, dx, dy) || !aligned_to(dw_post, 4) ||
+        !aligned_to(dgate, 4) || !aligned_to(dw_pre, 4))
+        return OCC_ERR_INVALID_ARG;
+    OCC_TRY(check_ws(*desc, workspace, ws_bytes, block_ws_bytes(*desc)));
+    OCC_HIP(launch_block_norm_back(dr, dh, r, y, w_post, gate, w_pre, desc->T, desc->d,
+                                   desc->dtype == OCC_BF16, opt->gate, opt->eps, opt->scale, dx,
+                                   dy, dw_post, dgate, dw_pre, static_cast<float *>(workspace),
+                                   static_cast<hipStream_t>(stream)));
+    return OCC_OK;
+}
+
+occ_status occ_balance_loss(const occ_layer_desc *desc, const occ_balance_desc *opt,
+                            const float *logits, const int32_t *ids, const uint8_t *valid,
+                            const int32_t *placement_host, int32_t *counts, float *probs,
+                            float *loss, void *workspace, size_t ws_bytes, void *stream) {
+    OCC_TRY(check_desc(desc));
+    if (!logits || !ids || !counts || !probs || !loss) return OCC_ERR_INVALID_ARG;
+    if (!aligned_to(logits, 4) || !aligned_to(ids, 4) || !aligned_to(counts, 4) ||
+        !aligned_to(probs, 4) || !aligned_to(loss, 4))
+        return OCC_ERR_INVALID_ARG;
+    PlaceTab tab;
+    OCC_TRY(balance_tab(*desc, opt, placement_host, &tab));
+    OCC_TRY(check_ws(*desc, workspace, ws_bytes, block_ws_bytes(*desc)));
+    OCC_HIP(launch_balance(logits, ids, valid, desc->T, desc->k, tab, opt->balance, opt->group,
+                           opt->z, counts, probs, loss, static_cast<float *>(workspace),
+                           static_cast<hipStream_t>(stream)));
+    return OCC_OK;
+}
+
+occ_status occ_balance_backward(const occ_layer_desc *desc, const occ_balance_desc *opt,
+                                const float *logits, const uint8_t *valid,
+                                const int32_t *placement_host, const int32_t *counts, float dloss,
+                                const float *dlogits_in, float *dlogits, void *stream) {
+    OCC_TRY(check_desc(desc));
+    if (!logits || !counts || !dlogits || !std::isfinite(dloss)) return OCC_ERR_INVALID_ARG;
+    if (!aligned_to(logits, 4) || !aligned_to(counts, 4) || !aligned_to(dlogits_in, 4) ||
+        !aligned_to(dlogits, 4))
+        return OCC_ERR_INVALID_ARG;
+    PlaceTab tab;
+    OCC_TRY(balance_tab(*desc, opt, placement_host, &tab));
+    OCC_HIP(launch_balance_back(logits, valid, counts, tab, desc->T, desc->k, opt->balance,
+                                opt->group, opt->z, dloss, dlogits_in, dlogits,
+                                static_cast<hipStream_t>(stream)));
+    return OCC_OK;
+}
+
+occ_status occ_gate_backward(const occ_layer_desc *desc, const float *dlogits, const void *x,
+                             const void *w_router, const void *dx_in, void *dx, float *dw_router,
+                             void *workspace, size_t ws_bytes, void *stream) {
+    OCC_TRY(check_desc(desc));
+    if (!dlogits || (!dx && !dw_router)) return OCC_ERR_INVALID_ARG;
+    if (dx ? !w_router : !!dx_in) return OCC_ERR_INVALID_ARG;
+    if (dw_router && !x) return OCC_ERR_INVALID_ARG;
+    if (!aligned_to(dlogits, 4) || !rows_aligned(x, w_router, dx_in, dx, dw_router))
+        return OCC_ERR_INVALID_ARG;
+    if (dw_router) OCC_TRY(check_ws(*desc, workspace, ws_bytes, block_ws_bytes(*desc)));
+    const int bf16 = desc->dtype == OCC_BF16;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    // dw_router first: dx may be the array that holds x
+    if (dw_router)
+        OCC_HIP(launch_gate_dw(dlogits, x, desc->T, desc->d, desc->Ne, bf16,
+                               static_cast<float *>(workspace), dw_router, s));
+    if (dx)
+        OCC_HIP(launch_gate_dx(dlogits, w_router, dx_in, desc->T, desc->d, desc->Ne, bf16, dx, s));
+    return OCC_OK;
+}
+
+occ_status occ_adamw_step(const occ_adamw_desc *opt, const occ_adamw_tensor *tensors_host,
+                          int32_t count, const float *dynamic, void *stream) {
+    if (!opt || count < 0 || (count > 0 && !tensors_host)) return OCC_ERR_INVALID_ARG;
+    const auto ranged = [](double v, double lo, bool open) {
+        return std::isfinite(v) && (open ? v > lo : v >= lo);
+    };
+    if ((opt->state != OCC_ADAMW_32BIT && opt->state != OCC_ADAMW_8BIT) ||
+        (opt->grad_dtype != OCC_F32 && opt->grad_dtype != OCC_BF16) || !ranged(opt->lr, 0., false) ||
+        !ranged(opt->beta1, 0., false) || opt->beta1 >= 1. || !ranged(opt->beta2, 0., false) ||
+        opt->beta2 >= 1. || !(static_cast<float>(opt->eps) > 0.f) || !std::isfinite(opt->eps) ||
+        !ranged(opt->weight_decay, 0., false) || !std::isfinite(opt->grad_scale) || opt->step < 1 ||
+        !aligned_to(dynamic, 4))
+        return OCC_ERR_INVALID_ARG;
+    const bool q8 = opt->state == OCC_ADAMW_8BIT, gb = opt->grad_dtype == OCC_BF16;
+    const size_t ms = q8 ? 1 : 4;
+    std::vector<AdamwTensor> list;
+    try {
+        list.reserve(count);
+    } catch (...) {
+        return OCC_ERR_UNSUPPORTED;
+    }
+    for (int i = 0; i < count; i++) {
+        const occ_adamw_tensor &t = tensors_host[i];
+        if (t.n < 0) return OCC_ERR_INVALID_ARG;
+        if (t.n == 0) continue;
+        if (t.n > kAdamwMaxElements) return OCC_ERR_UNSUPPORTED;
+        if (!t.p || !t.g || !t.m || !t.v || !t.p_out || !t.m_out || !t.v_out)
+            return OCC_ERR_INVALID_ARG;
+        if (!t.m_scale == q8 || !t.v_scale == q8 || !t.m_scale_out == q8 || !t.v_scale_out == q8)
+            return OCC_ERR_INVALID_ARG;
+        const auto fits = [&](size_t k) {  // arrays aligned to k elements
+            return aligned_to(t.p, 4 * k) && aligned_to(t.g, (gb ? 2 : 4) * k) &&
+                   aligned_to(t.m, ms * k) && aligned_to(t.v, ms * k) &&
+                   aligned_to(t.p_out, 4 * k) && aligned_to(t.m_out, ms * k) &&
+                   aligned_to(t.v_out, ms * k) && aligned_to(t.p_bf16, 2 * k);
+        };
+        if (!fits(1) || !aligned_to(t.m_scale, 4) || !aligned_to(t.v_scale, 4) ||
+            !aligned_to(t.m_scale_out, 4) || !aligned_to(t.v_scale_out, 4))
+            return OCC_ERR_INVALID_ARG;
+        list.push_back({t.n, t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.p_out, t.m_out, t.v_out,
+                        t.m_scale_out, t.v_scale_out, t.p_bf16, fits(4)});
+    }
+    AdamwStep st;
+    const double step = static_cast<double>(opt->step);
+    st.lr = static_cast<float>(opt->lr);
+    st.beta1 = static_cast<float>(opt->beta1);
+    st.one_b1 = static_cast<float>(1. - opt->beta1);
+    st.beta2 = static_cast<float>(opt->beta2);
+    st.one_b2 = static_cast<float>(1. - opt->beta2);
+    st.eps = static_cast<float>(opt->eps);
+    st.weight_decay = static_cast<float>(opt->weight_decay);
+    st.grad_scale = static_cast<float>(opt->grad_scale);
+    st.log_b1 = static_cast<float>(std::log(opt->beta1));
+    st.log_b2 = static_cast<float>(std::log(opt->beta2));
+    st.c1 = static_cast<float>(-std::expm1(step * std::log(opt->beta1)));
+    st.c2_rsqrt = static_cast<float>(1. / std::sqrt(-std::expm1(step * std::log(opt->beta2))));
+    st.dynamic = dynamic;
+    OCC_HIP(launch_adamw(list.data(), static_cast<int>(list.size()), st, q8, gb,
+                         static_cast<hipStream_t>(stream)));
     return OCC_OK;
 }
 

@@ -230,6 +230,61 @@ hipError_t launch_route_backward(const float *logits, const int32_t *ids, const 
                                  const float *dw_part, int nparts, int dw_stride, int T, int Ne,
                                  int k, float *dw, float *dlogits, hipStream_t s);
 
+// --- norms, gate and residual between two blocks (norm.hip) ---
+// r = x + scale gate w_post n(y), h = w_pre n(r); gate_kind as occ_block_gate;
+// y, w_post, gate, w_pre with h may be NULL.
+hipError_t launch_block_norm(const void *x, const void *y, const void *w_post, const void *gate,
+                             const void *w_pre, int T, int d, int bf16, int gate_kind, float eps,
+                             float scale, void *r, void *h, hipStream_t s);
+// Its backward; part holds norm_back_blocks x 3 x d floats.
+int norm_back_blocks(int T, int chunks);  // chunks: 16-byte pieces of a row
+hipError_t launch_block_norm_back(const void *dr, const void *dh, const void *r, const void *y,
+                                  const void *w_post, const void *gate, const void *w_pre, int T,
+                                  int d, int bf16, int gate_kind, float eps, float scale, void *dx,
+                                  void *dy, float *dw_post, float *dgate, float *dw_pre,
+                                  float *part, hipStream_t s);
+
+// --- router losses (balance.hip) ---
+size_t balance_part_bytes(int T, int Ne);
+hipError_t launch_balance(const float *logits, const int32_t *ids, const uint8_t *valid, int T,
+                          int k, const PlaceTab &tab, float cb, float cg, float cz,
+                          int32_t *counts, float *probs, float *loss, float *part, hipStream_t s);
+hipError_t launch_balance_back(const float *logits, const uint8_t *valid, const int32_t *counts,
+                               const PlaceTab &tab, int T, int k, float cb, float cg, float cz,
+                               float dloss, const float *dlogits_in, float *dlogits,
+                               hipStream_t s);
+
+// --- gate projection, backward (gate_bwd.hip) ---
+// dx = dx_in + dl w_router (dx_in may be NULL);  dw = dl^T x through
+// gate_dw_shares x Ne x d partial sums in part.
+int gate_dw_shares(int T, int d, int Ne, int bf16);
+hipError_t launch_gate_dx(const float *dl, const void *w_router, const void *dx_in, int T, int d,
+                          int Ne, int bf16, void *dx, hipStream_t s);
+hipError_t launch_gate_dw(const float *dl, const void *x, int T, int d, int Ne, int bf16,
+                          float *part, float *dw, hipStream_t s);
+
+// --- optimizer step (adamw.hip) ---
+constexpr int64_t kAdamwMaxElements = 1ll << 35;  // of one tensor
+struct AdamwTensor {
+    int64_t n;
+    const float *p;
+    const void *g, *m, *v;
+    const float *m_scale, *v_scale;
+    float *p_out;
+    void *m_out, *v_out;
+    float *m_scale_out, *v_scale_out;
+    void *p_bf16;
+    int64_t aligned;  // every array may be moved four elements at a time
+};
+struct AdamwStep {
+    float lr, beta1, one_b1, beta2, one_b2, eps, weight_decay, grad_scale;
+    float c1, c2_rsqrt;     // 1 - beta1^step, 1 / sqrt(1 - beta2^step)
+    float log_b1, log_b2;   // for a step read from `dynamic`
+    const float *dynamic;   // NULL or {lr, step, grad_scale} on the device
+};
+hipError_t launch_adamw(const AdamwTensor *tensors, int count, const AdamwStep &st, int q8,
+                        int grad_bf16, hipStream_t s);
+
 // --- co-activation statistics (coact.hip) ---
 hipError_t launch_coact(const int32_t *ids, int T, int k, const PlaceTab &tab, int32_t *C,
                         float *P, int64_t *n_sfd, double *ct, double *intra, hipStream_t s);

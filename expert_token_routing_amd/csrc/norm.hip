@@ -1,0 +1,450 @@
+// The boundary between two transformer blocks: the norm behind a block, its
+// gate and residual scale, the residual addition and the norm in front of the
+// next block in one pass over the rows, and the backward pass of that.
+//
+// Mathematics (n(v) = v rstd(v), rstd = 1 / sqrt(mean v^2 + eps) by rows):
+//   r = x + s g w_post n(y),   h = w_pre n(r).
+// The gradient of <q, n(v)> in v is rstd q - v rstd^3 mean(q v), so a row's
+// backward needs three sums before dr' = dr + (gradient through h) is known
+// (r.r, (dh w_pre).r, y.y) and one after it ((s dr' g w_post).y).
+//
+// Memory bound: the forward reads x and y and writes r and h once, the
+// backward reads dr, dh, r and y and writes dx and dy once.  A row stays in
+// registers as 16-byte chunks from its loads to its stores (chunk c of a row
+// with the thread c mod NT, so that a wave's loads are contiguous): one wave
+// per row up to 256 chunks (d = 2048 in bf16) with DPP sums and no barrier,
+// a workgroup of 256 threads per row above.  Workgroups walk the rows with a
+// fixed stride and keep the weights in registers.  In the backward each
+// thread also keeps fp32 sums of its columns' weight gradients over its rows;
+// they go to the workspace once per workgroup and a second kernel adds the
+// workgroups' sums in order, so results do not depend on timing.
+#include "launch.h"
+
+namespace occ {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+
+// A chunk is 16 bytes of a row: E values.
+template <typename E>
+struct Chunk;
+template <>
+struct Chunk<uint16_t> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(const u32x4 &c, float (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(c[i] << 16);
+            v[2 * i + 1] = __uint_as_float(c[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ u32x4 pack(const float (&v)[N]) {
+        u32x4 c;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            c[i] = static_cast<uint32_t>(f32_to_bf16_bits(v[2 * i])) |
+                   static_cast<uint32_t>(f32_to_bf16_bits(v[2 * i + 1])) << 16;
+        return c;
+    }
+};
+template <>
+struct Chunk<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(const u32x4 &c, float (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = __uint_as_float(c[i]);
+    }
+    static __device__ __forceinline__ u32x4 pack(const float (&v)[N]) {
+        u32x4 c;
+#pragma unroll
+        for (int i = 0; i < 4; i++) c[i] = __float_as_uint(v[i]);
+        return c;
+    }
+};
+
+// Sum over the NT threads that share a row.  NT = kThreads: through LDS, with
+// two sets of slots used in turn (the next sum's writes cannot meet this
+// one's reads, since the barrier in between orders them).
+template <int NT, int M>
+__device__ __forceinline__ void row_sums(float (&v)[M], float (&slots)[2][3][kWaves], int &turn) {
+#pragma unroll
+    for (int i = 0; i < M; i++) v[i] = wave_sum(v[i]);
+    if constexpr (NT > kWave) {
+        const int w = threadIdx.x / kWave;
+        if (lane_id() == 0) {
+#pragma unroll
+            for (int i = 0; i < M; i++) slots[turn][i][w] = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < M; i++) {
+            v[i] = 0.f;
+#pragma unroll
+            for (int q = 0; q < kWaves; q++) v[i] += slots[turn][i][q];
+        }
+        turn ^= 1;
+    }
+}
+
+struct NormArgs {
+    const u32x4 *x, *y, *w_post, *w_pre;
+    const void *gate;
+    u32x4 *r, *h;
+    int T, chunks;  // rows, 16-byte chunks of a row
+    int gate_kind;  // occ_block_gate
+    float inv_d, eps, scale;
+};
+
+template <typename E, int NT, int VPT>
+__global__ __launch_bounds__(kThreads) void k_norm(NormArgs a) {
+    constexpr int N = Chunk<E>::N;
+    __shared__ float slots[2][3][kWaves];
+    int turn = 0;
+    const int lane = threadIdx.x % NT, rows = kThreads / NT;
+    const int row0 = blockIdx.x * rows + threadIdx.x / NT;
+    bool in[VPT];
+    u32x4 wpost[VPT], wpre[VPT], wgate[VPT];
+    const u32x4 zero = {0, 0, 0, 0};
+    const u32x4 *gate_ch = a.gate_kind == 1 ? static_cast<const u32x4 *>(a.gate) : nullptr;
+    const float *gate_tok = a.gate_kind == 2 ? static_cast<const float *>(a.gate) : nullptr;
+#pragma unroll
+    for (int j = 0; j < VPT; j++) {
+        const int c = lane + NT * j;
+        in[j] = c < a.chunks;
+        wpost[j] = in[j] && a.w_post ? a.w_post[c] : zero;
+        wpre[j] = in[j] && a.w_pre ? a.w_pre[c] : zero;
+        wgate[j] = in[j] && gate_ch ? gate_ch[c] : zero;
+    }
+    for (int t = row0; t < a.T; t += gridDim.x * rows) {
+        const size_t base = static_cast<size_t>(t) * a.chunks + lane;
+        u32x4 xr[VPT], yr[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; j++) {
+            xr[j] = in[j] ? a.x[base + NT * j] : zero;
+            yr[j] = in[j] && a.y ? a.y[base + NT * j] : zero;
+        }
+        float s = a.scale;
+        if (gate_tok) s *= gate_tok[t];
+        if (a.w_post) {
+            float ssq[1] = {0.f};
+#pragma unroll
+            for (int j = 0; j < VPT; j++) {
+                float v[N];
+                Chunk<E>::unpack(yr[j], v);
+#pragma unroll
+                for (int i = 0; i < N; i++) ssq[0] = fmaf(v[i], v[i], ssq[0]);
+            }
+            row_sums<NT>(ssq, slots, turn);
+            s *= 1.f / sqrtf(fmaf(ssq[0], a.inv_d, a.eps));
+        }
+        float r[VPT][N];
+        float ssq[1] = {0.f};
+#pragma unroll
+        for (int j = 0; j < VPT; j++) {
+            Chunk<E>::unpack(xr[j], r[j]);
+            if (a.y) {
+                float z[N], w[N];
+                Chunk<E>::unpack(yr[j], z);
+                if (a.w_post) {
+                    Chunk<E>::unpack(wpost[j], w);
+#pragma unroll
+                    for (int i = 0; i < N; i++) z[i] *= w[i];
+                }
+                if (gate_ch) {
+                    Chunk<E>::unpack(wgate[j], w);
+#pragma unroll
+                    for (int i = 0; i < N; i++) z[i] *= w[i];
+                }
+#pragma unroll
+                for (int i = 0; i < N; i++) r[j][i] = fmaf(s, z[i], r[j][i]);
+                if (in[j]) a.r[base + NT * j] = Chunk<E>::pack(r[j]);
+            }
+#pragma unroll
+            for (int i = 0; i < N; i++) ssq[0] = fmaf(r[j][i], r[j][i], ssq[0]);
+        }
+        if (!a.h) continue;
+        row_sums<NT>(ssq, slots, turn);
+        const float rstd = 1.f / sqrtf(fmaf(ssq[0], a.inv_d, a.eps));
+#pragma unroll
+        for (int j = 0; j < VPT; j++) {
+            float w[N];
+            Chunk<E>::unpack(wpre[j], w);
+#pragma unroll
+            for (int i = 0; i < N; i++) w[i] *= r[j][i] * rstd;
+            if (in[j]) a.h[base + NT * j] = Chunk<E>::pack(w);
+        }
+    }
+}
+
+struct NormBackArgs {
+    const u32x4 *dr, *dh, *r, *y, *w_post, *w_pre;
+    const void *gate;
+    u32x4 *dx, *dy;
+    float *dgate_tok;  // T values (gate_kind 2)
+    float *part;       // [workgroup][3][d]: dw_post, dgate, dw_pre sums
+    int T, chunks, gate_kind;
+    float inv_d, eps, scale;
+};
+
+template <typename E, int NT, int VPT>
+__global__ __launch_bounds__(kThreads) void k_norm_back(NormBackArgs a) {
+    constexpr int N = Chunk<E>::N;
+    __shared__ float slots[2][3][kWaves];
+    int turn = 0;
+    const int lane = threadIdx.x % NT, rows = kThreads / NT;
+    const int row0 = blockIdx.x * rows + threadIdx.x / NT;
+    const u32x4 zero = {0, 0, 0, 0};
+    const u32x4 *gate_ch = a.gate_kind == 1 ? static_cast<const u32x4 *>(a.gate) : nullptr;
+    const float *gate_tok = a.gate_kind == 2 ? static_cast<const float *>(a.gate) : nullptr;
+    bool in[VPT];
+    u32x4 wpost[VPT], wpre[VPT], wgate[VPT];
+    float acc_post[VPT][N], acc_gate[VPT][N], acc_pre[VPT][N];
+#pragma unroll
+    for (int j = 0; j < VPT; j++) {
+        const int c = lane + NT * j;
+        in[j] = c < a.chunks;
+        wpost[j] = in[j] && a.w_post ? a.w_post[c] : zero;
+        wpre[j] = in[j] && a.w_pre ? a.w_pre[c] : zero;
+        wgate[j] = in[j] && gate_ch ? gate_ch[c] : zero;
+#pragma unroll
+        for (int i = 0; i < N; i++) acc_post[j][i] = acc_gate[j][i] = acc_pre[j][i] = 0.f;
+    }
+    for (int t = row0; t < a.T; t += gridDim.x * rows) {
+        const size_t base = static_cast<size_t>(t) * a.chunks + lane;
+        u32x4 drr[VPT], dhr[VPT], rr[VPT], yr[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; j++) {
+            drr[j] = in[j] && a.dr ? a.dr[base + NT * j] : zero;
+            dhr[j] = in[j] && a.dh ? a.dh[base + NT * j] : zero;
+            rr[j] = in[j] && a.dh ? a.r[base + NT * j] : zero;
+            yr[j] = in[j] && a.y ? a.y[base + NT * j] : zero;
+        }
+        float sums[3] = {0.f, 0.f, 0.f};  // r.r, (dh w_pre).r, y.y
+#pragma unroll
+        for (int j = 0; j < VPT; j++) {
+            float u[N], v[N], w[N];
+            Chunk<E>::unpack(rr[j], u);
+            Chunk<E>::unpack(dhr[j], v);
+            Chunk<E>::unpack(wpre[j], w);
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                sums[0] = fmaf(u[i], u[i], sums[0]);
+                sums[1] = fmaf(v[i] * w[i], u[i], sums[1]);
+            }
+            Chunk<E>::unpack(yr[j], u);
+#pragma unroll
+            for (int i = 0; i < N; i++) sums[2] = fmaf(u[i], u[i], sums[2]);
+        }
+        row_sums<NT>(sums, slots, turn);
+        const float rstd_r = 1.f / sqrtf(fmaf(sums[0], a.inv_d, a.eps));
+        const float back_r = sums[1] * a.inv_d * rstd_r * rstd_r * rstd_r;
+        const float rstd_y = a.w_post ? 1.f / sqrtf(fmaf(sums[2], a.inv_d, a.eps)) : 1.f;
+        const float gt = gate_tok ? gate_tok[t] : 1.f;
+
+        float q[VPT][N];       // scale gate dr' (w_post): the gradient at n(y), or at y
+        float two[2] = {0.f, 0.f};  // q.y, and dz.z for a token gate
+#pragma unroll
+        for (int j = 0; j < VPT; j++) {
+            float u[N], v[N], w[N];
+            Chunk<E>::unpack(drr[j], q[j]);
+            if (a.dh) {
+                Chunk<E>::unpack(rr[j], u);
+                Chunk<E>::unpack(dhr[j], v);
+                Chunk<E>::unpack(wpre[j], w);
+#pragma unroll
+                for (int i = 0; i < N; i++) {
+                    acc_pre[j][i] = fmaf(v[i], u[i] * rstd_r, acc_pre[j][i]);
+                    q[j][i] += rstd_r * (v[i] * w[i]) - u[i] * back_r;
+                }
+            }
+            if (in[j]) a.dx[base + NT * j] = Chunk<E>::pack(q[j]);
+            if (!a.dy) continue;
+            Chunk<E>::unpack(yr[j], u);
+            Chunk<E>::unpack(wpost[j], v);
+            Chunk<E>::unpack(wgate[j], w);
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const float dz = a.scale * q[j][i];
+                const float yn = u[i] * rstd_y;
+                const float wp = a.w_post ? v[i] : 1.f;
+                const float g = gate_ch ? w[i] : gt;
+                acc_gate[j][i] = fmaf(dz, yn * wp, acc_gate[j][i]);
+                acc_post[j][i] = fmaf(dz * g, yn, acc_post[j][i]);
+                two[1] = fmaf(dz, yn * wp, two[1]);
+                q[j][i] = dz * g * wp;
+                two[0] = fmaf(q[j][i], u[i], two[0]);
+            }
+        }
+        if (!a.dy) continue;
+        float back_y = 0.f;
+        if (a.w_post || gate_tok) {
+            row_sums<NT>(two, slots, turn);
+            if (a.w_post) back_y = two[0] * a.inv_d * rstd_y * rstd_y * rstd_y;
+            if (gate_tok && lane == 0) a.dgate_tok[t] = two[1];
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; j++) {
+            float u[N];
+            Chunk<E>::unpack(yr[j], u);
+#pragma unroll
+            for (int i = 0; i < N; i++) q[j][i] = rstd_y * q[j][i] - u[i] * back_y;
+            if (in[j]) a.dy[base + NT * j] = Chunk<E>::pack(q[j]);
+        }
+    }
+
+    // this workgroup's column sums, its waves' rows added in wave order
+    const int d = a.chunks * N;
+    float *out = a.part + static_cast<size_t>(blockIdx.x) * 3 * d;
+    if constexpr (NT > kWave) {
+#pragma unroll
+        for (int j = 0; j < VPT; j++)
+            if (in[j]) {
+                const int c = (lane + NT * j) * N;
+#pragma unroll
+                for (int i = 0; i < N; i++) {
+                    out[c + i] = acc_post[j][i];
+                    out[d + c + i] = acc_gate[j][i];
+                    out[2 * d + c + i] = acc_pre[j][i];
+                }
+            }
+    } else {
+        __shared__ float col[kWaves][NT * VPT * N];
+#pragma unroll
+        for (int k = 0; k < 3; k++) {
+            if (k) __syncthreads();
+            const auto &acc = k == 0 ? acc_post : k == 1 ? acc_gate : acc_pre;
+#pragma unroll
+            for (int j = 0; j < VPT; j++)
+#pragma unroll
+                for (int i = 0; i < N; i++)
+                    col[threadIdx.x / NT][(lane + NT * j) * N + i] = acc[j][i];
+            __syncthreads();
+            for (int c = threadIdx.x; c < d; c += kThreads) {
+                float s = 0.f;
+#pragma unroll
+                for (int q = 0; q < kWaves; q++) s += col[q][c];
+                out[k * d + c] = s;
+            }
+        }
+    }
+}
+
+// out[k][c] = sum over the workgroups' part[b][k][c], b ascending within each
+// of the 16 interleaved shares and the shares in order.
+constexpr int kFoldCols = 64, kFoldShares = 16;
+__global__ __launch_bounds__(kFoldCols *kFoldShares) void k_norm_fold(
+    const float *__restrict__ part, int blocks, int d, float *dw_post, float *dgate, float *dw_pre) {
+    __shared__ float s[kFoldShares][kFoldCols];
+    float *out = blockIdx.y == 0 ? dw_post : blockIdx.y == 1 ? dgate : dw_pre;
+    if (!out) return;
+    const int c = blockIdx.x * kFoldCols + threadIdx.x % kFoldCols, sh = threadIdx.x / kFoldCols;
+    float v = 0.f;
+    if (c < d)
+        for (int b = sh; b < blocks; b += kFoldShares)
+            v += part[(static_cast<size_t>(b) * 3 + blockIdx.y) * d + c];
+    s[sh][threadIdx.x % kFoldCols] = v;
+    __syncthreads();
+    if (sh || c >= d) return;
+    for (int q = 1; q < kFoldShares; q++) v += s[q][threadIdx.x];
+    out[c] = v;
+}
+
+// f(NT, VPT) for the smallest variant that holds a row of `chunks` chunks.
+template <typename F>
+void by_width(int chunks, F f) {
+    using std::integral_constant;
+    if (chunks <= 64)
+        f(integral_constant<int, kWave>{}, integral_constant<int, 1>{});
+    else if (chunks <= 128)
+        f(integral_constant<int, kWave>{}, integral_constant<int, 2>{});
+    else if (chunks <= 256)
+        f(integral_constant<int, kWave>{}, integral_constant<int, 4>{});
+    else if (chunks <= 512)
+        f(integral_constant<int, kThreads>{}, integral_constant<int, 2>{});
+    else
+        f(integral_constant<int, kThreads>{}, integral_constant<int, 4>{});
+}
+
+int rows_per_block(int chunks) { return chunks <= 256 ? kWaves : 1; }
+
+}  // namespace
+
+// Forward: enough workgroups to fill the CUs' waves.  Backward: two per CU,
+// since each leaves 3 d fp32 column sums behind.
+constexpr int kNormBlocks = 2048, kNormBackBlocks = 512;
+
+int norm_back_blocks(int T, int chunks) {
+    const int need = static_cast<int>(ceil_div(T, rows_per_block(chunks)));
+    return need < kNormBackBlocks ? need : kNormBackBlocks;
+}
+
+hipError_t launch_block_norm(const void *x, const void *y, const void *w_post, const void *gate,
+                             const void *w_pre, int T, int d, int bf16, int gate_kind, float eps,
+                             float scale, void *r, void *h, hipStream_t s) {
+    NormArgs a;
+    a.x = static_cast<const u32x4 *>(x);
+    a.y = static_cast<const u32x4 *>(y);
+    a.w_post = static_cast<const u32x4 *>(w_post);
+    a.w_pre = static_cast<const u32x4 *>(w_pre);
+    a.gate = gate;
+    a.r = static_cast<u32x4 *>(r);
+    a.h = static_cast<u32x4 *>(h);
+    a.T = T;
+    a.chunks = d / (bf16 ? 8 : 4);
+    a.gate_kind = gate_kind;
+    a.inv_d = 1.f / static_cast<float>(d);
+    a.eps = eps;
+    a.scale = scale;
+    const unsigned need = ceil_div(T, rows_per_block(a.chunks));
+    const unsigned grid = need < kNormBlocks ? need : kNormBlocks;
+    by_width(a.chunks, [&](auto nt, auto vpt) {
+        if (bf16)
+            k_norm<uint16_t, decltype(nt)::value, decltype(vpt)::value><<<grid, kThreads, 0, s>>>(a);
+        else
+            k_norm<float, decltype(nt)::value, decltype(vpt)::value><<<grid, kThreads, 0, s>>>(a);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_block_norm_back(const void *dr, const void *dh, const void *r, const void *y,
+                                  const void *w_post, const void *gate, const void *w_pre, int T,
+                                  int d, int bf16, int gate_kind, float eps, float scale, void *dx,
+                                  void *dy, float *dw_post, float *dgate, float *dw_pre,
+                                  float *part, hipStream_t s) {
+    NormBackArgs a;
+    a.dr = static_cast<const u32x4 *>(dr);
+    a.dh = static_cast<const u32x4 *>(dh);
+    a.r = static_cast<const u32x4 *>(r);
+    // y matters to its norm's and its gate's gradients only
+    a.y = w_post || gate ? static_cast<const u32x4 *>(y) : nullptr;
+    a.w_post = static_cast<const u32x4 *>(w_post);
+    a.w_pre = static_cast<const u32x4 *>(w_pre);
+    a.gate = gate;
+    a.dx = static_cast<u32x4 *>(dx);
+    a.dy = static_cast<u32x4 *>(dy);
+    a.dgate_tok = gate_kind == 2 ? dgate : nullptr;
+    a.part = part;
+    a.T = T;
+    a.chunks = d / (bf16 ? 8 : 4);
+    a.gate_kind = gate_kind;
+    a.inv_d = 1.f / static_cast<float>(d);
+    a.eps = eps;
+    a.scale = scale;
+    const int grid = norm_back_blocks(T, a.chunks);
+    by_width(a.chunks, [&](auto nt, auto vpt) {
+        if (bf16)
+            k_norm_back<uint16_t, decltype(nt)::value, decltype(vpt)::value>
+                <<<grid, kThreads, 0, s>>>(a);
+        else
+            k_norm_back<float, decltype(nt)::value, decltype(vpt)::value>
+                <<<grid, kThreads, 0, s>>>(a);
+    });
+    float *dgate_ch = gate_kind == 1 ? dgate : nullptr;
+    if (dw_post || dgate_ch || dw_pre)
+        k_norm_fold<<<dim3(ceil_div(d, kFoldCols), 3), kFoldCols * kFoldShares, 0, s>>>(
+            part, grid, d, dw_post, dgate_ch, dw_pre);
+    return hipGetLastError();
+}
+
+}  // namespace occ

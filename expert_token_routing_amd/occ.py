@@ -26,6 +26,9 @@ OCC_PRUNE_OFF, OCC_PRUNE_TRAVERSE, OCC_PRUNE_GROUPSUM, OCC_PRUNE_SIMILARITY = 0,
 OCC_FLAG_TRAIN = 1
 OCC_FLAG_DETERMINISTIC = 2
 OCC_NOALLOC_SCRATCH_BYTES = 128 << 20
+OCC_GATE_NONE, OCC_GATE_CHANNEL, OCC_GATE_TOKEN = 0, 1, 2
+OCC_ADAMW_32BIT, OCC_ADAMW_8BIT = 0, 1
+OCC_ADAMW_BLOCK = 256
 BSTAGES = ["dispatch", "dgrad_down", "dgrad_up", "shared", "combine", "wgrad_down", "wgrad_up",
            "route"]
 OCC_BSTAGE_COUNT = len(BSTAGES)
@@ -38,7 +41,9 @@ EXPORTED = ["occ_status_string", "occ_workspace_size", "occ_route",
             "occ_build_brim", "occ_moe_forward", "occ_moe_forward_routed", "occ_gate",
             "occ_moe_forward_gated", "occ_moe_backward", "occ_forward_views",
             "occ_coactivation_stats", "occ_place_experts", "occ_events_create",
-            "occ_events_destroy", "occ_event_elapsed_ms", "occ_moe_forward_noalloc"]
+            "occ_events_destroy", "occ_event_elapsed_ms", "occ_moe_forward_noalloc",
+            "occ_block_workspace_size", "occ_block_norm", "occ_block_norm_backward",
+            "occ_balance_loss", "occ_balance_backward", "occ_gate_backward", "occ_adamw_step"]
 
 
 class OccError(RuntimeError):
@@ -67,6 +72,28 @@ class ForwardView(ctypes.Structure):
                 ("x_sfd", ctypes.c_void_p), ("epd", ctypes.c_void_p),
                 ("sfd_out", ctypes.c_void_p), ("h_shared", ctypes.c_void_p),
                 ("y_shared", ctypes.c_void_p)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("scale", ctypes.c_float), ("gate", ctypes.c_int32)]
+
+
+class BalanceDesc(ctypes.Structure):
+    _fields_ = [("balance", ctypes.c_float), ("group", ctypes.c_float), ("z", ctypes.c_float)]
+
+
+class AdamwDesc(ctypes.Structure):
+    _fields_ = ([("state", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)] +
+                [(n, ctypes.c_double) for n in
+                 ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] +
+                [("step", ctypes.c_int64)])
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = ([("n", ctypes.c_int64)] +
+                [(n, ctypes.c_void_p) for n in
+                 ("p", "g", "m", "v", "m_scale", "v_scale", "p_out", "m_out", "v_out",
+                  "m_scale_out", "v_scale_out", "p_bf16")])
 
 
 _lib = None
@@ -103,6 +130,16 @@ def lib() -> ctypes.CDLL:
             "occ_forward_views": ([dp, vp, ctypes.POINTER(ForwardView)], ctypes.c_int),
             "occ_coactivation_stats": ([dp, vp, vp, vp, vp, vp, vp, vp, vp], ctypes.c_int),
             "occ_place_experts": ([vp, i32, i32, vp], ctypes.c_int),
+            "occ_block_workspace_size": ([dp, ctypes.POINTER(sz)], ctypes.c_int),
+            "occ_block_norm": ([dp, ctypes.POINTER(NormDesc)] + [vp] * 8, ctypes.c_int),
+            "occ_block_norm_backward": ([dp, ctypes.POINTER(NormDesc)] + [vp] * 13 + [sz, vp],
+                                        ctypes.c_int),
+            "occ_balance_loss": ([dp, ctypes.POINTER(BalanceDesc)] + [vp] * 8 + [sz, vp],
+                                 ctypes.c_int),
+            "occ_balance_backward": ([dp, ctypes.POINTER(BalanceDesc)] + [vp] * 4 +
+                                     [ctypes.c_float, vp, vp, vp], ctypes.c_int),
+            "occ_gate_backward": ([dp] + [vp] * 7 + [sz, vp], ctypes.c_int),
+            "occ_adamw_step": ([ctypes.POINTER(AdamwDesc), vp, i32, vp, vp], ctypes.c_int),
             "occ_events_create": ([i32, vp], ctypes.c_int),
             "occ_events_destroy": ([i32, vp], ctypes.c_int),
             "occ_event_elapsed_ms": ([vp, vp, ctypes.POINTER(ctypes.c_float)], ctypes.c_int),
@@ -353,6 +390,187 @@ def occ_moe_backward(desc: LayerDesc, dy, x, logits, placement, w_gate, w_up, w_
         _dev(dlogits, "dlogits", f32, (T, Ne)), _dev(workspace, "workspace", torch.uint8),
         workspace.numel(), ctypes.cast(ev, ctypes.c_void_p) if ev is not None else None,
         _stream(stream)), "occ_moe_backward")
+
+
+# ---- around the layer in a training step ----
+
+_TORCH = {OCC_F32: torch.float32, OCC_BF16: torch.bfloat16}
+
+
+def _queue(what: str, fn, args, tensors, stream):
+    """Calls fn(*args, stream) with the tensors' device as the current one; all of them (None
+    among them) must share it, and so must the stream."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{what}: tensors on {device} and on {t.device}")
+    if stream is not None and device is not None and stream.device != device:
+        raise ValueError(f"{what}: tensors on {device}, stream on {stream.device}")
+    if device is None or device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), what)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)), what)
+
+
+def occ_block_workspace_size(desc: LayerDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().occ_block_workspace_size(ctypes.byref(desc), ctypes.byref(n)),
+           "occ_block_workspace_size")
+    return n.value
+
+
+def alloc_block_workspace(desc: LayerDesc, device="cuda") -> torch.Tensor:
+    """A device byte tensor of occ_block_workspace_size bytes."""
+    return torch.empty(occ_block_workspace_size(desc), dtype=torch.uint8, device=device)
+
+
+def _ws(workspace):
+    if workspace is None:
+        return None, 0
+    return _dev(workspace, "workspace", torch.uint8), workspace.numel()
+
+
+def _norm_gate(desc: LayerDesc, opt: NormDesc, gate):
+    if opt.gate == OCC_GATE_TOKEN:
+        return _dev(gate, "gate", torch.float32, (desc.T,))
+    return _dev(gate, "gate", _TORCH.get(desc.dtype), (desc.d,))
+
+
+def occ_block_norm(desc: LayerDesc, opt: NormDesc, x, y, w_post, gate, w_pre, r, h, stream=None):
+    """r = x + scale gate w_post n(y), h = w_pre n(r); y, w_post, gate and w_pre with h may be
+    None (see occ.h)."""
+    dt, rows, d = _TORCH.get(desc.dtype), (desc.T, desc.d), (desc.d,)
+    args = (ctypes.byref(desc), ctypes.byref(opt), _dev(x, "x", dt, rows), _dev(y, "y", dt, rows),
+            _dev(w_post, "w_post", dt, d), _norm_gate(desc, opt, gate),
+            _dev(w_pre, "w_pre", dt, d), _dev(r, "r", dt, rows), _dev(h, "h", dt, rows))
+    _queue("occ_block_norm", lib().occ_block_norm, args, (x, y, w_post, gate, w_pre, r, h), stream)
+
+
+def occ_block_norm_backward(desc: LayerDesc, opt: NormDesc, dr, dh, r, y, w_post, gate, w_pre, dx,
+                            dy, dw_post, dgate, dw_pre, workspace, stream=None):
+    """Gradients of occ_block_norm from dr and dh (r: its r, or its x without y)."""
+    dt, rows, d, f32 = _TORCH.get(desc.dtype), (desc.T, desc.d), (desc.d,), torch.float32
+    gate_shape = (desc.T,) if opt.gate == OCC_GATE_TOKEN else d
+    args = (ctypes.byref(desc), ctypes.byref(opt), _dev(dr, "dr", dt, rows),
+            _dev(dh, "dh", dt, rows), _dev(r, "r", dt, rows), _dev(y, "y", dt, rows),
+            _dev(w_post, "w_post", dt, d), _norm_gate(desc, opt, gate),
+            _dev(w_pre, "w_pre", dt, d), _dev(dx, "dx", dt, rows), _dev(dy, "dy", dt, rows),
+            _dev(dw_post, "dw_post", f32, d), _dev(dgate, "dgate", f32, gate_shape),
+            _dev(dw_pre, "dw_pre", f32, d), *_ws(workspace))
+    _queue("occ_block_norm_backward", lib().occ_block_norm_backward, args,
+           (dr, dh, r, y, w_post, gate, w_pre, dx, dy, dw_post, dgate, dw_pre, workspace), stream)
+
+
+def _valid(valid, T):
+    if valid is not None and valid.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"valid must be torch.bool or torch.uint8, got {valid.dtype}")
+    return _dev(valid, "valid", None, (T,))
+
+
+def _placement(desc: LayerDesc, placement):
+    """The placement as host int32 (kept by the caller during the call), or None."""
+    if placement is None:
+        return None
+    return _host_i32(placement, "placement", (desc.Nd, desc.Ne // max(desc.Nd, 1)))
+
+
+def occ_balance_loss(desc: LayerDesc, opt: BalanceDesc, logits, ids, valid, placement, counts,
+                     probs, loss, workspace, stream=None):
+    """Router losses [sum, balance, group, z], mean probabilities, and the counts (Ne, then the
+    valid tokens)."""
+    T, Ne, k, f32 = desc.T, desc.Ne, desc.k, torch.float32
+    L = _placement(desc, placement)
+    args = (ctypes.byref(desc), ctypes.byref(opt), _dev(logits, "logits", f32, (T, Ne)),
+            _dev(ids, "ids", torch.int32, (T, k)), _valid(valid, T),
+            None if L is None else _hp(L), _dev(counts, "counts", torch.int32, (Ne + 1,)),
+            _dev(probs, "probs", f32, (Ne,)), _dev(loss, "loss", f32, (4,)), *_ws(workspace))
+    _queue("occ_balance_loss", lib().occ_balance_loss, args,
+           (logits, ids, valid, counts, probs, loss, workspace), stream)
+
+
+def occ_balance_backward(desc: LayerDesc, opt: BalanceDesc, logits, valid, placement, counts,
+                         dloss: float, dlogits_in, dlogits, stream=None):
+    """dlogits = dlogits_in + dloss times the losses' gradient in the logits."""
+    T, Ne, f32 = desc.T, desc.Ne, torch.float32
+    L = _placement(desc, placement)
+    args = (ctypes.byref(desc), ctypes.byref(opt), _dev(logits, "logits", f32, (T, Ne)),
+            _valid(valid, T), None if L is None else _hp(L),
+            _dev(counts, "counts", torch.int32, (Ne + 1,)), dloss,
+            _dev(dlogits_in, "dlogits_in", f32, (T, Ne)), _dev(dlogits, "dlogits", f32, (T, Ne)))
+    _queue("occ_balance_backward", lib().occ_balance_backward, args,
+           (logits, valid, counts, dlogits_in, dlogits), stream)
+
+
+def occ_gate_backward(desc: LayerDesc, dlogits, x, w_router, dx_in, dx, dw_router, workspace,
+                      stream=None):
+    """dx = dx_in + dlogits w_router, dw_router = dlogits^T x; dx or dw_router may be None."""
+    T, d, Ne, dt, f32 = desc.T, desc.d, desc.Ne, _TORCH.get(desc.dtype), torch.float32
+    args = (ctypes.byref(desc), _dev(dlogits, "dlogits", f32, (T, Ne)), _dev(x, "x", dt, (T, d)),
+            _dev(w_router, "w_router", dt, (Ne, d)), _dev(dx_in, "dx_in", dt, (T, d)),
+            _dev(dx, "dx", dt, (T, d)), _dev(dw_router, "dw_router", f32, (Ne, d)),
+            *_ws(workspace))
+    _queue("occ_gate_backward", lib().occ_gate_backward, args,
+           (dlogits, x, w_router, dx_in, dx, dw_router, workspace), stream)
+
+
+class AdamwTensors:
+    """The tensors of an optimizer, laid out once for occ_adamw_step (which holds no state of
+    its own): a list of dicts of device tensors
+
+      p (fp32), g (opt.grad_dtype), m, v (fp32, or torch.float8_e4m3fn with 8-bit states and
+      then m_scale, v_scale: one fp32 per OCC_ADAMW_BLOCK elements), and optionally p_bf16, the
+      bf16 copy to write, and p_out, m_out, v_out, m_scale_out, v_scale_out (in place otherwise).
+
+    The table keeps the tensors alive."""
+
+    def __init__(self, opt: AdamwDesc, tensors: list[dict]):
+        self.state, self.grad_dtype = opt.state, opt.grad_dtype
+        self.tensors = [dict(t) for t in tensors]
+        self.table = (AdamwTensor * max(len(self.tensors), 1))()
+        self.devices = []  # one tensor for each device among them
+        eight, f32 = opt.state == OCC_ADAMW_8BIT, torch.float32
+        state = torch.float8_e4m3fn if eight else f32
+        names = {n for n, _ in AdamwTensor._fields_[1:]}
+        for i, (t, row) in enumerate(zip(self.tensors, self.table)):
+            if set(t) - names:
+                raise ValueError(f"tensor {i}: unknown entries {sorted(set(t) - names)}")
+            shape = tuple(t["p"].shape)
+            row.n = t["p"].numel()
+            units = (-(-row.n // OCC_ADAMW_BLOCK),) if eight else None
+            for name, dtype in (("p", f32), ("g", _TORCH.get(opt.grad_dtype)), ("m", state),
+                                ("v", state), ("m_scale", f32), ("v_scale", f32)):
+                a, scale = t.get(name), name.endswith("_scale")
+                if (a is None) != (scale and not eight):
+                    raise ValueError(f"tensor {i}: {name} must be "
+                                     f"{'None' if a is not None else 'given'}")
+                want = units if scale else shape
+                address = _dev(a, f"tensor {i}: {name}", dtype, want)
+                setattr(row, name, address)
+                if name != "g":
+                    out = t.get(name + "_out")
+                    if out is not None and a is None:
+                        raise ValueError(f"tensor {i}: {name}_out must be None")
+                    setattr(row, name + "_out", address if out is None else
+                            _dev(out, f"tensor {i}: {name}_out", dtype, want))
+            row.p_bf16 = _dev(t.get("p_bf16"), f"tensor {i}: p_bf16", torch.bfloat16, shape)
+            for a in t.values():
+                if a is not None and all(a.device != b.device for b in self.devices):
+                    self.devices.append(a)
+
+
+def occ_adamw_step(opt: AdamwDesc, tensors: AdamwTensors, dynamic=None, stream=None):
+    """One AdamW step over the tensors; dynamic: None or a device fp32 tensor
+    [lr, step, grad_scale] that replaces the descriptor's."""
+    if (opt.state, opt.grad_dtype) != (tensors.state, tensors.grad_dtype):
+        raise ValueError("the descriptor's state and grad_dtype differ from the table's")
+    args = (ctypes.byref(opt), tensors.table, len(tensors.tensors),
+            _dev(dynamic, "dynamic", torch.float32, (3,)))
+    _queue("occ_adamw_step", lib().occ_adamw_step, args, (*tensors.devices, dynamic), stream)
 
 
 def occ_forward_views(desc: LayerDesc, workspace) -> ForwardView:

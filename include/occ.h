@@ -197,7 +197,8 @@ enum {
 const char *occ_status_string(occ_status status);
 
 /* Bytes of device workspace occ_moe_forward needs for this shape (enough for
- * every other call too).  It is sized for the worst case N_sfd = T*min(k, Nd),
+ * every other call of the layer too; the operators around it have
+ * occ_block_workspace_size).  It is sized for the worst case N_sfd = T*min(k, Nd),
  * so no call ever has to read a data-dependent size back to the host.
  * Errors: INVALID_ARG / UNSUPPORTED as for the other calls. */
 occ_status occ_workspace_size(const occ_layer_desc *desc, size_t *bytes_host);
@@ -409,6 +410,204 @@ occ_status occ_moe_backward(const occ_layer_desc *desc, const void *dy, const vo
                             float *dws_gate, float *dws_up, float *dws_down, float *dw,
                             float *dlogits, void *workspace, size_t ws_bytes,
                             void *const *stage_events, void *stream);
+
+/* ---- around the layer in a training step ----
+ *
+ * The operators below take the layer's descriptor, of which each uses the
+ * fields it names; the pointer, stream and error rules are the same.  Row
+ * tensors (T x d) and weights handed to them must be 16-byte aligned, other
+ * arrays aligned to their elements (INVALID_ARG otherwise).  An output may be
+ * the very same array as an input of the same type and shape; otherwise
+ * outputs overlap nothing.  All of them are deterministic: no atomic
+ * additions of floating-point values, sums in an order fixed by the sizes. */
+
+/* Bytes of device workspace that occ_block_norm_backward, occ_balance_loss
+ * and occ_gate_backward need for this shape (enough for each of them).  It is
+ * scratch: nothing is kept in it between calls, but calls that may overlap
+ * need one each, and it must not be the layer's own training workspace
+ * between a forward and its backward. */
+occ_status occ_block_workspace_size(const occ_layer_desc *desc, size_t *bytes_host);
+
+/* A gate on the block's output in occ_block_norm: none (1), one learned value
+ * per channel (d values of the descriptor's dtype), or one per token (T fp32
+ * values, as the routing weights are). */
+typedef enum occ_block_gate {
+    OCC_GATE_NONE = 0,
+    OCC_GATE_CHANNEL = 1,
+    OCC_GATE_TOKEN = 2
+} occ_block_gate;
+
+typedef struct occ_norm_desc {
+    float eps;    /* > 0, added to the mean square */
+    float scale;  /* residual scale of the block's output */
+    int32_t gate; /* occ_block_gate */
+} occ_norm_desc;
+
+/* The boundary between two blocks of a transformer, in one pass: the norm
+ * behind a block, its gate and residual scale, the addition to the residual
+ * stream, and the norm in front of the next block.  With
+ * n(v) = v / sqrt(mean(v^2) + eps) over a row's d values:
+ *   r = x + scale * gate * z,   z = w_post * n(y)  (z = y when w_post is NULL)
+ *   h = w_pre * n(r)
+ * Uses T, d and dtype.  Arithmetic is fp32; r and h are each rounded once (h
+ * is computed from r before its rounding).
+ *   x          T x d (dtype): the residual stream.
+ *   y          T x d (dtype): the block's output, or NULL: then r is x and is
+ *              not written, w_post, gate and r must be NULL, opt->gate NONE
+ *              (the norm in front of the first block).
+ *   w_post     d (dtype), or NULL: no norm behind the block.
+ *   gate       see occ_block_gate; NULL exactly for OCC_GATE_NONE.
+ *   w_pre      d (dtype), or NULL together with h (behind the last block).
+ *   r (out)    T x d (dtype), needed with y.
+ *   h (out)    T x d (dtype).
+ * Errors: INVALID_ARG for a missing or superfluous pointer, eps <= 0, a scale
+ * or eps that is not finite. */
+occ_status occ_block_norm(const occ_layer_desc *desc, const occ_norm_desc *opt, const void *x,
+                          const void *y, const void *w_post, const void *gate, const void *w_pre,
+                          void *r, void *h, void *stream);
+
+/* Its backward pass, from the gradients dr of r and dh of h:
+ *   dr' = dr + the gradient of dh through w_pre * n(r)
+ *   dx = dr',   dz = scale * dr',   dgate = sum of dz * z (over tokens for
+ *   CHANNEL, over channels for TOKEN),   dy = the gradient of gate * dz
+ *   through w_post * n(y),   dw_post = sum over tokens of gate * dz * n(y),
+ *   dw_pre = sum over tokens of dh * n(r).
+ * The rows' statistics are computed again from r and y.
+ *   dr         T x d (dtype), or NULL for zero (then dh is needed).
+ *   dh         T x d (dtype); NULL exactly when w_pre is NULL.
+ *   r          T x d (dtype): the forward's r (its x when y was NULL).  May be
+ *              NULL without w_pre.
+ *   y          T x d (dtype): the forward's y.  NULL when the forward had
+ *              none; may be NULL without w_post and gate (it is not read).
+ *   w_post, gate, w_pre   as in the forward.
+ *   dx (out)   T x d (dtype).
+ *   dy (out)   T x d (dtype); NULL exactly when the forward had no y.
+ *   dw_post, dw_pre (out)  d fp32;  dgate (out) d or T fp32: NULL exactly
+ *              where the weight or the gate is.
+ *   workspace  256-byte aligned, ws_bytes >= occ_block_workspace_size. */
+occ_status occ_block_norm_backward(const occ_layer_desc *desc, const occ_norm_desc *opt,
+                                   const void *dr, const void *dh, const void *r, const void *y,
+                                   const void *w_post, const void *gate, const void *w_pre,
+                                   void *dx, void *dy, float *dw_post, float *dgate,
+                                   float *dw_pre, void *workspace, size_t ws_bytes,
+                                   void *stream);
+
+/* Coefficients of the router's losses (finite; 0 leaves a term out). */
+typedef struct occ_balance_desc {
+    float balance; /* load balance over experts */
+    float group;   /* load balance over the placement's expert groups */
+    float z;       /* square of the logits' log-sum-exp */
+} occ_balance_desc;
+
+/* Losses that keep the router's load even, with the per-expert counts.  Over
+ * the n valid tokens, with p the full softmax of Eq. 2:
+ *   counts[e] = slots routed to e,  f_e = Ne counts[e] / (k n),  P_e = mean p_e
+ *   balance * sum_e f_e P_e                (1 times the coefficient when even)
+ *   group * sum_g F_g Q_g,   F_g = mean of f_e over the group's experts,
+ *                            Q_g = sum of P_e over them
+ *   z * mean of logsumexp(logits)^2
+ * Uses T, Ne, k and Nd.
+ *   logits     T x Ne fp32.  -inf leaves an expert out of the softmax; a row
+ *              of -inf alone counts with p = 0 and a log-sum-exp of 0.
+ *   ids        T x k int32, as written by occ_route (an id outside 0..Ne-1 is
+ *              not counted).
+ *   valid      T bytes, 0 for padding, or NULL: every token counts.  What
+ *              logits and ids hold in padding rows is not used.
+ *   placement_host  as for occ_route; may be NULL when opt->group is 0.
+ *   counts (out)    Ne + 1 int32: the experts' counts, then n.
+ *   probs (out)     Ne fp32: P (0 when n = 0).
+ *   loss (out)      4 fp32: the sum, then the three terms (0 when n = 0).
+ *   workspace       as for occ_block_norm_backward. */
+occ_status occ_balance_loss(const occ_layer_desc *desc, const occ_balance_desc *opt,
+                            const float *logits, const int32_t *ids, const uint8_t *valid,
+                            const int32_t *placement_host, int32_t *counts, float *probs,
+                            float *loss, void *workspace, size_t ws_bytes, void *stream);
+
+/* The gradient of those losses in the logits, the counts held fixed, added to
+ * what the layer's backward pass left there:
+ *   dlogits = dlogits_in + dloss / n * p (c - sum_j c_j p_j + 2 z logsumexp),
+ *   c_e = balance f_e + group F_(group of e)
+ * and dlogits = dlogits_in in padding rows.
+ *   counts      as written by occ_balance_loss on the same ids and valid.
+ *   dloss       gradient of the whole loss in this one (finite).
+ *   dlogits_in  T x Ne fp32, or NULL for zero.
+ *   dlogits (out)  T x Ne fp32. */
+occ_status occ_balance_backward(const occ_layer_desc *desc, const occ_balance_desc *opt,
+                                const float *logits, const uint8_t *valid,
+                                const int32_t *placement_host, const int32_t *counts, float dloss,
+                                const float *dlogits_in, float *dlogits, void *stream);
+
+/* Backward pass of occ_gate:
+ *   dx = dx_in + dlogits w_router,   dw_router = dlogits^T x
+ * Uses T, d, Ne and dtype; sums are fp32.  With bf16 tensors the fp32 dlogits
+ * enter the matrix cores as a sum of bf16 terms: two for dx (16 bits, below
+ * the rounding of dx), three for dw_router (all 24 bits); a dlogits value
+ * that is not finite gives NaN where it contributes.
+ *   dlogits    T x Ne fp32.
+ *   x          T x d (dtype); may be NULL without dw_router.
+ *   w_router   Ne x d (dtype); may be NULL without dx.
+ *   dx_in      T x d (dtype): what else flows into x (occ_moe_backward's dx),
+ *              or NULL for zero.
+ *   dx (out)   T x d (dtype), or NULL: not computed (then dx_in is NULL).
+ *   dw_router (out)  Ne x d fp32 (16-byte aligned), or NULL: not computed.
+ *   workspace  as for occ_block_norm_backward; may be NULL without dw_router.
+ * Errors: INVALID_ARG also when neither output is asked for. */
+occ_status occ_gate_backward(const occ_layer_desc *desc, const float *dlogits, const void *x,
+                             const void *w_router, const void *dx_in, void *dx, float *dw_router,
+                             void *workspace, size_t ws_bytes, void *stream);
+
+/* How AdamW's moments are held: fp32, or 8 bits with an fp32 unit per block
+ * of OCC_ADAMW_BLOCK consecutive elements.  In 8 bits m and the square root
+ * of v are OCP e4m3 codes; an element stands for code * unit, and the unit is
+ * the block's largest magnitude / 448 (the square root halves v's range of
+ * exponents).  A v > 0 never rounds to 0 (its code is at least 2^-9), so
+ * that a small v cannot leave m / eps; a block whose largest magnitude is
+ * below 2^-100 is held as zeros.  Codes and units of zero start a run. */
+#define OCC_ADAMW_BLOCK 256
+typedef enum occ_adamw_state { OCC_ADAMW_32BIT = 0, OCC_ADAMW_8BIT = 1 } occ_adamw_state;
+
+typedef struct occ_adamw_desc {
+    int32_t state;       /* occ_adamw_state */
+    int32_t grad_dtype;  /* occ_dtype of the gradients */
+    double lr;           /* >= 0 */
+    double beta1, beta2; /* in [0, 1) */
+    double eps;          /* > 0 */
+    double weight_decay; /* >= 0, decoupled */
+    double grad_scale;   /* gradients are multiplied by it (1 / loss scale, a clip factor) */
+    int64_t step;        /* 1 for the first step */
+} occ_adamw_desc;
+
+/* One tensor of n elements (0: skipped).  Every *_out may be the array that
+ * it is the new value of (the usual step in place) or another one; m_scale
+ * and v_scale (ceil(n / OCC_ADAMW_BLOCK) fp32) only with 8-bit states, NULL
+ * otherwise.  p is fp32; p_bf16 is NULL or receives the new p rounded to
+ * bf16, the copy that the layer computes with. */
+typedef struct occ_adamw_tensor {
+    int64_t n;
+    const float *p;
+    const void *g;
+    const void *m, *v;
+    const float *m_scale, *v_scale;
+    float *p_out;
+    void *m_out, *v_out;
+    float *m_scale_out, *v_scale_out;
+    void *p_bf16;
+} occ_adamw_tensor;
+
+/* One AdamW step over `count` tensors (read by the time the call returns):
+ *   g' = grad_scale g;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   p = (1 - lr weight_decay) p - lr m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, from the moments before they are rounded to 8 bits.
+ *   dynamic    NULL, or 3 fp32 in device memory that replace lr, step and
+ *              grad_scale: for a captured graph, whose replays then take new
+ *              values.  They are not checked.
+ * A gradient that is not finite makes its element's p, m and v so (with 8-bit
+ * states its whole block's); tensors aligned to 16 bytes are faster.
+ * Errors: INVALID_ARG (a value out of the ranges above, a missing or
+ * superfluous pointer, an array not aligned to its elements), UNSUPPORTED
+ * (n > 2^35). */
+occ_status occ_adamw_step(const occ_adamw_desc *opt, const occ_adamw_tensor *tensors_host,
+                          int32_t count, const float *dynamic, void *stream);
 
 /* Device addresses of the intermediates occ_moe_forward leaves in a
  * workspace (pure host arithmetic, nothing queued). */
