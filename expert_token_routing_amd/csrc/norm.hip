@@ -10,21 +10,34 @@
 //
 // Memory bound: the forward reads x and y and writes r and h once, the
 // backward reads dr, dh, r and y and writes dx and dy once.  A row stays in
-// registers as 16-byte chunks from its loads to its stores (chunk c of a row
-// with the thread c mod NT, so that a wave's loads are contiguous): one wave
-// per row up to 256 chunks (d = 2048 in bf16) with DPP sums and no barrier,
-// a workgroup of 256 threads per row above.  Workgroups walk the rows with a
-// fixed stride and keep the weights in registers.  In the backward each
-// thread also keeps fp32 sums of its columns' weight gradients over its rows;
-// they go to the workspace once per workgroup and a second kernel adds the
-// workgroups' sums in order, so results do not depend on timing.
+// registers as 16-byte chunks from its loads to its stores, and a team of
+// threads shares it (chunk c with thread c mod NT, so that a wave's loads are
+// contiguous).  Teams are as wide as leaves each thread one or two chunks:
+// short dependent chains and few registers, so that many rows are in flight;
+// a team of several waves adds its sums through LDS.  At d = 2048 in bf16
+// (256 chunks), T = 65536 forward: 184 us with 128 threads a row, 190 with
+// 256, 200 with 64 (one wave, no barrier).
+// The forward gives each row to a team of its own.  In the backward each
+// thread also keeps fp32 sums of its columns' weight gradients, so its teams
+// walk over rows with a fixed stride, the next row's loads issued before this
+// one's sums (46 us at T = 8192, d = 2048, 50 without); a workgroup's sums go
+// to the workspace once and a second kernel adds the workgroups' in order, so
+// results do not depend on timing.
+// Measured at d = 2048 bf16, all parts present: forward T = 65536 184 us
+// (5.8 TB/s of the bytes it cannot do without), backward T = 8192 46 + 5 us
+// (4.0 TB/s), one token 2.6 us.
+// Stores past the caches measure 3% faster alone and slower by 2 to 5% with
+// the kernel that reads their rows, so they are ordinary.
+#include <algorithm>
+
 #include "launch.h"
 
 namespace occ {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
+// NT threads share a row, in workgroups of at least 256 threads.
+template <int NT>
+constexpr int kBlock = NT > 256 ? NT : 256;
 
 // A chunk is 16 bytes of a row: E values.
 template <typename E>
@@ -63,15 +76,18 @@ struct Chunk<float> {
     }
 };
 
-// Sum over the NT threads that share a row.  NT = kThreads: through LDS, with
-// two sets of slots used in turn (the next sum's writes cannot meet this
-// one's reads, since the barrier in between orders them).
+// Sums over the NT threads that share a row.  Rows of several waves go
+// through LDS, with two sets of slots used in turn (the next sum's writes
+// cannot meet this one's reads, since the barrier in between orders them).
+constexpr int kMaxWaves = 8;
+typedef float Slots[2][3][kMaxWaves];
 template <int NT, int M>
-__device__ __forceinline__ void row_sums(float (&v)[M], float (&slots)[2][3][kWaves], int &turn) {
+__device__ __forceinline__ void row_sums(float (&v)[M], Slots &slots, int &turn) {
+    constexpr int kRowWaves = NT / kWave;
 #pragma unroll
     for (int i = 0; i < M; i++) v[i] = wave_sum(v[i]);
-    if constexpr (NT > kWave) {
-        const int w = threadIdx.x / kWave;
+    if constexpr (kRowWaves > 1) {
+        const int w = threadIdx.x / kWave, w0 = threadIdx.x / NT * kRowWaves;
         if (lane_id() == 0) {
 #pragma unroll
             for (int i = 0; i < M; i++) slots[turn][i][w] = v[i];
@@ -81,7 +97,7 @@ __device__ __forceinline__ void row_sums(float (&v)[M], float (&slots)[2][3][kWa
         for (int i = 0; i < M; i++) {
             v[i] = 0.f;
 #pragma unroll
-            for (int q = 0; q < kWaves; q++) v[i] += slots[turn][i][q];
+            for (int q = 0; q < kRowWaves; q++) v[i] += slots[turn][i][w0 + q];
         }
         turn ^= 1;
     }
@@ -91,18 +107,19 @@ struct NormArgs {
     const u32x4 *x, *y, *w_post, *w_pre;
     const void *gate;
     u32x4 *r, *h;
-    int T, chunks;  // rows, 16-byte chunks of a row
+    unsigned T;     // rows
+    int chunks;     // 16-byte chunks of a row
     int gate_kind;  // occ_block_gate
     float inv_d, eps, scale;
 };
 
 template <typename E, int NT, int VPT>
-__global__ __launch_bounds__(kThreads) void k_norm(NormArgs a) {
+__global__ __launch_bounds__(kBlock<NT>) void k_norm(NormArgs a) {
     constexpr int N = Chunk<E>::N;
-    __shared__ float slots[2][3][kWaves];
+    __shared__ Slots slots;
     int turn = 0;
-    const int lane = threadIdx.x % NT, rows = kThreads / NT;
-    const int row0 = blockIdx.x * rows + threadIdx.x / NT;
+    constexpr int kRows = kBlock<NT> / NT;
+    const int lane = threadIdx.x % NT, sub = threadIdx.x / NT;
     bool in[VPT];
     u32x4 wpost[VPT], wpre[VPT], wgate[VPT];
     const u32x4 zero = {0, 0, 0, 0};
@@ -116,16 +133,19 @@ __global__ __launch_bounds__(kThreads) void k_norm(NormArgs a) {
         wpre[j] = in[j] && a.w_pre ? a.w_pre[c] : zero;
         wgate[j] = in[j] && gate_ch ? gate_ch[c] : zero;
     }
-    for (int t = row0; t < a.T; t += gridDim.x * rows) {
+    // the trip count is the workgroup's: its rows' sums may need barriers
+    for (unsigned t0 = blockIdx.x * kRows; t0 < a.T; t0 += gridDim.x * kRows) {
+        const unsigned t = t0 + sub;
+        const bool live = t < a.T;
         const size_t base = static_cast<size_t>(t) * a.chunks + lane;
         u32x4 xr[VPT], yr[VPT];
 #pragma unroll
         for (int j = 0; j < VPT; j++) {
-            xr[j] = in[j] ? a.x[base + NT * j] : zero;
-            yr[j] = in[j] && a.y ? a.y[base + NT * j] : zero;
+            xr[j] = live && in[j] ? a.x[base + NT * j] : zero;
+            yr[j] = live && in[j] && a.y ? a.y[base + NT * j] : zero;
         }
         float s = a.scale;
-        if (gate_tok) s *= gate_tok[t];
+        if (gate_tok && live) s *= gate_tok[t];
         if (a.w_post) {
             float ssq[1] = {0.f};
 #pragma unroll
@@ -158,7 +178,7 @@ __global__ __launch_bounds__(kThreads) void k_norm(NormArgs a) {
                 }
 #pragma unroll
                 for (int i = 0; i < N; i++) r[j][i] = fmaf(s, z[i], r[j][i]);
-                if (in[j]) a.r[base + NT * j] = Chunk<E>::pack(r[j]);
+                if (live && in[j]) a.r[base + NT * j] = Chunk<E>::pack(r[j]);
             }
 #pragma unroll
             for (int i = 0; i < N; i++) ssq[0] = fmaf(r[j][i], r[j][i], ssq[0]);
@@ -172,7 +192,7 @@ __global__ __launch_bounds__(kThreads) void k_norm(NormArgs a) {
             Chunk<E>::unpack(wpre[j], w);
 #pragma unroll
             for (int i = 0; i < N; i++) w[i] *= r[j][i] * rstd;
-            if (in[j]) a.h[base + NT * j] = Chunk<E>::pack(w);
+            if (live && in[j]) a.h[base + NT * j] = Chunk<E>::pack(w);
         }
     }
 }
@@ -183,17 +203,19 @@ struct NormBackArgs {
     u32x4 *dx, *dy;
     float *dgate_tok;  // T values (gate_kind 2)
     float *part;       // [workgroup][3][d]: dw_post, dgate, dw_pre sums
-    int T, chunks, gate_kind;
+    bool want[3];      // which of them
+    unsigned T;
+    int chunks, gate_kind;
     float inv_d, eps, scale;
 };
 
 template <typename E, int NT, int VPT>
-__global__ __launch_bounds__(kThreads) void k_norm_back(NormBackArgs a) {
+__global__ __launch_bounds__(kBlock<NT>) void k_norm_back(NormBackArgs a) {
     constexpr int N = Chunk<E>::N;
-    __shared__ float slots[2][3][kWaves];
+    __shared__ Slots slots;
     int turn = 0;
-    const int lane = threadIdx.x % NT, rows = kThreads / NT;
-    const int row0 = blockIdx.x * rows + threadIdx.x / NT;
+    constexpr int kRows = kBlock<NT> / NT;
+    const int lane = threadIdx.x % NT, sub = threadIdx.x / NT;
     const u32x4 zero = {0, 0, 0, 0};
     const u32x4 *gate_ch = a.gate_kind == 1 ? static_cast<const u32x4 *>(a.gate) : nullptr;
     const float *gate_tok = a.gate_kind == 2 ? static_cast<const float *>(a.gate) : nullptr;
@@ -210,16 +232,28 @@ __global__ __launch_bounds__(kThreads) void k_norm_back(NormBackArgs a) {
 #pragma unroll
         for (int i = 0; i < N; i++) acc_post[j][i] = acc_gate[j][i] = acc_pre[j][i] = 0.f;
     }
-    for (int t = row0; t < a.T; t += gridDim.x * rows) {
+    const unsigned stride = gridDim.x * kRows;
+    u32x4 drn[VPT], dhn[VPT], rn[VPT], yn[VPT];  // the next row's chunks
+    auto load = [&](unsigned t) {
+        const size_t base = static_cast<size_t>(t) * a.chunks + lane;
+#pragma unroll
+        for (int j = 0; j < VPT; j++) {
+            const bool here = t < a.T && in[j];
+            drn[j] = here && a.dr ? a.dr[base + NT * j] : zero;
+            dhn[j] = here && a.dh ? a.dh[base + NT * j] : zero;
+            rn[j] = here && a.dh ? a.r[base + NT * j] : zero;
+            yn[j] = here && a.y ? a.y[base + NT * j] : zero;
+        }
+    };
+    load(blockIdx.x * kRows + sub);
+    for (unsigned t0 = blockIdx.x * kRows; t0 < a.T; t0 += stride) {
+        const unsigned t = t0 + sub;
+        const bool live = t < a.T;
         const size_t base = static_cast<size_t>(t) * a.chunks + lane;
         u32x4 drr[VPT], dhr[VPT], rr[VPT], yr[VPT];
 #pragma unroll
-        for (int j = 0; j < VPT; j++) {
-            drr[j] = in[j] && a.dr ? a.dr[base + NT * j] : zero;
-            dhr[j] = in[j] && a.dh ? a.dh[base + NT * j] : zero;
-            rr[j] = in[j] && a.dh ? a.r[base + NT * j] : zero;
-            yr[j] = in[j] && a.y ? a.y[base + NT * j] : zero;
-        }
+        for (int j = 0; j < VPT; j++) drr[j] = drn[j], dhr[j] = dhn[j], rr[j] = rn[j], yr[j] = yn[j];
+        load(t + stride);
         float sums[3] = {0.f, 0.f, 0.f};  // r.r, (dh w_pre).r, y.y
 #pragma unroll
         for (int j = 0; j < VPT; j++) {
@@ -240,7 +274,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_back(NormBackArgs a) {
         const float rstd_r = 1.f / sqrtf(fmaf(sums[0], a.inv_d, a.eps));
         const float back_r = sums[1] * a.inv_d * rstd_r * rstd_r * rstd_r;
         const float rstd_y = a.w_post ? 1.f / sqrtf(fmaf(sums[2], a.inv_d, a.eps)) : 1.f;
-        const float gt = gate_tok ? gate_tok[t] : 1.f;
+        const float gt = gate_tok && live ? gate_tok[t] : 1.f;
 
         float q[VPT][N];       // scale gate dr' (w_post): the gradient at n(y), or at y
         float two[2] = {0.f, 0.f};  // q.y, and dz.z for a token gate
@@ -258,7 +292,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_back(NormBackArgs a) {
                     q[j][i] += rstd_r * (v[i] * w[i]) - u[i] * back_r;
                 }
             }
-            if (in[j]) a.dx[base + NT * j] = Chunk<E>::pack(q[j]);
+            if (live && in[j]) a.dx[base + NT * j] = Chunk<E>::pack(q[j]);
             if (!a.dy) continue;
             Chunk<E>::unpack(yr[j], u);
             Chunk<E>::unpack(wpost[j], v);
@@ -281,7 +315,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_back(NormBackArgs a) {
         if (a.w_post || gate_tok) {
             row_sums<NT>(two, slots, turn);
             if (a.w_post) back_y = two[0] * a.inv_d * rstd_y * rstd_y * rstd_y;
-            if (gate_tok && lane == 0) a.dgate_tok[t] = two[1];
+            if (gate_tok && live && lane == 0) a.dgate_tok[t] = two[1];
         }
 #pragma unroll
         for (int j = 0; j < VPT; j++) {
@@ -289,41 +323,35 @@ __global__ __launch_bounds__(kThreads) void k_norm_back(NormBackArgs a) {
             Chunk<E>::unpack(yr[j], u);
 #pragma unroll
             for (int i = 0; i < N; i++) q[j][i] = rstd_y * q[j][i] - u[i] * back_y;
-            if (in[j]) a.dy[base + NT * j] = Chunk<E>::pack(q[j]);
+            if (live && in[j]) a.dy[base + NT * j] = Chunk<E>::pack(q[j]);
         }
     }
 
-    // this workgroup's column sums, its waves' rows added in wave order
+    // this workgroup's column sums, its rows' added in order
     const int d = a.chunks * N;
     float *out = a.part + static_cast<size_t>(blockIdx.x) * 3 * d;
-    if constexpr (NT > kWave) {
+    __shared__ float col[kRows > 1 ? kRows : 1][kRows > 1 ? NT * VPT * N : 1];
 #pragma unroll
-        for (int j = 0; j < VPT; j++)
-            if (in[j]) {
-                const int c = (lane + NT * j) * N;
-#pragma unroll
-                for (int i = 0; i < N; i++) {
-                    out[c + i] = acc_post[j][i];
-                    out[d + c + i] = acc_gate[j][i];
-                    out[2 * d + c + i] = acc_pre[j][i];
-                }
-            }
-    } else {
-        __shared__ float col[kWaves][NT * VPT * N];
-#pragma unroll
-        for (int k = 0; k < 3; k++) {
-            if (k) __syncthreads();
-            const auto &acc = k == 0 ? acc_post : k == 1 ? acc_gate : acc_pre;
+    for (int k = 0; k < 3; k++) {
+        if (!a.want[k]) continue;
+        const auto &acc = k == 0 ? acc_post : k == 1 ? acc_gate : acc_pre;
+        if constexpr (kRows == 1) {
 #pragma unroll
             for (int j = 0; j < VPT; j++)
 #pragma unroll
                 for (int i = 0; i < N; i++)
-                    col[threadIdx.x / NT][(lane + NT * j) * N + i] = acc[j][i];
+                    if (in[j]) out[k * d + (lane + NT * j) * N + i] = acc[j][i];
+        } else {
+            __syncthreads();  // the sums before these have been read
+#pragma unroll
+            for (int j = 0; j < VPT; j++)
+#pragma unroll
+                for (int i = 0; i < N; i++) col[sub][(lane + NT * j) * N + i] = acc[j][i];
             __syncthreads();
-            for (int c = threadIdx.x; c < d; c += kThreads) {
+            for (int c = threadIdx.x; c < d; c += kBlock<NT>) {
                 float s = 0.f;
 #pragma unroll
-                for (int q = 0; q < kWaves; q++) s += col[q][c];
+                for (int q = 0; q < kRows; q++) s += col[q][c];
                 out[k * d + c] = s;
             }
         }
@@ -341,6 +369,7 @@ __global__ __launch_bounds__(kFoldCols *kFoldShares) void k_norm_fold(
     const int c = blockIdx.x * kFoldCols + threadIdx.x % kFoldCols, sh = threadIdx.x / kFoldCols;
     float v = 0.f;
     if (c < d)
+#pragma unroll 8
         for (int b = sh; b < blocks; b += kFoldShares)
             v += part[(static_cast<size_t>(b) * 3 + blockIdx.y) * d + c];
     s[sh][threadIdx.x % kFoldCols] = v;
@@ -350,32 +379,34 @@ __global__ __launch_bounds__(kFoldCols *kFoldShares) void k_norm_fold(
     out[c] = v;
 }
 
-// f(NT, VPT) for the smallest variant that holds a row of `chunks` chunks.
+// Threads that share a row of `chunks` chunks and chunks of each thread.
 template <typename F>
 void by_width(int chunks, F f) {
     using std::integral_constant;
     if (chunks <= 64)
-        f(integral_constant<int, kWave>{}, integral_constant<int, 1>{});
+        f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
     else if (chunks <= 128)
-        f(integral_constant<int, kWave>{}, integral_constant<int, 2>{});
+        f(integral_constant<int, 128>{}, integral_constant<int, 1>{});
     else if (chunks <= 256)
-        f(integral_constant<int, kWave>{}, integral_constant<int, 4>{});
+        f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
     else if (chunks <= 512)
-        f(integral_constant<int, kThreads>{}, integral_constant<int, 2>{});
+        f(integral_constant<int, 512>{}, integral_constant<int, 1>{});
     else
-        f(integral_constant<int, kThreads>{}, integral_constant<int, 4>{});
+        f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
 }
 
-int rows_per_block(int chunks) { return chunks <= 256 ? kWaves : 1; }
+// Rows that a workgroup takes at once: NT as chosen above.
+int rows_per_block(int nt) { return nt >= 256 ? 1 : 256 / nt; }
 
 }  // namespace
 
-// Forward: enough workgroups to fill the CUs' waves.  Backward: two per CU,
-// since each leaves 3 d fp32 column sums behind.
-constexpr int kNormBlocks = 2048, kNormBackBlocks = 512;
+// Backward workgroups at most: two per CU, since each leaves 3 d fp32 sums
+// behind (one per CU: 52 us at T = 8192, d = 2048 against 46; four: 50).
+constexpr int kNormBackBlocks = 512;
 
 int norm_back_blocks(int T, int chunks) {
-    const int need = static_cast<int>(ceil_div(T, rows_per_block(chunks)));
+    int need = 0;
+    by_width(chunks, [&](auto nt, auto) { need = ceil_div(T, rows_per_block(nt)); });
     return need < kNormBackBlocks ? need : kNormBackBlocks;
 }
 
@@ -396,13 +427,14 @@ hipError_t launch_block_norm(const void *x, const void *y, const void *w_post, c
     a.inv_d = 1.f / static_cast<float>(d);
     a.eps = eps;
     a.scale = scale;
-    const unsigned need = ceil_div(T, rows_per_block(a.chunks));
-    const unsigned grid = need < kNormBlocks ? need : kNormBlocks;
     by_width(a.chunks, [&](auto nt, auto vpt) {
+        constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
+        // one row per team, up to the most threads that a launch holds
+        const unsigned grid = std::min(ceil_div(T, rows_per_block(NT)), 1u << 22);
         if (bf16)
-            k_norm<uint16_t, decltype(nt)::value, decltype(vpt)::value><<<grid, kThreads, 0, s>>>(a);
+            k_norm<uint16_t, NT, VPT><<<grid, kBlock<NT>, 0, s>>>(a);
         else
-            k_norm<float, decltype(nt)::value, decltype(vpt)::value><<<grid, kThreads, 0, s>>>(a);
+            k_norm<float, NT, VPT><<<grid, kBlock<NT>, 0, s>>>(a);
     });
     return hipGetLastError();
 }
@@ -425,6 +457,9 @@ hipError_t launch_block_norm_back(const void *dr, const void *dh, const void *r,
     a.dy = static_cast<u32x4 *>(dy);
     a.dgate_tok = gate_kind == 2 ? dgate : nullptr;
     a.part = part;
+    a.want[0] = dw_post;
+    a.want[1] = gate_kind == 1;
+    a.want[2] = dw_pre;
     a.T = T;
     a.chunks = d / (bf16 ? 8 : 4);
     a.gate_kind = gate_kind;
@@ -433,12 +468,11 @@ hipError_t launch_block_norm_back(const void *dr, const void *dh, const void *r,
     a.scale = scale;
     const int grid = norm_back_blocks(T, a.chunks);
     by_width(a.chunks, [&](auto nt, auto vpt) {
+        constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
         if (bf16)
-            k_norm_back<uint16_t, decltype(nt)::value, decltype(vpt)::value>
-                <<<grid, kThreads, 0, s>>>(a);
+            k_norm_back<uint16_t, NT, VPT><<<grid, kBlock<NT>, 0, s>>>(a);
         else
-            k_norm_back<float, decltype(nt)::value, decltype(vpt)::value>
-                <<<grid, kThreads, 0, s>>>(a);
+            k_norm_back<float, NT, VPT><<<grid, kBlock<NT>, 0, s>>>(a);
     });
     float *dgate_ch = gate_kind == 1 ? dgate : nullptr;
     if (dw_post || dgate_ch || dw_pre)

@@ -397,24 +397,38 @@ def occ_moe_backward(desc: LayerDesc, dy, x, logits, placement, w_gate, w_up, w_
 _TORCH = {OCC_F32: torch.float32, OCC_BF16: torch.bfloat16}
 
 
-def _queue(what: str, fn, args, tensors, stream):
-    """Calls fn(*args, stream) with the tensors' device as the current one; all of them (None
-    among them) must share it, and so must the stream."""
-    device = None
-    for t in tensors:
-        if t is None:
-            continue
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{what}: tensors on {device} and on {t.device}")
-    if stream is not None and device is not None and stream.device != device:
-        raise ValueError(f"{what}: tensors on {device}, stream on {stream.device}")
-    if device is None or device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), what)
+def _addr(t: torch.Tensor | None, name: str, dtype, shape: tuple, index: int):
+    """The address of a contiguous device tensor of this type and shape on the call's device."""
+    if t is None:
+        return None
+    if (index < 0 or t.get_device() != index or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
+        _dev(t, name, dtype, shape)  # says which check fails
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{index}")
+    return t.data_ptr()
+
+
+def _device(t: torch.Tensor | None) -> int:
+    """The device of a call's tensors, taken from one that it cannot do without (-1: the tensor
+    is missing, which the library refuses, or is a host tensor, which _addr refuses)."""
+    return -1 if t is None else t.get_device()
+
+
+def _queue(what: str, fn, index: int, stream, *args):
+    """fn(*args, stream) with device `index` as the current one."""
+    if index < 0:
+        raise OccError(OCC_ERR_INVALID_ARG, what)
+    if stream is None:
+        stream = torch.cuda.current_stream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"{what}: tensors on cuda:{index}, stream on {stream.device}")
+    if torch.cuda.current_device() == index:
+        status = fn(*args, stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)), what)
+        with torch.cuda.device(index):
+            status = fn(*args, stream.cuda_stream)
+    if status != OCC_OK:
+        raise OccError(status, what)
 
 
 def occ_block_workspace_size(desc: LayerDesc) -> int:
@@ -429,93 +443,94 @@ def alloc_block_workspace(desc: LayerDesc, device="cuda") -> torch.Tensor:
     return torch.empty(occ_block_workspace_size(desc), dtype=torch.uint8, device=device)
 
 
-def _ws(workspace):
+def _ws(workspace, index: int):
     if workspace is None:
         return None, 0
-    return _dev(workspace, "workspace", torch.uint8), workspace.numel()
+    return (_addr(workspace, "workspace", torch.uint8, (workspace.numel(),), index),
+            workspace.numel())
 
 
-def _norm_gate(desc: LayerDesc, opt: NormDesc, gate):
+def _norm_gate(desc: LayerDesc, opt: NormDesc):
+    """The type and shape of a gate (its gradient has that shape in fp32)."""
     if opt.gate == OCC_GATE_TOKEN:
-        return _dev(gate, "gate", torch.float32, (desc.T,))
-    return _dev(gate, "gate", _TORCH.get(desc.dtype), (desc.d,))
+        return torch.float32, (desc.T,)
+    return _TORCH.get(desc.dtype), (desc.d,)
 
 
 def occ_block_norm(desc: LayerDesc, opt: NormDesc, x, y, w_post, gate, w_pre, r, h, stream=None):
     """r = x + scale gate w_post n(y), h = w_pre n(r); y, w_post, gate and w_pre with h may be
     None (see occ.h)."""
-    dt, rows, d = _TORCH.get(desc.dtype), (desc.T, desc.d), (desc.d,)
-    args = (ctypes.byref(desc), ctypes.byref(opt), _dev(x, "x", dt, rows), _dev(y, "y", dt, rows),
-            _dev(w_post, "w_post", dt, d), _norm_gate(desc, opt, gate),
-            _dev(w_pre, "w_pre", dt, d), _dev(r, "r", dt, rows), _dev(h, "h", dt, rows))
-    _queue("occ_block_norm", lib().occ_block_norm, args, (x, y, w_post, gate, w_pre, r, h), stream)
+    dt, d, i = _TORCH.get(desc.dtype), (desc.d,), _device(x)
+    rows = (desc.T, desc.d)
+    _queue("occ_block_norm", lib().occ_block_norm, i, stream, desc, opt,
+           _addr(x, "x", dt, rows, i), _addr(y, "y", dt, rows, i),
+           _addr(w_post, "w_post", dt, d, i), _addr(gate, "gate", *_norm_gate(desc, opt), i),
+           _addr(w_pre, "w_pre", dt, d, i), _addr(r, "r", dt, rows, i), _addr(h, "h", dt, rows, i))
 
 
 def occ_block_norm_backward(desc: LayerDesc, opt: NormDesc, dr, dh, r, y, w_post, gate, w_pre, dx,
                             dy, dw_post, dgate, dw_pre, workspace, stream=None):
     """Gradients of occ_block_norm from dr and dh (r: its r, or its x without y)."""
-    dt, rows, d, f32 = _TORCH.get(desc.dtype), (desc.T, desc.d), (desc.d,), torch.float32
-    gate_shape = (desc.T,) if opt.gate == OCC_GATE_TOKEN else d
-    args = (ctypes.byref(desc), ctypes.byref(opt), _dev(dr, "dr", dt, rows),
-            _dev(dh, "dh", dt, rows), _dev(r, "r", dt, rows), _dev(y, "y", dt, rows),
-            _dev(w_post, "w_post", dt, d), _norm_gate(desc, opt, gate),
-            _dev(w_pre, "w_pre", dt, d), _dev(dx, "dx", dt, rows), _dev(dy, "dy", dt, rows),
-            _dev(dw_post, "dw_post", f32, d), _dev(dgate, "dgate", f32, gate_shape),
-            _dev(dw_pre, "dw_pre", f32, d), *_ws(workspace))
-    _queue("occ_block_norm_backward", lib().occ_block_norm_backward, args,
-           (dr, dh, r, y, w_post, gate, w_pre, dx, dy, dw_post, dgate, dw_pre, workspace), stream)
+    dt, d, i, f32 = _TORCH.get(desc.dtype), (desc.d,), _device(dx), torch.float32
+    rows, (gate_dt, gate_shape) = (desc.T, desc.d), _norm_gate(desc, opt)
+    _queue("occ_block_norm_backward", lib().occ_block_norm_backward, i, stream, desc, opt,
+           _addr(dr, "dr", dt, rows, i), _addr(dh, "dh", dt, rows, i), _addr(r, "r", dt, rows, i),
+           _addr(y, "y", dt, rows, i), _addr(w_post, "w_post", dt, d, i),
+           _addr(gate, "gate", gate_dt, gate_shape, i), _addr(w_pre, "w_pre", dt, d, i),
+           _addr(dx, "dx", dt, rows, i), _addr(dy, "dy", dt, rows, i),
+           _addr(dw_post, "dw_post", f32, d, i), _addr(dgate, "dgate", f32, gate_shape, i),
+           _addr(dw_pre, "dw_pre", f32, d, i), *_ws(workspace, i))
 
 
-def _valid(valid, T):
-    if valid is not None and valid.dtype not in (torch.bool, torch.uint8):
+def _mask(valid, T: int, index: int):
+    if valid is not None and valid.dtype is not torch.bool and valid.dtype is not torch.uint8:
         raise ValueError(f"valid must be torch.bool or torch.uint8, got {valid.dtype}")
-    return _dev(valid, "valid", None, (T,))
+    return None if valid is None else _addr(valid, "valid", valid.dtype, (T,), index)
 
 
-def _placement(desc: LayerDesc, placement):
-    """The placement as host int32 (kept by the caller during the call), or None."""
+def _place(desc: LayerDesc, placement):
+    """The placement as host int32 and its address, or Nones."""
     if placement is None:
-        return None
-    return _host_i32(placement, "placement", (desc.Nd, desc.Ne // max(desc.Nd, 1)))
+        return None, None
+    L = _host_i32(placement, "placement", (desc.Nd, desc.Ne // max(desc.Nd, 1)))
+    return L, L.ctypes.data
 
 
 def occ_balance_loss(desc: LayerDesc, opt: BalanceDesc, logits, ids, valid, placement, counts,
                      probs, loss, workspace, stream=None):
     """Router losses [sum, balance, group, z], mean probabilities, and the counts (Ne, then the
     valid tokens)."""
-    T, Ne, k, f32 = desc.T, desc.Ne, desc.k, torch.float32
-    L = _placement(desc, placement)
-    args = (ctypes.byref(desc), ctypes.byref(opt), _dev(logits, "logits", f32, (T, Ne)),
-            _dev(ids, "ids", torch.int32, (T, k)), _valid(valid, T),
-            None if L is None else _hp(L), _dev(counts, "counts", torch.int32, (Ne + 1,)),
-            _dev(probs, "probs", f32, (Ne,)), _dev(loss, "loss", f32, (4,)), *_ws(workspace))
-    _queue("occ_balance_loss", lib().occ_balance_loss, args,
-           (logits, ids, valid, counts, probs, loss, workspace), stream)
+    T, Ne, f32, i32, i = desc.T, desc.Ne, torch.float32, torch.int32, _device(logits)
+    L, place = _place(desc, placement)
+    _queue("occ_balance_loss", lib().occ_balance_loss, i, stream, desc, opt,
+           _addr(logits, "logits", f32, (T, Ne), i), _addr(ids, "ids", i32, (T, desc.k), i),
+           _mask(valid, T, i), place, _addr(counts, "counts", i32, (Ne + 1,), i),
+           _addr(probs, "probs", f32, (Ne,), i), _addr(loss, "loss", f32, (4,), i),
+           *_ws(workspace, i))
 
 
 def occ_balance_backward(desc: LayerDesc, opt: BalanceDesc, logits, valid, placement, counts,
                          dloss: float, dlogits_in, dlogits, stream=None):
     """dlogits = dlogits_in + dloss times the losses' gradient in the logits."""
-    T, Ne, f32 = desc.T, desc.Ne, torch.float32
-    L = _placement(desc, placement)
-    args = (ctypes.byref(desc), ctypes.byref(opt), _dev(logits, "logits", f32, (T, Ne)),
-            _valid(valid, T), None if L is None else _hp(L),
-            _dev(counts, "counts", torch.int32, (Ne + 1,)), dloss,
-            _dev(dlogits_in, "dlogits_in", f32, (T, Ne)), _dev(dlogits, "dlogits", f32, (T, Ne)))
-    _queue("occ_balance_backward", lib().occ_balance_backward, args,
-           (logits, valid, counts, dlogits_in, dlogits), stream)
+    T, Ne, f32, i = desc.T, desc.Ne, torch.float32, _device(logits)
+    L, place = _place(desc, placement)
+    _queue("occ_balance_backward", lib().occ_balance_backward, i, stream, desc, opt,
+           _addr(logits, "logits", f32, (T, Ne), i), _mask(valid, T, i), place,
+           _addr(counts, "counts", torch.int32, (Ne + 1,), i), dloss,
+           _addr(dlogits_in, "dlogits_in", f32, (T, Ne), i),
+           _addr(dlogits, "dlogits", f32, (T, Ne), i))
 
 
 def occ_gate_backward(desc: LayerDesc, dlogits, x, w_router, dx_in, dx, dw_router, workspace,
                       stream=None):
     """dx = dx_in + dlogits w_router, dw_router = dlogits^T x; dx or dw_router may be None."""
     T, d, Ne, dt, f32 = desc.T, desc.d, desc.Ne, _TORCH.get(desc.dtype), torch.float32
-    args = (ctypes.byref(desc), _dev(dlogits, "dlogits", f32, (T, Ne)), _dev(x, "x", dt, (T, d)),
-            _dev(w_router, "w_router", dt, (Ne, d)), _dev(dx_in, "dx_in", dt, (T, d)),
-            _dev(dx, "dx", dt, (T, d)), _dev(dw_router, "dw_router", f32, (Ne, d)),
-            *_ws(workspace))
-    _queue("occ_gate_backward", lib().occ_gate_backward, args,
-           (dlogits, x, w_router, dx_in, dx, dw_router, workspace), stream)
+    i = _device(dlogits)
+    _queue("occ_gate_backward", lib().occ_gate_backward, i, stream, desc,
+           _addr(dlogits, "dlogits", f32, (T, Ne), i), _addr(x, "x", dt, (T, d), i),
+           _addr(w_router, "w_router", dt, (Ne, d), i), _addr(dx_in, "dx_in", dt, (T, d), i),
+           _addr(dx, "dx", dt, (T, d), i), _addr(dw_router, "dw_router", f32, (Ne, d), i),
+           *_ws(workspace, i))
 
 
 class AdamwTensors:
@@ -532,45 +547,53 @@ class AdamwTensors:
         self.state, self.grad_dtype = opt.state, opt.grad_dtype
         self.tensors = [dict(t) for t in tensors]
         self.table = (AdamwTensor * max(len(self.tensors), 1))()
-        self.devices = []  # one tensor for each device among them
+        self.index = None  # the tensors' device
         eight, f32 = opt.state == OCC_ADAMW_8BIT, torch.float32
         state = torch.float8_e4m3fn if eight else f32
         names = {n for n, _ in AdamwTensor._fields_[1:]}
-        for i, (t, row) in enumerate(zip(self.tensors, self.table)):
+        for k, (t, row) in enumerate(zip(self.tensors, self.table)):
             if set(t) - names:
-                raise ValueError(f"tensor {i}: unknown entries {sorted(set(t) - names)}")
+                raise ValueError(f"tensor {k}: unknown entries {sorted(set(t) - names)}")
+
+            def address(name, dtype, shape):
+                return _addr(t.get(name), f"tensor {k}: {name}", dtype, shape, self.index)
+
+            if t.get("p") is None:
+                raise ValueError(f"tensor {k}: p must be given")
+            if self.index is None:
+                self.index = _device(t["p"])
             shape = tuple(t["p"].shape)
             row.n = t["p"].numel()
-            units = (-(-row.n // OCC_ADAMW_BLOCK),) if eight else None
+            units = (-(-row.n // OCC_ADAMW_BLOCK),)
             for name, dtype in (("p", f32), ("g", _TORCH.get(opt.grad_dtype)), ("m", state),
                                 ("v", state), ("m_scale", f32), ("v_scale", f32)):
-                a, scale = t.get(name), name.endswith("_scale")
-                if (a is None) != (scale and not eight):
-                    raise ValueError(f"tensor {i}: {name} must be "
-                                     f"{'None' if a is not None else 'given'}")
+                scale = name.endswith("_scale")
+                given = t.get(name) is not None
+                if given == (scale and not eight):
+                    raise ValueError(f"tensor {k}: {name} must be {'None' if given else 'given'}")
                 want = units if scale else shape
-                address = _dev(a, f"tensor {i}: {name}", dtype, want)
-                setattr(row, name, address)
-                if name != "g":
-                    out = t.get(name + "_out")
-                    if out is not None and a is None:
-                        raise ValueError(f"tensor {i}: {name}_out must be None")
-                    setattr(row, name + "_out", address if out is None else
-                            _dev(out, f"tensor {i}: {name}_out", dtype, want))
-            row.p_bf16 = _dev(t.get("p_bf16"), f"tensor {i}: p_bf16", torch.bfloat16, shape)
-            for a in t.values():
-                if a is not None and all(a.device != b.device for b in self.devices):
-                    self.devices.append(a)
+                setattr(row, name, address(name, dtype, want))
+                if name == "g":
+                    continue
+                out = name + "_out"
+                if t.get(out) is None:
+                    setattr(row, out, getattr(row, name))
+                elif given:
+                    setattr(row, out, address(out, dtype, want))
+                else:
+                    raise ValueError(f"tensor {k}: {out} must be None")
+            row.p_bf16 = address("p_bf16", torch.bfloat16, shape)
 
 
 def occ_adamw_step(opt: AdamwDesc, tensors: AdamwTensors, dynamic=None, stream=None):
     """One AdamW step over the tensors; dynamic: None or a device fp32 tensor
     [lr, step, grad_scale] that replaces the descriptor's."""
-    if (opt.state, opt.grad_dtype) != (tensors.state, tensors.grad_dtype):
+    if opt.state != tensors.state or opt.grad_dtype != tensors.grad_dtype:
         raise ValueError("the descriptor's state and grad_dtype differ from the table's")
-    args = (ctypes.byref(opt), tensors.table, len(tensors.tensors),
-            _dev(dynamic, "dynamic", torch.float32, (3,)))
-    _queue("occ_adamw_step", lib().occ_adamw_step, args, (*tensors.devices, dynamic), stream)
+    if not tensors.tensors:
+        return
+    _queue("occ_adamw_step", lib().occ_adamw_step, tensors.index, stream, opt, tensors.table,
+           len(tensors.tensors), _addr(dynamic, "dynamic", torch.float32, (3,), tensors.index))
 
 
 def occ_forward_views(desc: LayerDesc, workspace) -> ForwardView:
