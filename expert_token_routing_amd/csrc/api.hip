@@ -329,7 +329,7 @@ int row_chunks(const occ_layer_desc &D) { return static_cast<int>(D.d * elem_byt
 size_t block_ws_bytes(const occ_layer_desc &D) {
     const size_t d = D.d, bf16 = D.dtype == OCC_BF16;
     return align_up(std::max<size_t>(
-        {norm_back_blocks(D.T, row_chunks(D)) * 3 * d * 4, balance_part_bytes(D.T, D.Ne),
+        {norm_back_blocks(D.T, row_chunks(D)) * 2 * d * 4, balance_part_bytes(D.T, D.Ne),
          static_cast<size_t>(gate_dw_shares(D.T, D.d, D.Ne, bf16)) * D.Ne * d * 4}));
 }
 

@@ -35,28 +35,6 @@ constexpr int kBalWaves = kBalThreads / kWave;
 constexpr int kBackThreads = 512;
 constexpr int kTokens = 2;  // tokens that a forward team has in flight
 
-constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
-
-// Reductions over teams of L lanes; every lane of the team gets the result.
-template <int L, typename F>
-__device__ __forceinline__ float team_reduce(float v, F f) {
-    v = f(v, dpp_f<kDppXor1, 0xf>(v, v));
-    v = f(v, dpp_f<kDppXor2, 0xf>(v, v));
-    v = f(v, dpp_f<kDppHalfMirror, 0xf>(v, v));
-    v = f(v, dpp_f<kDppMirror, 0xf>(v, v));
-    if constexpr (L >= 32) v = f(v, __shfl_xor(v, 16));
-    if constexpr (L >= 64) v = f(v, __shfl_xor(v, 32));
-    return v;
-}
-template <int L>
-__device__ __forceinline__ float team_sum(float v) {
-    return team_reduce<L>(v, [](float a, float b) { return a + b; });
-}
-template <int L>
-__device__ __forceinline__ float team_max(float v) {
-    return team_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
-}
-
 // A token's logits, expert l + L i in x[i] and -inf behind Ne.
 template <int L, int NI>
 __device__ __forceinline__ void team_load(const float *__restrict__ row, bool in, int l, int Ne,
@@ -75,7 +53,7 @@ __device__ __forceinline__ float team_softmax(float (&p)[NI]) {
     float m = p[0];
 #pragma unroll
     for (int i = 1; i < NI; i++) m = fmaxf(m, p[i]);
-    m = team_max<L>(m);
+    m = group_max<L>(m);
     const float shift = m == -INFINITY ? 0.f : m;
     float s = 0.f;
 #pragma unroll
@@ -83,7 +61,7 @@ __device__ __forceinline__ float team_softmax(float (&p)[NI]) {
         p[i] = __expf(p[i] - shift);
         s += p[i];
     }
-    s = team_sum<L>(s);
+    s = group_sum<L>(s);
     const bool none = s == 0.f;
     const float inv = none ? 0.f : 1.f / s;
 #pragma unroll
@@ -260,7 +238,7 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_final(const float *__re
     double p = 0.;
     int c = 0;
     if (sh < shares)
-#pragma unroll 16
+#pragma unroll 8
         for (int b = sh; b < blocks; b += shares) {
             const float *row = part + static_cast<size_t>(b) * part_words(Ne);
             p += row[e];
@@ -316,7 +294,7 @@ __global__ __launch_bounds__(kBackThreads) void k_balance_back(
         const float lse = team_softmax<L, NI>(p);
 #pragma unroll
         for (int i = 0; i < NI; i++) dot = fmaf(c[i], p[i], dot);
-        const float add = 2.f * cz * lse - team_sum<L>(dot);
+        const float add = 2.f * cz * lse - group_sum<L>(dot);
 #pragma unroll
         for (int i = 0; i < NI; i++) {
             const int e = l + L * i;

@@ -102,6 +102,28 @@ __device__ __forceinline__ float wave_max(float v) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), kWave - 1));
 }
 
+// Reduction over aligned groups of L lanes (2, 4, ..., 64) by an associative
+// and commutative f; every lane of a group gets its result.
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+template <int L, typename F>
+__device__ __forceinline__ float group_reduce(float v, F f) {
+    if constexpr (L >= 2) v = f(v, dpp_f<kDppXor1, 0xf>(v, v));
+    if constexpr (L >= 4) v = f(v, dpp_f<kDppXor2, 0xf>(v, v));
+    if constexpr (L >= 8) v = f(v, dpp_f<kDppHalfMirror, 0xf>(v, v));
+    if constexpr (L >= 16) v = f(v, dpp_f<kDppMirror, 0xf>(v, v));
+    if constexpr (L >= 32) v = f(v, __shfl_xor(v, 16));
+    if constexpr (L >= 64) v = f(v, __shfl_xor(v, 32));
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+    return group_reduce<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
+    return group_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
 // Wave-wide arg-max of (value, index): larger value wins, ties to the lower
 // index.  Every lane returns the winner.
 __device__ __forceinline__ void wave_argmax(float &v, int &i) {

@@ -236,7 +236,7 @@ hipError_t launch_route_backward(const float *logits, const int32_t *ids, const 
 hipError_t launch_block_norm(const void *x, const void *y, const void *w_post, const void *gate,
                              const void *w_pre, int T, int d, int bf16, int gate_kind, float eps,
                              float scale, void *r, void *h, hipStream_t s);
-// Its backward; part holds norm_back_blocks x 3 x d floats.
+// Its backward; part holds norm_back_blocks x 2 x d floats.
 int norm_back_blocks(int T, int chunks);  // chunks: 16-byte pieces of a row
 hipError_t launch_block_norm_back(const void *dr, const void *dh, const void *r, const void *y,
                                   const void *w_post, const void *gate, const void *w_pre, int T,

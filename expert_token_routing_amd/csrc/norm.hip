@@ -6,7 +6,10 @@
 //   r = x + s g w_post n(y),   h = w_pre n(r).
 // The gradient of <q, n(v)> in v is rstd q - v rstd^3 mean(q v), so a row's
 // backward needs three sums before dr' = dr + (gradient through h) is known
-// (r.r, (dh w_pre).r, y.y) and one after it ((s dr' g w_post).y).
+// (r.r, (dh w_pre).r, y.y) and one after it ((dr' g w_post).y), which is also a
+// token gate's gradient.  The gradients of w_post and of a channel gate come
+// from one column sum, S = sum over rows of s g_token dr' n(y): gate S and
+// w_post S.
 //
 // Memory bound: the forward reads x and y and writes r and h once, the
 // backward reads dr, dh, r and y and writes dx and dy once.  A row stays in
@@ -20,12 +23,13 @@
 // The forward gives each row to a team of its own.  In the backward each
 // thread also keeps fp32 sums of its columns' weight gradients, so its teams
 // walk over rows with a fixed stride, the next row's loads issued before this
-// one's sums (46 us at T = 8192, d = 2048, 50 without); a workgroup's sums go
-// to the workspace once and a second kernel adds the workgroups' in order, so
-// results do not depend on timing.
+// one's sums; a workgroup's sums go to the workspace once and a second kernel
+// adds the workgroups' in order, so results do not depend on timing.
+// Workgroups of 1024 threads, one per CU, leave the fewest such sums: 299 us
+// at T = 65536, d = 2048 against 313 with two of 256 threads.
 // Measured at d = 2048 bf16, all parts present: forward T = 65536 184 us
-// (5.8 TB/s of the bytes it cannot do without), backward T = 8192 46 + 5 us
-// (4.0 TB/s), one token 2.6 us.
+// (5.8 TB/s of the bytes it cannot do without), one token 2.6; backward
+// T = 65536 299 us (5.4 TB/s), T = 8192 44.7 + 4.8 us (4.1 TB/s).
 // Stores past the caches measure 3% faster alone and slower by 2 to 5% with
 // the kernel that reads their rows, so they are ordinary.
 #include <algorithm>
@@ -35,9 +39,11 @@
 namespace occ {
 namespace {
 
-// NT threads share a row, in workgroups of at least 256 threads.
+// NT threads share a row: forward in workgroups of at least 256 threads,
+// backward in workgroups of 1024.
 template <int NT>
 constexpr int kBlock = NT > 256 ? NT : 256;
+constexpr int kBackBlock = 1024;
 
 // A chunk is 16 bytes of a row: E values.
 template <typename E>
@@ -79,7 +85,7 @@ struct Chunk<float> {
 // Sums over the NT threads that share a row.  Rows of several waves go
 // through LDS, with two sets of slots used in turn (the next sum's writes
 // cannot meet this one's reads, since the barrier in between orders them).
-constexpr int kMaxWaves = 8;
+constexpr int kMaxWaves = kBackBlock / kWave;
 typedef float Slots[2][3][kMaxWaves];
 template <int NT, int M>
 __device__ __forceinline__ void row_sums(float (&v)[M], Slots &slots, int &turn) {
@@ -94,11 +100,8 @@ __device__ __forceinline__ void row_sums(float (&v)[M], Slots &slots, int &turn)
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < M; i++) {
-            v[i] = 0.f;
-#pragma unroll
-            for (int q = 0; q < kRowWaves; q++) v[i] += slots[turn][i][w0 + q];
-        }
+        for (int i = 0; i < M; i++)
+            v[i] = group_sum<kRowWaves>(slots[turn][i][w0 + lane_id() % kRowWaves]);
         turn ^= 1;
     }
 }
@@ -202,184 +205,157 @@ struct NormBackArgs {
     const void *gate;
     u32x4 *dx, *dy;
     float *dgate_tok;  // T values (gate_kind 2)
-    float *part;       // [workgroup][3][d]: dw_post, dgate, dw_pre sums
-    bool want[3];      // which of them
+    float *part;       // [workgroup][2][d]: column sums of dz n(y) and of dh n(r)
+    bool want[2];      // which of them
     unsigned T;
     int chunks, gate_kind;
     float inv_d, eps, scale;
 };
 
-template <typename E, int NT, int VPT>
-__global__ __launch_bounds__(kBlock<NT>) void k_norm_back(NormBackArgs a) {
-    constexpr int N = Chunk<E>::N;
+// One chunk of a row per thread.
+template <typename E, int NT>
+__global__ __launch_bounds__(kBackBlock) void k_norm_back(NormBackArgs a) {
+    constexpr int N = Chunk<E>::N, kRows = kBackBlock / NT;
     __shared__ Slots slots;
     int turn = 0;
-    constexpr int kRows = kBlock<NT> / NT;
-    const int lane = threadIdx.x % NT, sub = threadIdx.x / NT;
+    const int c = threadIdx.x % NT, sub = threadIdx.x / NT;
+    const bool in = c < a.chunks;
     const u32x4 zero = {0, 0, 0, 0};
     const u32x4 *gate_ch = a.gate_kind == 1 ? static_cast<const u32x4 *>(a.gate) : nullptr;
     const float *gate_tok = a.gate_kind == 2 ? static_cast<const float *>(a.gate) : nullptr;
-    bool in[VPT];
-    u32x4 wpost[VPT], wpre[VPT], wgate[VPT];
-    float acc_post[VPT][N], acc_gate[VPT][N], acc_pre[VPT][N];
+    const u32x4 wpre = in && a.w_pre ? a.w_pre[c] : zero;
+    float gw[N];  // channel gate times w_post
+    float acc_y[N], acc_r[N];
+    {
+        float g[N];
+        Chunk<E>::unpack(in && a.w_post ? a.w_post[c] : zero, gw);
+        Chunk<E>::unpack(in && gate_ch ? gate_ch[c] : zero, g);
 #pragma unroll
-    for (int j = 0; j < VPT; j++) {
-        const int c = lane + NT * j;
-        in[j] = c < a.chunks;
-        wpost[j] = in[j] && a.w_post ? a.w_post[c] : zero;
-        wpre[j] = in[j] && a.w_pre ? a.w_pre[c] : zero;
-        wgate[j] = in[j] && gate_ch ? gate_ch[c] : zero;
-#pragma unroll
-        for (int i = 0; i < N; i++) acc_post[j][i] = acc_gate[j][i] = acc_pre[j][i] = 0.f;
-    }
-    const unsigned stride = gridDim.x * kRows;
-    u32x4 drn[VPT], dhn[VPT], rn[VPT], yn[VPT];  // the next row's chunks
-    auto load = [&](unsigned t) {
-        const size_t base = static_cast<size_t>(t) * a.chunks + lane;
-#pragma unroll
-        for (int j = 0; j < VPT; j++) {
-            const bool here = t < a.T && in[j];
-            drn[j] = here && a.dr ? a.dr[base + NT * j] : zero;
-            dhn[j] = here && a.dh ? a.dh[base + NT * j] : zero;
-            rn[j] = here && a.dh ? a.r[base + NT * j] : zero;
-            yn[j] = here && a.y ? a.y[base + NT * j] : zero;
+        for (int i = 0; i < N; i++) {
+            gw[i] = (a.w_post ? gw[i] : 1.f) * (gate_ch ? g[i] : 1.f);
+            acc_y[i] = acc_r[i] = 0.f;
         }
+    }
+    u32x4 drn, dhn, rn, yn;  // the next row's chunk
+    auto load = [&](unsigned t) {
+        const size_t at = static_cast<size_t>(t) * a.chunks + c;
+        const bool here = t < a.T && in;
+        drn = here && a.dr ? a.dr[at] : zero;
+        dhn = here && a.dh ? a.dh[at] : zero;
+        rn = here && a.dh ? a.r[at] : zero;
+        yn = here && a.y ? a.y[at] : zero;
     };
+    const unsigned stride = gridDim.x * kRows;
     load(blockIdx.x * kRows + sub);
+    // the trip count is the workgroup's: its rows' sums may need barriers
     for (unsigned t0 = blockIdx.x * kRows; t0 < a.T; t0 += stride) {
         const unsigned t = t0 + sub;
         const bool live = t < a.T;
-        const size_t base = static_cast<size_t>(t) * a.chunks + lane;
-        u32x4 drr[VPT], dhr[VPT], rr[VPT], yr[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; j++) drr[j] = drn[j], dhr[j] = dhn[j], rr[j] = rn[j], yr[j] = yn[j];
+        const size_t at = static_cast<size_t>(t) * a.chunks + c;
+        float q[N], dh[N], r[N], y[N], w[N];
+        Chunk<E>::unpack(drn, q);
+        Chunk<E>::unpack(dhn, dh);
+        Chunk<E>::unpack(rn, r);
+        Chunk<E>::unpack(yn, y);
+        Chunk<E>::unpack(wpre, w);
         load(t + stride);
         float sums[3] = {0.f, 0.f, 0.f};  // r.r, (dh w_pre).r, y.y
 #pragma unroll
-        for (int j = 0; j < VPT; j++) {
-            float u[N], v[N], w[N];
-            Chunk<E>::unpack(rr[j], u);
-            Chunk<E>::unpack(dhr[j], v);
-            Chunk<E>::unpack(wpre[j], w);
-#pragma unroll
-            for (int i = 0; i < N; i++) {
-                sums[0] = fmaf(u[i], u[i], sums[0]);
-                sums[1] = fmaf(v[i] * w[i], u[i], sums[1]);
-            }
-            Chunk<E>::unpack(yr[j], u);
-#pragma unroll
-            for (int i = 0; i < N; i++) sums[2] = fmaf(u[i], u[i], sums[2]);
+        for (int i = 0; i < N; i++) {
+            w[i] *= dh[i];
+            sums[0] = fmaf(r[i], r[i], sums[0]);
+            sums[1] = fmaf(w[i], r[i], sums[1]);
+            sums[2] = fmaf(y[i], y[i], sums[2]);
         }
         row_sums<NT>(sums, slots, turn);
         const float rstd_r = 1.f / sqrtf(fmaf(sums[0], a.inv_d, a.eps));
         const float back_r = sums[1] * a.inv_d * rstd_r * rstd_r * rstd_r;
         const float rstd_y = a.w_post ? 1.f / sqrtf(fmaf(sums[2], a.inv_d, a.eps)) : 1.f;
         const float gt = gate_tok && live ? gate_tok[t] : 1.f;
-
-        float q[VPT][N];       // scale gate dr' (w_post): the gradient at n(y), or at y
-        float two[2] = {0.f, 0.f};  // q.y, and dz.z for a token gate
-#pragma unroll
-        for (int j = 0; j < VPT; j++) {
-            float u[N], v[N], w[N];
-            Chunk<E>::unpack(drr[j], q[j]);
-            if (a.dh) {
-                Chunk<E>::unpack(rr[j], u);
-                Chunk<E>::unpack(dhr[j], v);
-                Chunk<E>::unpack(wpre[j], w);
-#pragma unroll
-                for (int i = 0; i < N; i++) {
-                    acc_pre[j][i] = fmaf(v[i], u[i] * rstd_r, acc_pre[j][i]);
-                    q[j][i] += rstd_r * (v[i] * w[i]) - u[i] * back_r;
-                }
-            }
-            if (live && in[j]) a.dx[base + NT * j] = Chunk<E>::pack(q[j]);
-            if (!a.dy) continue;
-            Chunk<E>::unpack(yr[j], u);
-            Chunk<E>::unpack(wpost[j], v);
-            Chunk<E>::unpack(wgate[j], w);
+        const float to_y = a.scale * gt * rstd_y;
+        if (a.dh) {
 #pragma unroll
             for (int i = 0; i < N; i++) {
-                const float dz = a.scale * q[j][i];
-                const float yn = u[i] * rstd_y;
-                const float wp = a.w_post ? v[i] : 1.f;
-                const float g = gate_ch ? w[i] : gt;
-                acc_gate[j][i] = fmaf(dz, yn * wp, acc_gate[j][i]);
-                acc_post[j][i] = fmaf(dz * g, yn, acc_post[j][i]);
-                two[1] = fmaf(dz, yn * wp, two[1]);
-                q[j][i] = dz * g * wp;
-                two[0] = fmaf(q[j][i], u[i], two[0]);
+                acc_r[i] = fmaf(dh[i] * rstd_r, r[i], acc_r[i]);
+                q[i] += fmaf(rstd_r, w[i], -r[i] * back_r);
             }
         }
+        // q is dr', and then dr' gate_ch w_post
+        if (live && in) a.dx[at] = Chunk<E>::pack(q);
         if (!a.dy) continue;
+        float dot[1] = {0.f};  // (dr' gate_ch w_post).y
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            acc_y[i] = fmaf(q[i] * to_y, y[i], acc_y[i]);
+            q[i] *= gw[i];
+            dot[0] = fmaf(q[i], y[i], dot[0]);
+        }
         float back_y = 0.f;
         if (a.w_post || gate_tok) {
-            row_sums<NT>(two, slots, turn);
-            if (a.w_post) back_y = two[0] * a.inv_d * rstd_y * rstd_y * rstd_y;
-            if (gate_tok && live && lane == 0) a.dgate_tok[t] = two[1];
+            row_sums<NT>(dot, slots, turn);
+            if (a.w_post) back_y = dot[0] * to_y * a.inv_d * rstd_y * rstd_y;
+            if (gate_tok && live && c == 0) a.dgate_tok[t] = a.scale * rstd_y * dot[0];
         }
 #pragma unroll
-        for (int j = 0; j < VPT; j++) {
-            float u[N];
-            Chunk<E>::unpack(yr[j], u);
-#pragma unroll
-            for (int i = 0; i < N; i++) q[j][i] = rstd_y * q[j][i] - u[i] * back_y;
-            if (live && in[j]) a.dy[base + NT * j] = Chunk<E>::pack(q[j]);
-        }
+        for (int i = 0; i < N; i++) q[i] = fmaf(to_y, q[i], -y[i] * back_y);
+        if (live && in) a.dy[at] = Chunk<E>::pack(q);
     }
 
     // this workgroup's column sums, its rows' added in order
     const int d = a.chunks * N;
-    float *out = a.part + static_cast<size_t>(blockIdx.x) * 3 * d;
-    __shared__ float col[kRows > 1 ? kRows : 1][kRows > 1 ? NT * VPT * N : 1];
+    float *out = a.part + static_cast<size_t>(blockIdx.x) * 2 * d;
+    __shared__ float col[kRows][NT * N];
 #pragma unroll
-    for (int k = 0; k < 3; k++) {
+    for (int k = 0; k < 2; k++) {
         if (!a.want[k]) continue;
-        const auto &acc = k == 0 ? acc_post : k == 1 ? acc_gate : acc_pre;
-        if constexpr (kRows == 1) {
+        __syncthreads();  // the sums before these have been read
 #pragma unroll
-            for (int j = 0; j < VPT; j++)
+        for (int i = 0; i < N; i++) col[sub][c * N + i] = k ? acc_r[i] : acc_y[i];
+        __syncthreads();
+        for (int j = threadIdx.x; j < d; j += kBackBlock) {
+            float s = 0.f;
 #pragma unroll
-                for (int i = 0; i < N; i++)
-                    if (in[j]) out[k * d + (lane + NT * j) * N + i] = acc[j][i];
-        } else {
-            __syncthreads();  // the sums before these have been read
-#pragma unroll
-            for (int j = 0; j < VPT; j++)
-#pragma unroll
-                for (int i = 0; i < N; i++) col[sub][(lane + NT * j) * N + i] = acc[j][i];
-            __syncthreads();
-            for (int c = threadIdx.x; c < d; c += kBlock<NT>) {
-                float s = 0.f;
-#pragma unroll
-                for (int q = 0; q < kRows; q++) s += col[q][c];
-                out[k * d + c] = s;
-            }
+            for (int q = 0; q < kRows; q++) s += col[q][j];
+            out[k * d + j] = s;
         }
     }
 }
 
-// out[k][c] = sum over the workgroups' part[b][k][c], b ascending within each
-// of the 16 interleaved shares and the shares in order.
+// Column c's sums over the workgroups: each of 16 interleaved shares in
+// order, then the shares in order.  With S of dz n(y), dz without the channel
+// gate: dw_post = gate S, dgate = w_post S.
 constexpr int kFoldCols = 64, kFoldShares = 16;
+template <typename E>
 __global__ __launch_bounds__(kFoldCols *kFoldShares) void k_norm_fold(
-    const float *__restrict__ part, int blocks, int d, float *dw_post, float *dgate, float *dw_pre) {
-    __shared__ float s[kFoldShares][kFoldCols];
-    float *out = blockIdx.y == 0 ? dw_post : blockIdx.y == 1 ? dgate : dw_pre;
-    if (!out) return;
+    const float *__restrict__ part, int blocks, int d, const E *w_post, const E *gate_ch,
+    float *dw_post, float *dgate_ch, float *dw_pre) {
+    __shared__ float s_sum[kFoldShares][kFoldCols];
+    if (blockIdx.y ? !dw_pre : !dw_post && !dgate_ch) return;
     const int c = blockIdx.x * kFoldCols + threadIdx.x % kFoldCols, sh = threadIdx.x / kFoldCols;
     float v = 0.f;
     if (c < d)
 #pragma unroll 8
         for (int b = sh; b < blocks; b += kFoldShares)
-            v += part[(static_cast<size_t>(b) * 3 + blockIdx.y) * d + c];
-    s[sh][threadIdx.x % kFoldCols] = v;
+            v += part[(static_cast<size_t>(b) * 2 + blockIdx.y) * d + c];
+    s_sum[sh][threadIdx.x % kFoldCols] = v;
     __syncthreads();
     if (sh || c >= d) return;
-    for (int q = 1; q < kFoldShares; q++) v += s[q][threadIdx.x];
-    out[c] = v;
+    for (int q = 1; q < kFoldShares; q++) v += s_sum[q][threadIdx.x];
+    const auto value = [](E e) {
+        if constexpr (sizeof(E) == 2)
+            return bf16_bits_to_f32(e);
+        else
+            return e;
+    };
+    if (blockIdx.y) {
+        dw_pre[c] = v;
+        return;
+    }
+    if (dw_post) dw_post[c] = gate_ch ? value(gate_ch[c]) * v : v;
+    if (dgate_ch) dgate_ch[c] = w_post ? value(w_post[c]) * v : v;
 }
 
-// Threads that share a row of `chunks` chunks and chunks of each thread.
+// Forward: threads that share a row of `chunks` chunks and chunks of each.
 template <typename F>
 void by_width(int chunks, F f) {
     using std::integral_constant;
@@ -395,19 +371,32 @@ void by_width(int chunks, F f) {
         f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
 }
 
-// Rows that a workgroup takes at once: NT as chosen above.
-int rows_per_block(int nt) { return nt >= 256 ? 1 : 256 / nt; }
+// Backward: threads that share a row, one per chunk.
+template <typename F>
+void by_width_back(int chunks, F f) {
+    using std::integral_constant;
+    if (chunks <= 64)
+        f(integral_constant<int, 64>{});
+    else if (chunks <= 128)
+        f(integral_constant<int, 128>{});
+    else if (chunks <= 256)
+        f(integral_constant<int, 256>{});
+    else if (chunks <= 512)
+        f(integral_constant<int, 512>{});
+    else
+        f(integral_constant<int, 1024>{});
+}
 
 }  // namespace
 
-// Backward workgroups at most: two per CU, since each leaves 3 d fp32 sums
-// behind (one per CU: 52 us at T = 8192, d = 2048 against 46; four: 50).
-constexpr int kNormBackBlocks = 512;
+// Backward workgroups at most: one per CU, since each leaves 2 d fp32 sums
+// behind (T = 8192, d = 2048: 48 us a call; two per CU 54).
+constexpr int kNormBackBlocks = 256;
 
 int norm_back_blocks(int T, int chunks) {
-    int need = 0;
-    by_width(chunks, [&](auto nt, auto) { need = ceil_div(T, rows_per_block(nt)); });
-    return need < kNormBackBlocks ? need : kNormBackBlocks;
+    unsigned need = 0;
+    by_width_back(chunks, [&](auto nt) { need = ceil_div(T, kBackBlock / decltype(nt)::value); });
+    return static_cast<int>(std::min(need, static_cast<unsigned>(kNormBackBlocks)));
 }
 
 hipError_t launch_block_norm(const void *x, const void *y, const void *w_post, const void *gate,
@@ -430,7 +419,7 @@ hipError_t launch_block_norm(const void *x, const void *y, const void *w_post, c
     by_width(a.chunks, [&](auto nt, auto vpt) {
         constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
         // one row per team, up to the most threads that a launch holds
-        const unsigned grid = std::min(ceil_div(T, rows_per_block(NT)), 1u << 22);
+        const unsigned grid = std::min(ceil_div(T, kBlock<NT> / NT), 1u << 22);
         if (bf16)
             k_norm<uint16_t, NT, VPT><<<grid, kBlock<NT>, 0, s>>>(a);
         else
@@ -457,9 +446,8 @@ hipError_t launch_block_norm_back(const void *dr, const void *dh, const void *r,
     a.dy = static_cast<u32x4 *>(dy);
     a.dgate_tok = gate_kind == 2 ? dgate : nullptr;
     a.part = part;
-    a.want[0] = dw_post;
-    a.want[1] = gate_kind == 1;
-    a.want[2] = dw_pre;
+    a.want[0] = dw_post || gate_kind == 1;
+    a.want[1] = dw_pre;
     a.T = T;
     a.chunks = d / (bf16 ? 8 : 4);
     a.gate_kind = gate_kind;
@@ -467,17 +455,26 @@ hipError_t launch_block_norm_back(const void *dr, const void *dh, const void *r,
     a.eps = eps;
     a.scale = scale;
     const int grid = norm_back_blocks(T, a.chunks);
-    by_width(a.chunks, [&](auto nt, auto vpt) {
-        constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
+    by_width_back(a.chunks, [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
         if (bf16)
-            k_norm_back<uint16_t, NT, VPT><<<grid, kBlock<NT>, 0, s>>>(a);
+            k_norm_back<uint16_t, NT><<<grid, kBackBlock, 0, s>>>(a);
         else
-            k_norm_back<float, NT, VPT><<<grid, kBlock<NT>, 0, s>>>(a);
+            k_norm_back<float, NT><<<grid, kBackBlock, 0, s>>>(a);
     });
-    float *dgate_ch = gate_kind == 1 ? dgate : nullptr;
-    if (dw_post || dgate_ch || dw_pre)
-        k_norm_fold<<<dim3(ceil_div(d, kFoldCols), 3), kFoldCols * kFoldShares, 0, s>>>(
-            part, grid, d, dw_post, dgate_ch, dw_pre);
+    if (!a.want[0] && !a.want[1]) return hipGetLastError();
+    const dim3 fold(ceil_div(d, kFoldCols), 2);
+    const auto reduce = [&](auto e) {
+        typedef decltype(e) E;
+        k_norm_fold<E><<<fold, kFoldCols * kFoldShares, 0, s>>>(
+            part, grid, d, static_cast<const E *>(w_post),
+            gate_kind == 1 ? static_cast<const E *>(gate) : nullptr, dw_post,
+            gate_kind == 1 ? dgate : nullptr, dw_pre);
+    };
+    if (bf16)
+        reduce(uint16_t{});
+    else
+        reduce(float{});
     return hipGetLastError();
 }
 

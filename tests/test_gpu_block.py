@@ -763,7 +763,7 @@ def test_training_step_gradients_against_64_bits():
             0.1 * torch.logsumexp(logits[rows], 1).square().mean())
     names = list(v)
     grads = torch.autograd.grad(loss + (r * st.goal.double()).sum(), [x0] + [v[n] for n in names])
-    rel = lambda a, b: float((a.double() - b).norm() / b.norm())
+    rel = lambda a, b: float((a.double() - b.detach()).norm() / b.detach().norm())
     assert abs(float(st.loss[0]) - float(loss.detach())) <= 2e-2 * abs(float(loss.detach()))
     assert rel(st.r, r) <= 2e-2
     for got, want, name in zip([st.dx] + [st.grad[n] for n in names], grads, ["x"] + names):
