@@ -13,18 +13,21 @@
 // copy), 10 + 6 in 8 bits.  One launch takes up to kMaxTensors tensors, whose
 // table travels by value in the kernel's arguments (no device copy of it to
 // keep), and cuts them into pieces of kPiece elements; a workgroup finds its
-// tensor from its number and streams one piece with 16-byte accesses, four
+// tensor from its number and moves one piece with 16-byte accesses, four
 // elements per lane.  A wave's 64 lanes then hold the 256 elements of one
-// 8-bit block, whose largest magnitude is a wave maximum.
+// 8-bit block, whose largest magnitude is a wave maximum.  Every lane has all
+// its loads in flight at once and the workgroups cross the tensors in order:
+// pieces of 4 elements per lane measure 2105 us for 403 M elements in fp32
+// (5.7 TB/s), of 8 2297, of 16 2250, of 32 2319.  8 bits, 35 M elements:
+// 128 us (4.9 TB/s; with IEEE square roots and divisions 140); six small
+// tensors 4.4 us.
 #include "launch.h"
 
 namespace occ {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kStep = kThreads * 4;  // elements per pass of the workgroup
-constexpr int kPasses = 4;
-constexpr int kPiece = kStep * kPasses;
+constexpr int kPiece = kThreads * 4;  // elements of a workgroup
 constexpr int kMaxTensors = 30;
 constexpr uint64_t kMaxBlocks = 0xffffffffull / kThreads;  // a launch holds fewer than 2^32 threads
 static_assert(kAdamwMaxElements / kPiece < kMaxBlocks, "one tensor fits a launch");
@@ -81,22 +84,24 @@ __device__ __forceinline__ uint32_t to_e4m3(const float (&v)[4]) {
     return static_cast<uint32_t>(c);
 }
 
-// The wave's 256 values as codes, and their unit.  SQUARED: v holds sqrt(v),
-// whose nonzero values keep a nonzero code.
-template <bool SQUARED>
-__device__ __forceinline__ uint32_t quantise(const float (&v)[4], float &unit) {
+// The wave's 256 values as codes, and their unit.  keep[j]: a value that is
+// not zero keeps a code that is not.
+template <bool KEEP>
+__device__ __forceinline__ uint32_t quantise(const float (&v)[4], const float (&keep)[4],
+                                             float &unit) {
     const float top = wave_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])),
                                      fmaxf(fabsf(v[2]), fabsf(v[3]))));
     unit = 0.f;
     float c[4] = {0.f, 0.f, 0.f, 0.f};
     if (!(top < kSmallest)) {
         unit = top / kE4m3Max;
+        const float per = kE4m3Max / top;
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            c[j] = v[j] / unit;
+            c[j] = v[j] * per;
             // NaN (from a gradient that is not finite) passes both
             c[j] = c[j] > kE4m3Max ? kE4m3Max : c[j] < -kE4m3Max ? -kE4m3Max : c[j];
-            if (SQUARED && v[j] > 0.f && c[j] < kE4m3Min) c[j] = kE4m3Min;
+            if (KEEP && keep[j] > 0.f && c[j] < kE4m3Min) c[j] = kE4m3Min;
         }
     }
     return to_e4m3(c);
@@ -124,74 +129,72 @@ __global__ __launch_bounds__(kThreads) void k_adamw(Table tab, AdamwStep st) {
         c2_rsqrt = 1.f / sqrtf(-expm1f(step * st.log_b2));
     }
     const float decay = fmaf(-lr, st.weight_decay, 1.f), rate = lr / c1;
+    const int64_t i = i0 + threadIdx.x * 4;
+    // a wave whose elements all lie behind the tensor's end has nothing to do
+    if (i0 + (threadIdx.x & ~(kWave - 1)) * 4 >= n) return;
+    const bool whole = T.aligned && i + 4 <= n;
+    float p[4], g[4], m[4], v[4];
+    load4<f32x4, float>(T.p, i, n, whole, p);
+    if constexpr (GBF16) {
+        typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+        uint16_t gb[4];
+        load4<u16x4, uint16_t>(T.g, i, n, whole, gb);
 #pragma unroll
-    for (int u = 0; u < kPasses; u++) {
-        const int64_t i = i0 + u * kStep + threadIdx.x * 4;
-        // a wave whose elements all lie behind the tensor's end has nothing to do
-        if (i0 + u * kStep + (threadIdx.x & ~(kWave - 1)) * 4 >= n) break;
-        const bool whole = T.aligned && i + 4 <= n;
-        float p[4], g[4], m[4], v[4];
-        load4<f32x4, float>(T.p, i, n, whole, p);
-        if constexpr (GBF16) {
-            typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
-            uint16_t gb[4];
-            load4<u16x4, uint16_t>(T.g, i, n, whole, gb);
+        for (int j = 0; j < 4; j++) g[j] = bf16_bits_to_f32(gb[j]);
+    } else {
+        load4<f32x4, float>(T.g, i, n, whole, g);
+    }
+    const int64_t qb = i / kQBlock;
+    if constexpr (Q8) {
+        typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
+        uint8_t mc[4], vc[4];
+        load4<u8x4, uint8_t>(T.m, i, n, whole, mc);
+        load4<u8x4, uint8_t>(T.v, i, n, whole, vc);
+        // a lane behind the end holds zeros; its block exists (the wave's first lane's does)
+        from_e4m3(mc[0] | mc[1] << 8 | mc[2] << 16 | static_cast<uint32_t>(mc[3]) << 24,
+                  T.m_scale[qb], m);
+        from_e4m3(vc[0] | vc[1] << 8 | vc[2] << 16 | static_cast<uint32_t>(vc[3]) << 24,
+                  T.v_scale[qb], v);
 #pragma unroll
-            for (int j = 0; j < 4; j++) g[j] = bf16_bits_to_f32(gb[j]);
-        } else {
-            load4<f32x4, float>(T.g, i, n, whole, g);
-        }
-        const int64_t qb = i / kQBlock;
-        if constexpr (Q8) {
-            typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
-            uint8_t mc[4], vc[4];
-            load4<u8x4, uint8_t>(T.m, i, n, whole, mc);
-            load4<u8x4, uint8_t>(T.v, i, n, whole, vc);
-            // a lane behind the end holds zeros; its block exists (the wave's first lane's does)
-            from_e4m3(mc[0] | mc[1] << 8 | mc[2] << 16 | static_cast<uint32_t>(mc[3]) << 24,
-                      T.m_scale[qb], m);
-            from_e4m3(vc[0] | vc[1] << 8 | vc[2] << 16 | static_cast<uint32_t>(vc[3]) << 24,
-                      T.v_scale[qb], v);
+        for (int j = 0; j < 4; j++) v[j] *= v[j];
+    } else {
+        load4<f32x4, float>(T.m, i, n, whole, m);
+        load4<f32x4, float>(T.v, i, n, whole, v);
+    }
+    float root[4];
+    uint16_t copy[4];
 #pragma unroll
-            for (int j = 0; j < 4; j++) v[j] *= v[j];
-        } else {
-            load4<f32x4, float>(T.m, i, n, whole, m);
-            load4<f32x4, float>(T.v, i, n, whole, v);
+    for (int j = 0; j < 4; j++) {
+        const float gj = g[j] * gs;
+        m[j] = fmaf(st.beta1, m[j], st.one_b1 * gj);
+        v[j] = fmaf(st.beta2, v[j], st.one_b2 * gj * gj);
+        // hardware square root and reciprocal: 2^-23 relative of the step each
+        root[j] = __builtin_amdgcn_sqrtf(v[j]);
+        p[j] = fmaf(decay, p[j], -rate * (m[j] * __builtin_amdgcn_rcpf(fmaf(root[j], c2_rsqrt, st.eps))));
+        copy[j] = f32_to_bf16_bits(p[j]);
+    }
+    store4<f32x4, float>(T.p_out, i, n, whole, p);
+    if (T.p_bf16) {
+        typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+        store4<u16x4, uint16_t>(T.p_bf16, i, n, whole, copy);
+    }
+    if constexpr (Q8) {
+        typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
+        float um, uv;
+        const uint32_t qm = quantise<false>(m, m, um), qv = quantise<true>(root, v, uv);
+        const uint8_t mc[4] = {static_cast<uint8_t>(qm), static_cast<uint8_t>(qm >> 8),
+                               static_cast<uint8_t>(qm >> 16), static_cast<uint8_t>(qm >> 24)};
+        const uint8_t vc[4] = {static_cast<uint8_t>(qv), static_cast<uint8_t>(qv >> 8),
+                               static_cast<uint8_t>(qv >> 16), static_cast<uint8_t>(qv >> 24)};
+        store4<u8x4, uint8_t>(T.m_out, i, n, whole, mc);
+        store4<u8x4, uint8_t>(T.v_out, i, n, whole, vc);
+        if (lane_id() == 0) {
+            T.m_scale_out[qb] = um;
+            T.v_scale_out[qb] = uv;
         }
-        float root[4];
-        uint16_t copy[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float gj = g[j] * gs;
-            m[j] = fmaf(st.beta1, m[j], st.one_b1 * gj);
-            v[j] = fmaf(st.beta2, v[j], st.one_b2 * gj * gj);
-            root[j] = sqrtf(v[j]);
-            p[j] = fmaf(decay, p[j], -rate * (m[j] / fmaf(root[j], c2_rsqrt, st.eps)));
-            copy[j] = f32_to_bf16_bits(p[j]);
-        }
-        store4<f32x4, float>(T.p_out, i, n, whole, p);
-        if (T.p_bf16) {
-            typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
-            store4<u16x4, uint16_t>(T.p_bf16, i, n, whole, copy);
-        }
-        if constexpr (Q8) {
-            typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
-            float um, uv;
-            const uint32_t qm = quantise<false>(m, um), qv = quantise<true>(root, uv);
-            const uint8_t mc[4] = {static_cast<uint8_t>(qm), static_cast<uint8_t>(qm >> 8),
-                                   static_cast<uint8_t>(qm >> 16), static_cast<uint8_t>(qm >> 24)};
-            const uint8_t vc[4] = {static_cast<uint8_t>(qv), static_cast<uint8_t>(qv >> 8),
-                                   static_cast<uint8_t>(qv >> 16), static_cast<uint8_t>(qv >> 24)};
-            store4<u8x4, uint8_t>(T.m_out, i, n, whole, mc);
-            store4<u8x4, uint8_t>(T.v_out, i, n, whole, vc);
-            if (lane_id() == 0) {
-                T.m_scale_out[qb] = um;
-                T.v_scale_out[qb] = uv;
-            }
-        } else {
-            store4<f32x4, float>(T.m_out, i, n, whole, m);
-            store4<f32x4, float>(T.v_out, i, n, whole, v);
-        }
+    } else {
+        store4<f32x4, float>(T.m_out, i, n, whole, m);
+        store4<f32x4, float>(T.v_out, i, n, whole, v);
     }
 }
 

@@ -264,7 +264,7 @@ hipError_t launch_gate_dw(const float *dl, const void *x, int T, int d, int Ne, 
                           float *part, float *dw, hipStream_t s);
 
 // --- optimizer step (adamw.hip) ---
-constexpr int64_t kAdamwMaxElements = 1ll << 35;  // of one tensor
+constexpr int64_t kAdamwMaxElements = 1ll << 33;  // of one tensor
 struct AdamwTensor {
     int64_t n;
     const float *p;

@@ -605,7 +605,7 @@ typedef struct occ_adamw_tensor {
  * states its whole block's); tensors aligned to 16 bytes are faster.
  * Errors: INVALID_ARG (a value out of the ranges above, a missing or
  * superfluous pointer, an array not aligned to its elements), UNSUPPORTED
- * (n > 2^35). */
+ * (n > 2^33). */
 occ_status occ_adamw_step(const occ_adamw_desc *opt, const occ_adamw_tensor *tensors_host,
                           int32_t count, const float *dynamic, void *stream);
 
