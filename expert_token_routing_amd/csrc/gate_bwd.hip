@@ -30,9 +30,12 @@
 // 95 us (5.8 TB/s of 553 MB), 174 us as one call (4.7 TB/s of its 822 MB; one
 // bf16 term in place of three leaves the call as it is: the memory bounds
 // it); Ne = 64, T = 8192: 17 + 4.5 and 17 us.
-// fp32: v_mfma_f32_16x16x4_f32 on the operands as they lie (one value per
-// lane and step), exact products.
+//   k_gate_dx_tile   dx with more than 64 experts, through LDS; 130 experts,
+//               T = 8192, d = 2048: 25.7 us (68 MB: 11 at 6 TB/s).
+// fp32: v_mfma_f32_16x16x4_f32, exact products, in k_gate_dx_tile (T = 4096,
+// d = 2048, 64 experts: 20 us for 68 MB) and k_gate_dw_f32 (24 us).
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 
@@ -40,10 +43,12 @@ namespace occ {
 namespace {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef __attribute__((ext_vector_type(2))) unsigned int u32x2;
+typedef f32x4 f32x4_unaligned __attribute__((aligned(4)));  // the hardware takes dword alignment
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kDxCols = 64;     // columns of a wave in k_gate_dx_f32
+constexpr int kDxCols = 128;    // columns of a wave in k_gate_dx
 constexpr int kDwThreads = 512; // k_gate_dw
 constexpr int kDwCols = 256;    // columns of a workgroup in k_gate_dw
 constexpr int kDwColsF = 64;    // in k_gate_dw_f32
@@ -51,13 +56,17 @@ constexpr int kDwExperts = 64;  // experts of a workgroup in either
 
 // Workgroup b runs on XCD b mod 8, each with an L2 of its own.  A token range
 // meets every column group, so its groups get numbers that share an XCD: the
-// range's dlogits are fetched into one L2 instead of eight.
-__device__ __forceinline__ void share_of(int groups, int &group, unsigned &share) {
-    const unsigned r = blockIdx.x >> 3;
+// range's dlogits are fetched into one L2 instead of eight.  Fewer ranges
+// than XCDs spread their groups over all of them instead.
+__device__ __forceinline__ bool share_of(int groups, unsigned shares, int &group, unsigned &share) {
+    const unsigned r = shares < 8 ? blockIdx.x : blockIdx.x >> 3;
     group = static_cast<int>(r % groups);
-    share = r / groups * 8 + (blockIdx.x & 7);
+    share = shares < 8 ? r / groups : r / groups * 8 + (blockIdx.x & 7);
+    return share < shares;
 }
-unsigned share_grid(int groups, unsigned shares) { return groups * ceil_div(shares, 8) * 8; }
+unsigned share_grid(int groups, unsigned shares) {
+    return groups * (shares < 8 ? shares : ceil_div(shares, 8) * 8);
+}
 
 // Two values as bf16, the first in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -114,21 +123,21 @@ __device__ __forceinline__ void transpose8(const V (&r)[8], bf16x8_t (&out)[NI])
     }
 }
 
-// KS: 32-deep steps over the experts; NI: 16-column fragments of a wave, 8 or
-// 4.  Waves are independent (no barrier).
-template <int KS, int NI, bool VEC>
+// KS: 32-deep steps over the experts.  Waves are independent (no barrier).
+template <int KS, bool VEC>
 __global__ __launch_bounds__(kThreads) void k_gate_dx(const float *__restrict__ dl,
                                                       const uint16_t *__restrict__ wr,
                                                       const uint16_t *dx_in, uint16_t *dx,
                                                       unsigned T, int d, int Ne, int groups,
                                                       unsigned shares) {
-    typedef __attribute__((ext_vector_type(NI / 2))) unsigned int Cols;  // NI columns
+    constexpr int NI = kDxCols / 16;  // 16-column fragments
+    typedef u32x4 Cols;               // NI columns
     const int l = lane_id(), i16 = l & 15, G = l >> 4;
     int group;
     unsigned tile;
-    share_of(groups, group, tile);
+    if (!share_of(groups, shares, group, tile)) return;
     const int c0 = (group * kWaves + threadIdx.x / kWave) * (16 * NI);
-    if (c0 >= d || tile >= shares) return;
+    if (c0 >= d) return;
     bf16x8_t w[KS][NI];
     // column i of fragment ni is NI i + ni
     const int cw = c0 + NI * i16;
@@ -226,8 +235,8 @@ __global__ __launch_bounds__(kThreads) void k_gate_dx(const float *__restrict__ 
 template <int MB>
 __global__ __launch_bounds__(kDwThreads) void k_gate_dw(const float *__restrict__ dl,
                                                         const uint16_t *__restrict__ x, unsigned T,
-                                                        int d, int Ne, int groups, unsigned shares,
-                                                        unsigned per_share,
+                                                        int d, int Ne, int groups, int col_groups,
+                                                        unsigned shares, unsigned per_share,
                                                         float *__restrict__ part) {
     typedef bf16x8_t Terms[2][2][MB][3][kWave];  // [buffer][half][expert block][term][lane]
     typedef f32x4 Sums[4][MB * 4][kWave];
@@ -238,9 +247,8 @@ __global__ __launch_bounds__(kDwThreads) void k_gate_dw(const float *__restrict_
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), half = wv >> 2, cg = wv & 3;
     int group;
     unsigned share;
-    share_of(groups, group, share);
-    if (share >= shares) return;
-    const int c0 = group * kDwCols + 64 * cg, e0 = blockIdx.y * kDwExperts;
+    if (!share_of(groups, shares, group, share)) return;
+    const int c0 = group % col_groups * kDwCols + 64 * cg, e0 = group / col_groups * kDwExperts;
     const bool col_in = c0 < d;  // d is a multiple of 64
     const unsigned t0 = share * per_share, t1 = min(T, t0 + per_share);
     f32x4 acc[MB][4];
@@ -250,7 +258,6 @@ __global__ __launch_bounds__(kDwThreads) void k_gate_dw(const float *__restrict_
         for (int q = 0; q < 4; q++) acc[m][q] = f32x4{0.f, 0.f, 0.f, 0.f};
     // Step n's 8 tokens of this lane: 4 columns of x, and the dlogits of one
     // expert (behind Ne the last one's again, whose sums are not stored)
-    typedef __attribute__((ext_vector_type(2))) unsigned int u32x2;
     const unsigned rows = min(T, 64u), last = T - rows;
     unsigned at_x[8], at_e[8];
 #pragma unroll
@@ -340,94 +347,279 @@ __global__ __launch_bounds__(kDwThreads) void k_gate_dw(const float *__restrict_
     }
 }
 
-// fp32: a wave makes 64 tokens x 64 columns of dx, contracting 4 experts per
-// step; the product is transposed and its columns mapped as in k_gate_dx.
-__global__ __launch_bounds__(kThreads) void k_gate_dx_f32(const float *__restrict__ dl,
-                                                          const float *__restrict__ wr,
-                                                          const float *dx_in, float *dx,
-                                                          unsigned T, int d, int Ne) {
-    const int l = lane_id(), i16 = l & 15, G = l >> 4;
-    const int c0 = (blockIdx.x * kWaves + threadIdx.x / kWave) * kDxCols;
-    if (c0 >= d) return;
-    for (unsigned t0 = blockIdx.y * 64; t0 < T; t0 += gridDim.y * 64) {
-        f32x4 acc[4][4];  // [token block][ni]
+// dx for every fp32 shape and for bf16 with more than 64 experts: tiles of
+// 32 MB tokens x 64 WN columns by 2 WN waves (128 x 256 or 64 x 128), the
+// experts contracted in steps of kDepth through LDS (two buffers; the next
+// step's operands are in flight in registers).  Wave (wm, wn) of 2 x WN makes
+// 16 MB tokens x 64 columns; column 4 i + ni of those is column i of fragment
+// ni, so that a lane ends with 4 consecutive columns.
+// bf16: 32 experts a step; dlogits are split into their two terms on the way
+// into LDS and W_r's columns transposed in registers, both stored as the
+// 16-byte operands (8 consecutive experts) that a lane feeds to the MFMA.
+// fp32: 16 experts a step; a lane's operand of MFMA s is expert 4 (lane / 16)
+// + s, so that one 16-byte read of a token's dlogits feeds four MFMAs.
+template <typename E, int MB, int WN>
+struct DxTile;
+template <int MB, int WN>
+struct DxTile<uint16_t, MB, WN> {
+    static constexpr int kDepth = 32;
+    // 16-byte operands: dlogits [term][expert / 8][token], W_r [expert / 8][column]
+    bf16x8_t a[2][4][32 * MB], b[4][64 * WN];
+    struct Next {
+        float dl[8];
+        u32x2 w[8];
+    };
+};
+template <int MB, int WN>
+struct DxTile<float, MB, WN> {
+    static constexpr int kDepth = 16;
+    f32x4 a[4][32 * MB];       // [expert / 4][token]
+    float b[16][64 * WN + 4];  // padded: a lane's four reads of 16 columns miss each other's banks
+    struct Next {
+        f32x4 dl, w[2];
+    };
+};
+
+// One workgroup per tile.  Without SMALL there are a tile's tokens and a
+// step's experts at least: a tile (a step) that would reach past the last
+// token (expert) starts early enough not to, and leaves out what others do.
+// SMALL takes the rest, with clamped addresses.
+template <typename E, int MB, int WN, bool SMALL>
+__global__ __launch_bounds__(2 * WN *kWave, 4) void k_gate_dx_tile(
+    const float *__restrict__ dl, const E *__restrict__ wr, const E *dx_in, E *dx, unsigned T,
+    int d, int Ne, int groups, unsigned tiles) {
+    typedef DxTile<E, MB, WN> Tile;
+    constexpr int kTokens = 32 * MB, kDepth = Tile::kDepth, kOwn = kDepth / 4;
+    constexpr bool kBf16 = sizeof(E) == 2;
+    __shared__ Tile lds[2];
+    int group;
+    unsigned tile;
+    if (!share_of(groups, tiles, group, tile)) return;
+    const int tid = threadIdx.x, l = lane_id(), i16 = l & 15, G = l >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(tid / kWave), wm = wv / WN, wn = wv % WN;
+    const int c0 = group * 64 * WN;
+    const unsigned first = tile * kTokens, t0 = SMALL ? first : min(first, T - kTokens);
+
+    // This thread's share of a step: dlogits of one token, kOwn consecutive
+    // experts, and W_r: 16 WN lanes hold 4 columns each of a row; bf16 8 rows
+    // of one operand (the first waves alone), fp32 two rows.
+    constexpr int kRowLanes = 16 * WN, kRowsAtOnce = kWave / kRowLanes;
+    const int a_tok = tid / 4, a_k = tid % 4 * kOwn;
+    const unsigned a_at = 4 * (a_tok * Ne + a_k);
+    const int w_sub = l / kRowLanes, w_col = l % kRowLanes * 4;
+    const int w_rows = kBf16 ? 8 : 1;  // consecutive rows of a lane
+    const unsigned w_at = sizeof(E) * (w_sub * w_rows * d + min(c0 + w_col, d - 4));
+    const float *dl0 = dl + static_cast<size_t>(t0) * Ne;
+    typename Tile::Next next;
+    // first expert of a step's operands
+    auto start = [&](int e0) { return __builtin_amdgcn_readfirstlane(SMALL ? e0 : min(e0, Ne - kDepth)); };
+    auto weights = [&](int row) {  // row: the first of the kRowsAtOnce rows, or operands of rows
+        if constexpr (SMALL) {
+            const int own = min(row + w_sub * w_rows, Ne - 1);
+            return wr + static_cast<size_t>(own) * d + min(c0 + w_col, d - 4);
+        } else {
+            return reinterpret_cast<const E *>(
+                reinterpret_cast<const char *>(wr + static_cast<size_t>(row) * d) + w_at);
+        }
+    };
+    auto load = [&](int e0) {
+        const int e = start(e0);
+        if constexpr (SMALL) {
+            const float *row = dl + static_cast<size_t>(min(t0 + a_tok, T - 1)) * Ne;
 #pragma unroll
-        for (int m = 0; m < 4; m++)
+            for (int j = 0; j < kOwn; j++) next.dl[j] = row[min(e + a_k + j, Ne - 1)];
+        } else {
+#pragma unroll
+            for (int j = 0; j < kOwn; j += 4) {
+                const f32x4 v = load_at<f32x4_unaligned>(dl0 + e + j, a_at);
+#pragma unroll
+                for (int q = 0; q < 4; q++) next.dl[j + q] = v[q];
+            }
+        }
+        if constexpr (kBf16) {
+            if (wv * kRowsAtOnce < 4) {
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    next.w[j] = *reinterpret_cast<const u32x2 *>(
+                        weights(e + 8 * kRowsAtOnce * wv + j));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+                next.w[j] = *reinterpret_cast<const f32x4 *>(weights(e + (2 * wv + j) * kRowsAtOnce));
+        }
+    };
+    auto store = [&](int e0, Tile &to) {
+        // experts of another step, and behind the last, have zero dlogits
+        const int e = start(e0);
+        float v[kOwn];
+#pragma unroll
+        for (int j = 0; j < kOwn; j++) {
+            const int ej = e + a_k + j;
+            v[j] = ej >= e0 && ej < Ne ? next.dl[j] : 0.f;
+        }
+        if constexpr (kBf16) {
+            bf16x8_t terms[2];
+            split_terms<2>(v, terms);
+            to.a[0][tid % 4][a_tok] = terms[0];
+            to.a[1][tid % 4][a_tok] = terms[1];
+            if (wv * kRowsAtOnce < 4) {
+                bf16x8_t b[4];
+                transpose8<4>(next.w, b);
+#pragma unroll
+                for (int q = 0; q < 4; q++) to.b[wv * kRowsAtOnce + w_sub][w_col + q] = b[q];
+            }
+        } else {
+            to.a[tid % 4][a_tok] = f32x4{v[0], v[1], v[2], v[3]};
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+                *reinterpret_cast<f32x4 *>(&to.b[(2 * wv + j) * kRowsAtOnce + w_sub][w_col]) = next.w[j];
+        }
+    };
+
+    // This lane's outputs: tokens t0 + own + 16 m + v, columns c .. c + 3.
+    typedef typename std::conditional<kBf16, u32x2, f32x4>::type Cols;
+    const int c = c0 + 64 * wn + 4 * i16, own = 16 * MB * wm + 4 * G;
+    const unsigned o_at = sizeof(E) * (own * d + min(c, d - 4));
+    load(0);
+    // sums start from dx_in
+    f32x4 acc[MB][4];  // [16 tokens][ni]
+    if (dx_in) {
+        const E *from = dx_in + static_cast<size_t>(t0) * d;
+#pragma unroll
+        for (int m = 0; m < MB; m++)
+#pragma unroll
+            for (int v = 0; v < 4; v++) {
+                Cols in = {};
+                if (!SMALL || t0 + own + 16 * m + v < T)
+                    in = load_at<Cols>(from + (16 * m + v) * d, o_at);
+                if constexpr (kBf16) {
+                    acc[m][0][v] = low_bf16(in[0]);
+                    acc[m][1][v] = high_bf16(in[0]);
+                    acc[m][2][v] = low_bf16(in[1]);
+                    acc[m][3][v] = high_bf16(in[1]);
+                } else {
+#pragma unroll
+                    for (int ni = 0; ni < 4; ni++) acc[m][ni][v] = in[ni];
+                }
+            }
+    } else {
+#pragma unroll
+        for (int m = 0; m < MB; m++)
 #pragma unroll
             for (int ni = 0; ni < 4; ni++) acc[m][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int e0 = 0; e0 < Ne; e0 += 4) {
-            const int e = e0 + G;
-            float a[4], w[4];
+    }
+    int buf = 0;
+    for (int e0 = 0; e0 < Ne; e0 += kDepth, buf ^= 1) {
+        Tile &at = lds[buf];
+        store(e0, at);
+        if (e0 + kDepth < Ne) load(e0 + kDepth);
+        // the other buffer's readers have passed the barrier before this one
+        __syncthreads();
+        if constexpr (kBf16) {
+            bf16x8_t b[4];
 #pragma unroll
-            for (int m = 0; m < 4; m++)
-                a[m] = e < Ne ? dl[static_cast<size_t>(min(t0 + 16 * m + i16, T - 1)) * Ne + e] : 0.f;
+            for (int ni = 0; ni < 4; ni++) b[ni] = at.b[G][64 * wn + 4 * i16 + ni];
 #pragma unroll
-            for (int ni = 0; ni < 4; ni++) {
-                const int c = c0 + 16 * (i16 >> 2) + 4 * ni + (i16 & 3);
-                w[ni] = e < Ne && c < d ? wr[static_cast<size_t>(e) * d + c] : 0.f;
-            }
+            for (int m = 0; m < MB; m++)
 #pragma unroll
-            for (int m = 0; m < 4; m++)
+                for (int q = 0; q < 2; q++) {
+                    const bf16x8_t a = at.a[q][G][16 * MB * wm + 16 * m + i16];
 #pragma unroll
-                for (int ni = 0; ni < 4; ni++)
-                    acc[m][ni] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[ni], a[m], acc[m][ni], 0, 0, 0);
-        }
-        if (c0 + 16 * G >= d) continue;  // d is a multiple of 16
+                    for (int ni = 0; ni < 4; ni++)
+                        acc[m][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[ni], acc[m][ni], 0, 0, 0);
+                }
+        } else {
+            f32x4 a[MB];
 #pragma unroll
-        for (int m = 0; m < 4; m++) {
-            const unsigned t = t0 + 16 * m + i16;
-            if (t >= T) continue;
-            const size_t at = static_cast<size_t>(t) * d + c0 + 16 * G;
+            for (int m = 0; m < MB; m++) a[m] = at.a[G][16 * MB * wm + 16 * m + i16];
 #pragma unroll
-            for (int ni = 0; ni < 4; ni++) {
-                f32x4 v = acc[m][ni];
-                if (dx_in) v += *reinterpret_cast<const f32x4 *>(dx_in + at + 4 * ni);
-                *reinterpret_cast<f32x4 *>(dx + at + 4 * ni) = v;
+            for (int q = 0; q < 4; q++) {  // expert 4 G + q
+                const f32x4 b = *reinterpret_cast<const f32x4 *>(&at.b[4 * G + q][64 * wn + 4 * i16]);
+#pragma unroll
+                for (int m = 0; m < MB; m++)
+#pragma unroll
+                    for (int ni = 0; ni < 4; ni++)
+                        acc[m][ni] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m][q], b[ni], acc[m][ni], 0, 0, 0);
             }
         }
     }
+    if (c >= d) return;
+    E *to = dx + static_cast<size_t>(t0) * d;
+#pragma unroll
+    for (int m = 0; m < MB; m++)
+#pragma unroll
+        for (int v = 0; v < 4; v++) {
+            Cols o;
+            if constexpr (kBf16)
+                o = Cols{pack_bf16(acc[m][0][v], acc[m][1][v]), pack_bf16(acc[m][2][v], acc[m][3][v])};
+            else
+                o = Cols{acc[m][0][v], acc[m][1][v], acc[m][2][v], acc[m][3][v]};
+            const unsigned t = t0 + own + 16 * m + v;
+            if (t >= first && t < T)
+                *reinterpret_cast<Cols *>(reinterpret_cast<char *>(to + (16 * m + v) * d) + o_at) = o;
+        }
 }
 
 // fp32: a wave makes 64 experts x 64 columns of dW_r from a quarter of the
-// workgroup's tokens, 8 at a time.
+// workgroup's tokens, 16 per step.  Expert 4 i + m is row i of block m and
+// column 4 i + q column i of block q, so that a lane's operands of 16 MFMAs
+// are one 16-byte piece of a token's dlogits and one of its x.  What lies
+// behind a token's last expert is read with it (its sums are not stored),
+// except near the end of the array.
 __global__ __launch_bounds__(kThreads) void k_gate_dw_f32(const float *__restrict__ dl,
                                                           const float *__restrict__ x, unsigned T,
-                                                          int d, int Ne, unsigned per_share,
+                                                          int d, int Ne, int groups, int col_groups,
+                                                          unsigned shares, unsigned per_share,
                                                           float *__restrict__ part) {
     __shared__ f32x4 s_acc[kWaves / 2][16][kWave];
-    const int l = lane_id(), i16 = l & 15, G = l >> 4, wv = threadIdx.x / kWave;
-    const int c0 = blockIdx.x * kDwColsF, e0 = blockIdx.y * kDwExperts;
-    const unsigned t0 = blockIdx.z * per_share, t1 = min(T, t0 + per_share);
-    f32x4 acc[4][4];  // [expert block][column block]
+    int group;
+    unsigned share;
+    if (!share_of(groups, shares, group, share)) return;
+    const int l = lane_id(), i16 = l & 15, G = l >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int c0 = group % col_groups * kDwColsF, e0 = group / col_groups * kDwExperts;
+    const unsigned t0 = share * per_share, t1 = min(T, t0 + per_share);
+    const int col = min(c0 + 4 * i16, d - 4), exp = min(e0 + 4 * i16, Ne - 1);
+    f32x4 acc[4][4];  // [m][q]
 #pragma unroll
     for (int m = 0; m < 4; m++)
 #pragma unroll
         for (int q = 0; q < 4; q++) acc[m][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // two steps of 4 tokens at a time, their loads first
-    for (unsigned tt = t0 + 8 * wv; tt < t1; tt += 8 * kWaves) {
-        float a[2][4], b[2][4];
+    f32x4 an[4], bn[4];  // the next step's tokens t + 4 u + G
+    auto load = [&](unsigned t) {
+        // 3 values behind a row lie in the next three at most
+        const bool inside = t + 16 + 3 <= T;
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-            const unsigned t = tt + 4 * u + G;
+        for (int u = 0; u < 4; u++) {
+            const size_t tu = min(t + 4 * u + G, T - 1);
+            const float *row = dl + tu * Ne;
+            if (inside) {
+                an[u] = *reinterpret_cast<const f32x4_unaligned *>(row + exp);
+            } else {
 #pragma unroll
-            for (int m = 0; m < 4; m++) {
-                const int e = e0 + 16 * m + i16;
-                a[u][m] = t < t1 && e < Ne ? dl[static_cast<size_t>(t) * Ne + e] : 0.f;
+                for (int m = 0; m < 4; m++) an[u][m] = row[min(exp + m, Ne - 1)];
             }
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const int c = c0 + 16 * q + i16;
-                b[u][q] = t < t1 && c < d ? x[static_cast<size_t>(t) * d + c] : 0.f;
-            }
+            bn[u] = *reinterpret_cast<const f32x4 *>(x + tu * d + col);
         }
+    };
+    load(t0 + 16 * wv);
+    for (unsigned t = t0 + 16 * wv; t < t1; t += 16 * kWaves) {
+        f32x4 a[4], b[4];
 #pragma unroll
-        for (int u = 0; u < 2; u++)
+        for (int u = 0; u < 4; u++) {
+            // tokens behind the share count nothing
+            a[u] = t + 4 * u + G < t1 ? an[u] : f32x4{0.f, 0.f, 0.f, 0.f};
+            b[u] = bn[u];
+        }
+        load(t + 16 * kWaves);
+#pragma unroll
+        for (int u = 0; u < 4; u++)
 #pragma unroll
             for (int m = 0; m < 4; m++)
 #pragma unroll
                 for (int q = 0; q < 4; q++)
-                    acc[m][q] =
-                        __builtin_amdgcn_mfma_f32_16x16x4f32(a[u][m], b[u][q], acc[m][q], 0, 0, 0);
+                    acc[m][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[u][m], b[u][q], acc[m][q], 0, 0, 0);
     }
 #pragma unroll
     for (int half = kWaves / 2; half > 0; half >>= 1) {
@@ -444,17 +636,18 @@ __global__ __launch_bounds__(kThreads) void k_gate_dw_f32(const float *__restric
                 for (int q = 0; q < 4; q++) acc[m][q] += s_acc[wv][m * 4 + q][l];
         __syncthreads();
     }
-    if (wv) return;
-    float *out = part + static_cast<size_t>(blockIdx.z) * Ne * d;
+    if (wv || c0 + 4 * i16 >= d) return;
+    // lane: experts e0 + 4 (4 G + v) + m, columns c0 + 4 i16 + q
+    float *out = part + static_cast<size_t>(share) * Ne * d;
 #pragma unroll
     for (int m = 0; m < 4; m++)
 #pragma unroll
-        for (int v = 0; v < 4; v++)
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const int e = e0 + 16 * m + 4 * G + v, c = c0 + 16 * q + i16;
-                if (e < Ne && c < d) out[static_cast<size_t>(e) * d + c] = acc[m][q][v];
-            }
+        for (int v = 0; v < 4; v++) {
+            const int e = e0 + 16 * G + 4 * v + m;
+            if (e < Ne)
+                *reinterpret_cast<f32x4 *>(out + static_cast<size_t>(e) * d + col) =
+                    f32x4{acc[m][0][v], acc[m][1][v], acc[m][2][v], acc[m][3][v]};
+        }
 }
 
 // dw = the sum of the token shares' partial sums: thread (i, q) adds shares q,
@@ -481,46 +674,63 @@ __global__ __launch_bounds__(kThreads) void k_gate_dw_fold(const f32x4 *__restri
 }  // namespace
 
 // Token shares of dW_r, from the shape alone, so that sums do not depend on
-// the device's state: enough for one workgroup per CU, of one step each at
-// least (64 tokens, 32 in fp32).  A share costs Ne x d fp32 written and read.
+// the device's state: enough for one workgroup per CU (two in fp32, of half
+// the waves: T = 4096, d = 2048, 64 experts 20 us against 24, four 27), of two
+// steps each at least (128 tokens).  A share costs Ne x d fp32 written and
+// read.
 int gate_dw_shares(int T, int d, int Ne, int bf16) {
     const unsigned cols = ceil_div(d, bf16 ? kDwCols : kDwColsF);
-    const unsigned want = ceil_div(256, cols * ceil_div(Ne, kDwExperts));
-    return static_cast<int>(std::min(want, ceil_div(T, bf16 ? 64 : 32)));
+    const unsigned want = ceil_div(bf16 ? 256 : 512, cols * ceil_div(Ne, kDwExperts));
+    return static_cast<int>(std::min(want, ceil_div(T, 128)));
 }
 
 hipError_t launch_gate_dx(const float *dl, const void *w_router, const void *dx_in, int T, int d,
                           int Ne, int bf16, void *dx, hipStream_t s) {
-    if (!bf16) {
-        k_gate_dx_f32<<<dim3(ceil_div(d, kWaves * kDxCols), std::min(ceil_div(T, 64), 4096u)), kThreads,
-                        0, s>>>(dl, static_cast<const float *>(w_router),
-                                static_cast<const float *>(dx_in), static_cast<float *>(dx), T, d, Ne);
+    // bf16: the register kernel holds up to 64 experts' weights; with more,
+    // tiles, large ones where there is one for every CU (130 experts, d = 2048:
+    // T = 4096 15.8 us against 16.0, T = 8192 25.7 against 30.5) and small ones
+    // below (T = 512 6.8 against 11.0).  fp32: small tiles, which the large
+    // ones beat by 5% at most (250 experts, T = 16384).
+    const auto tiles_of = [&](auto e, auto mb, auto wn) {
+        typedef decltype(e) E;
+        constexpr int MB = decltype(mb)::value, WN = decltype(wn)::value;
+        const int groups = ceil_div(d, 64 * WN);
+        const unsigned tiles = ceil_div(T, 32 * MB), grid = share_grid(groups, tiles);
+        const auto *w = static_cast<const E *>(w_router), *in = static_cast<const E *>(dx_in);
+        auto *out = static_cast<E *>(dx);
+        if (T < 32 * MB || Ne < DxTile<E, MB, WN>::kDepth)
+            k_gate_dx_tile<E, MB, WN, true>
+                <<<grid, 2 * WN * kWave, 0, s>>>(dl, w, in, out, T, d, Ne, groups, tiles);
+        else
+            k_gate_dx_tile<E, MB, WN, false>
+                <<<grid, 2 * WN * kWave, 0, s>>>(dl, w, in, out, T, d, Ne, groups, tiles);
         return hipGetLastError();
-    }
+    };
+    using std::integral_constant;
+    if (!bf16) return tiles_of(float{}, integral_constant<int, 2>{}, integral_constant<int, 2>{});
+    if (Ne > 64 && static_cast<int64_t>(ceil_div(T, 128)) * ceil_div(d, 256) >= 256)
+        return tiles_of(uint16_t{}, integral_constant<int, 4>{}, integral_constant<int, 4>{});
+    if (Ne > 64)
+        return tiles_of(uint16_t{}, integral_constant<int, 2>{}, integral_constant<int, 2>{});
     const bool vec = Ne % 4 == 0 && reinterpret_cast<uintptr_t>(dl) % 16 == 0;
-    auto run = [&](auto ks, auto ni) {
-        constexpr int KS = decltype(ks)::value, NI = decltype(ni)::value;
+    auto run = [&](auto ks) {
+        constexpr int KS = decltype(ks)::value;
         // waves walk over enough token tiles to pay for their W_r fragments
-        const unsigned cols = ceil_div(d, kWaves * 16 * NI);
+        const unsigned cols = ceil_div(d, kWaves * kDxCols);
         const unsigned shares = std::min(ceil_div(512, cols), ceil_div(T, 16));
         const unsigned grid = share_grid(cols, shares);
         const auto *w = static_cast<const uint16_t *>(w_router);
         const auto *in = static_cast<const uint16_t *>(dx_in);
         auto *out = static_cast<uint16_t *>(dx);
         if (vec)
-            k_gate_dx<KS, NI, true><<<grid, kThreads, 0, s>>>(dl, w, in, out, T, d, Ne, cols, shares);
+            k_gate_dx<KS, true><<<grid, kThreads, 0, s>>>(dl, w, in, out, T, d, Ne, cols, shares);
         else
-            k_gate_dx<KS, NI, false><<<grid, kThreads, 0, s>>>(dl, w, in, out, T, d, Ne, cols, shares);
+            k_gate_dx<KS, false><<<grid, kThreads, 0, s>>>(dl, w, in, out, T, d, Ne, cols, shares);
     };
-    using std::integral_constant;
     if (Ne <= 32)
-        run(integral_constant<int, 1>{}, integral_constant<int, 8>{});
-    else if (Ne <= 64)
-        run(integral_constant<int, 2>{}, integral_constant<int, 8>{});
-    else if (Ne <= 128)
-        run(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+        run(integral_constant<int, 1>{});
     else
-        run(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+        run(integral_constant<int, 2>{});
     return hipGetLastError();
 }
 
@@ -528,22 +738,22 @@ hipError_t launch_gate_dw(const float *dl, const void *x, int T, int d, int Ne, 
                           float *part, float *dw, hipStream_t s) {
     const int shares = gate_dw_shares(T, d, Ne, bf16);
     // whole steps; the last shares may then be empty, and sum to zero
-    const unsigned step = bf16 ? 64 : 32, per = ceil_div(ceil_div(T, shares), step) * step;
-    const unsigned eg = ceil_div(Ne, kDwExperts);
+    const unsigned per = ceil_div(ceil_div(T, shares), 64) * 64;
+    const int cols = ceil_div(d, bf16 ? kDwCols : kDwColsF);
+    const int groups = cols * static_cast<int>(ceil_div(Ne, kDwExperts));
+    const unsigned grid = share_grid(groups, shares);
     float *out = shares > 1 ? part : dw;
     if (bf16) {
-        const int groups = ceil_div(d, kDwCols);
-        const dim3 grid(share_grid(groups, shares), eg);
         const auto *xb = static_cast<const uint16_t *>(x);
         if (Ne <= 16)
-            k_gate_dw<1><<<grid, kDwThreads, 0, s>>>(dl, xb, T, d, Ne, groups, shares, per, out);
+            k_gate_dw<1><<<grid, kDwThreads, 0, s>>>(dl, xb, T, d, Ne, groups, cols, shares, per, out);
         else if (Ne <= 32)
-            k_gate_dw<2><<<grid, kDwThreads, 0, s>>>(dl, xb, T, d, Ne, groups, shares, per, out);
+            k_gate_dw<2><<<grid, kDwThreads, 0, s>>>(dl, xb, T, d, Ne, groups, cols, shares, per, out);
         else
-            k_gate_dw<4><<<grid, kDwThreads, 0, s>>>(dl, xb, T, d, Ne, groups, shares, per, out);
+            k_gate_dw<4><<<grid, kDwThreads, 0, s>>>(dl, xb, T, d, Ne, groups, cols, shares, per, out);
     } else {
-        k_gate_dw_f32<<<dim3(ceil_div(d, kDwColsF), eg, shares), kThreads, 0, s>>>(
-            dl, static_cast<const float *>(x), T, d, Ne, per, out);
+        k_gate_dw_f32<<<grid, kThreads, 0, s>>>(dl, static_cast<const float *>(x), T, d, Ne, groups, cols,
+                                                shares, per, out);
     }
     if (shares > 1) {
         const size_t n4 = static_cast<size_t>(Ne) * d / 4;
