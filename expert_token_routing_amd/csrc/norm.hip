@@ -17,7 +17,9 @@
 // threads shares it (chunk c with thread c mod NT, so that a wave's loads are
 // contiguous).  Teams are as wide as leaves each thread one or two chunks:
 // short dependent chains and few registers, so that many rows are in flight;
-// a team of several waves adds its sums through LDS.  At d = 2048 in bf16
+// a team of several waves adds its sums through LDS, and a row of up to 32
+// chunks takes 16 or 32 lanes of a wave (T = 65536, d = 128 forward 13 us, 24
+// with a wave to a row; backward 27 against 50).  At d = 2048 in bf16
 // (256 chunks), T = 65536 forward: 184 us with 128 threads a row, 190 with
 // 256, 200 with 64 (one wave, no barrier).
 // The forward gives each row to a team of its own.  In the backward each
@@ -91,7 +93,7 @@ template <int NT, int M>
 __device__ __forceinline__ void row_sums(float (&v)[M], Slots &slots, int &turn) {
     constexpr int kRowWaves = NT / kWave;
 #pragma unroll
-    for (int i = 0; i < M; i++) v[i] = wave_sum(v[i]);
+    for (int i = 0; i < M; i++) v[i] = NT < kWave ? group_sum<NT>(v[i]) : wave_sum(v[i]);
     if constexpr (kRowWaves > 1) {
         const int w = threadIdx.x / kWave, w0 = threadIdx.x / NT * kRowWaves;
         if (lane_id() == 0) {
@@ -359,7 +361,11 @@ __global__ __launch_bounds__(kFoldCols *kFoldShares) void k_norm_fold(
 template <typename F>
 void by_width(int chunks, F f) {
     using std::integral_constant;
-    if (chunks <= 64)
+    if (chunks <= 16)
+        f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+    else if (chunks <= 32)
+        f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+    else if (chunks <= 64)
         f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
     else if (chunks <= 128)
         f(integral_constant<int, 128>{}, integral_constant<int, 1>{});
@@ -375,7 +381,11 @@ void by_width(int chunks, F f) {
 template <typename F>
 void by_width_back(int chunks, F f) {
     using std::integral_constant;
-    if (chunks <= 64)
+    if (chunks <= 16)
+        f(integral_constant<int, 16>{});
+    else if (chunks <= 32)
+        f(integral_constant<int, 32>{});
+    else if (chunks <= 64)
         f(integral_constant<int, 64>{});
     else if (chunks <= 128)
         f(integral_constant<int, 128>{});

@@ -541,8 +541,9 @@ occ_status occ_balance_backward(const occ_layer_desc *desc, const occ_balance_de
  *   dx = dx_in + dlogits w_router,   dw_router = dlogits^T x
  * Uses T, d, Ne and dtype; sums are fp32.  With bf16 tensors the fp32 dlogits
  * enter the matrix cores as a sum of bf16 terms: two for dx (16 bits, below
- * the rounding of dx), three for dw_router (all 24 bits); a dlogits value
- * that is not finite gives NaN where it contributes.
+ * the rounding of dx), three for dw_router (all 24 bits).  A value that is not
+ * finite gives NaN or infinity where it contributes (an x value: in its
+ * column of dw_router).
  *   dlogits    T x Ne fp32.
  *   x          T x d (dtype); may be NULL without dw_router.
  *   w_router   Ne x d (dtype); may be NULL without dx.

@@ -77,7 +77,7 @@ FORMS = {
 NORM_SHAPES = [(BF16, 1, 64), (BF16, 3, 192), (BF16, 7, 512), (BF16, 130, 1024), (BF16, 33, 1088),
                (BF16, 1001, 2048), (BF16, 5, 2112), (BF16, 600, 4096), (BF16, 3, 4160),
                (BF16, 70, 8192), (BF16, 9000, 64), (F32, 1, 16), (F32, 37, 80), (F32, 11, 272),
-               (F32, 300, 1024), (F32, 65, 1040), (F32, 6, 4096), (F32, 2100, 48)]
+               (F32, 300, 1024), (F32, 65, 1040), (F32, 6, 4096), (F32, 2100, 48), (BF16, 5000, 256), (F32, 70000, 16)]
 
 
 def norm_inputs(dtype, T, d, form, seed):
@@ -147,6 +147,20 @@ def test_norm_forward_and_backward(dtype, T, d, form):
     kept = r if r is not None else t["x"]
     out = run_norm_back(t, grads, kept, opt, dtype)
     check_norm_back(t, grads, kept, opt, out)
+
+
+def test_norm_backward_without_y_when_nothing_reads_it():
+    """Neither norm nor gate behind the block: dy = scale dr', with y or without."""
+    t, grads, opt = norm_inputs(BF16, 50, 320, "prenorm", seed=9)
+    r, _ = run_norm(t, opt, BF16)
+    want = run_norm_back(t, grads, r, opt, BF16)
+    dx, dy, dw = nan_like((50, 320), BF16), nan_like((50, 320), BF16), nan_like((320,))
+    desc = layer(50, 320, dtype=BF16)
+    occ.occ_block_norm_backward(desc, opt, grads["dr"], grads["dh"], r, None, None, None,
+                                t["w_pre"], dx, dy, None, None, dw,
+                                occ.alloc_block_workspace(desc))
+    assert torch.equal(dx, want["dx"]) and torch.equal(dy, want["dy"])
+    assert torch.equal(dw, want["dw_pre"])
 
 
 def test_norm_rows_of_zeros_and_of_extreme_size():
