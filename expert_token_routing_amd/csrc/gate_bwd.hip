@@ -677,8 +677,11 @@ __global__ __launch_bounds__(kThreads) void k_gate_dw_fold(const f32x4 *__restri
 // the device's state: enough for one workgroup per CU (two in fp32, of half
 // the waves: T = 4096, d = 2048, 64 experts 20 us against 24, four 27), of two
 // steps each at least (128 tokens).  A share costs Ne x d fp32 written and
-// read.
+// read, and several shares another launch: up to 256 tokens make one (a call
+// at T = 256, d = 128, 8 experts bf16: 12.1 us against 14.8, 9.6 against 10.0
+// in a graph; at T = 512 the longer share costs more, 13.7 against 11.0).
 int gate_dw_shares(int T, int d, int Ne, int bf16) {
+    if (T <= 256) return 1;
     const unsigned cols = ceil_div(d, bf16 ? kDwCols : kDwColsF);
     const unsigned want = ceil_div(bf16 ? 256 : 512, cols * ceil_div(Ne, kDwExperts));
     return static_cast<int>(std::min(want, ceil_div(T, 128)));
