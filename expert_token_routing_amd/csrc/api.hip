@@ -777,12 +777,8 @@ occ_status occ_gate_backward(const occ_layer_desc *desc, const float *dlogits, c
     if (dw_router) OCC_TRY(check_ws(*desc, workspace, ws_bytes, block_ws_bytes(*desc)));
     const int bf16 = desc->dtype == OCC_BF16;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    // dw_router first: dx may be the array that holds x
-    if (dw_router)
-        OCC_HIP(launch_gate_dw(dlogits, x, desc->T, desc->d, desc->Ne, bf16,
-                               static_cast<float *>(workspace), dw_router, s));
-    if (dx)
-        OCC_HIP(launch_gate_dx(dlogits, w_router, dx_in, desc->T, desc->d, desc->Ne, bf16, dx, s));
+    OCC_HIP(launch_gate_bwd(dlogits, x, w_router, dx_in, desc->T, desc->d, desc->Ne, bf16, dx,
+                            static_cast<float *>(workspace), dw_router, s));
     return OCC_OK;
 }
 

@@ -10,13 +10,15 @@
 // bf16 terms, each the rounding of what the ones before it leave: two terms
 // (16 bits, far below the bf16 rounding of dx) in dx, three (all 24 bits of
 // an fp32 value) in dW_r, whose outputs are fp32.
-//   k_gate_dx   a wave owns 128 columns, keeps W_r's fragments for them in
-//               registers (Ne x 128, transposed there once) and walks over
-//               16-token tiles.  Column 8 i + ni is column i of fragment ni,
-//               so that a lane ends with 8 consecutive columns of four tokens
-//               and 16 lanes move 256 bytes of a row at once (in 64-byte
-//               pieces: 118 us at T = 65536, d = 2048, Ne = 60 against 95).
-//   k_gate_dw   a workgroup owns 256 columns, 64 experts and a share of the
+//   gate_dx     a wave owns 128 columns, keeps W_r's fragments for them in
+//               registers (up to 64 experts x 128, transposed there once) and
+//               walks over 16-token tiles.  Column 8 i + ni is column i of
+//               fragment ni, so that a lane ends with 8 consecutive columns of
+//               four tokens and 16 lanes move 256 bytes of a row at once (in
+//               64-byte pieces: 118 us at T = 65536, d = 2048, Ne = 60
+//               against 95).
+//   gate_dx_tile  more than 64 experts, through LDS.
+//   gate_dw     a workgroup owns 256 columns, 64 experts and a share of the
 //               tokens, 64 per step.  MFMA wants 8 consecutive tokens of one
 //               column per lane, x holds columns consecutively: each lane
 //               loads 4 columns of its 8 tokens and transposes them in
@@ -26,14 +28,17 @@
 //               fragments, while the step before is multiplied.  The two
 //               halves are added at the end, and the shares by a second
 //               kernel in order.
-// Measured at d = 2048, Ne = 60, T = 65536: dW_r 75 us + 6 for the shares, dx
-// 95 us (5.8 TB/s of 553 MB), 174 us as one call (4.7 TB/s of its 822 MB; one
-// bf16 term in place of three leaves the call as it is: the memory bounds
-// it); Ne = 64, T = 8192: 17 + 4.5 and 17 us.
-//   k_gate_dx_tile   dx with more than 64 experts, through LDS; 130 experts,
-//               T = 8192, d = 2048: 25.7 us (68 MB: 11 at 6 TB/s).
-// fp32: v_mfma_f32_16x16x4_f32, exact products, in k_gate_dx_tile (T = 4096,
-// d = 2048, 64 experts: 20 us for 68 MB) and k_gate_dw_f32 (24 us).
+// fp32: v_mfma_f32_16x16x4_f32, exact products, in gate_dx_tile and gate_dw_f32.
+//
+// One launch makes both products, each by workgroups of its own, so that one's
+// start, its waits and its last workgroups lie under the other's work
+// (k_gate_bwd, k_gate_bwd_f32).  Against a launch for each: T = 256, d = 2048,
+// 64 experts 10.4 us against 14.6 (bf16), 11.7 against 17.2 (fp32); T = 8192
+// 31 against 39, 60 against 65; T = 32768 90 against 96, 202 against 201; 250
+// experts in bf16 T = 1024 19 against 28, T = 32768 218 against 209.
+// Measured at d = 2048 bf16: Ne = 60, T = 65536 164 us + 5 for the shares
+// (4.9 TB/s of 822 MB, with one bf16 term in place of three as long: the
+// memory bounds it); Ne = 64, T = 8192 27 + 4.7 us (3.3 TB/s of 104 MB).
 #include <algorithm>
 #include <type_traits>
 
@@ -48,24 +53,50 @@ typedef f32x4 f32x4_unaligned __attribute__((aligned(4)));  // the hardware take
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kDxCols = 128;    // columns of a wave in k_gate_dx
-constexpr int kDwThreads = 512; // k_gate_dw
-constexpr int kDwCols = 256;    // columns of a workgroup in k_gate_dw
-constexpr int kDwColsF = 64;    // in k_gate_dw_f32
+constexpr int kDxCols = 128;    // columns of a wave in gate_dx
+constexpr int kBfThreads = 512; // k_gate_bwd
+constexpr int kDwCols = 256;    // columns of a workgroup in gate_dw
+constexpr int kDwColsF = 64;    // in gate_dw_f32
 constexpr int kDwExperts = 64;  // experts of a workgroup in either
 
 // Workgroup b runs on XCD b mod 8, each with an L2 of its own.  A token range
 // meets every column group, so its groups get numbers that share an XCD: the
 // range's dlogits are fetched into one L2 instead of eight.  Fewer ranges
 // than XCDs spread their groups over all of them instead.
-__device__ __forceinline__ bool share_of(int groups, unsigned shares, int &group, unsigned &share) {
-    const unsigned r = shares < 8 ? blockIdx.x : blockIdx.x >> 3;
+__device__ __forceinline__ bool share_of(unsigned block, int groups, unsigned shares, int &group,
+                                         unsigned &share) {
+    const unsigned r = shares < 8 ? block : block >> 3;
     group = static_cast<int>(r % groups);
-    share = shares < 8 ? r / groups : r / groups * 8 + (blockIdx.x & 7);
+    share = shares < 8 ? r / groups : r / groups * 8 + (block & 7);
     return share < shares;
 }
 unsigned share_grid(int groups, unsigned shares) {
     return groups * (shares < 8 ? shares : ceil_div(shares, 8) * 8);
+}
+
+// What the workgroups of one product need.  blocks: how many of a launch are
+// its own, whole multiples of the XCDs (0: not computed).
+struct DxArgs {
+    const void *w_router, *dx_in;
+    void *dx;
+    int groups;
+    unsigned shares;  // or tiles
+    unsigned blocks;
+};
+struct DwArgs {
+    const void *x;
+    float *out;  // [share][Ne][d]
+    int groups, col_groups;
+    unsigned shares, per_share, blocks;
+};
+unsigned whole_xcds(unsigned blocks) { return ceil_div(blocks, 8) * 8; }
+
+// This workgroup's number among those of its product; dx_first: dx's come first.
+__device__ __forceinline__ unsigned own_block(const DwArgs &dw, const DxArgs &dx, bool dx_first,
+                                              bool &is_dw) {
+    const unsigned first = dx_first ? dx.blocks : dw.blocks;
+    is_dw = (blockIdx.x < first) != dx_first;
+    return blockIdx.x < first ? blockIdx.x : blockIdx.x - first;
 }
 
 // Two values as bf16, the first in the low half.
@@ -125,18 +156,20 @@ __device__ __forceinline__ void transpose8(const V (&r)[8], bf16x8_t (&out)[NI])
 
 // KS: 32-deep steps over the experts.  Waves are independent (no barrier).
 template <int KS, bool VEC>
-__global__ __launch_bounds__(kThreads) void k_gate_dx(const float *__restrict__ dl,
-                                                      const uint16_t *__restrict__ wr,
-                                                      const uint16_t *dx_in, uint16_t *dx,
-                                                      unsigned T, int d, int Ne, int groups,
-                                                      unsigned shares) {
+__device__ __forceinline__ void gate_dx(unsigned block, const float *__restrict__ dl, unsigned T,
+                                        int d, int Ne, const DxArgs &A) {
+    const auto *__restrict__ wr = static_cast<const uint16_t *>(A.w_router);
+    const auto *dx_in = static_cast<const uint16_t *>(A.dx_in);
+    auto *dx = static_cast<uint16_t *>(A.dx);
+    const int groups = A.groups;
+    const unsigned shares = A.shares;
     constexpr int NI = kDxCols / 16;  // 16-column fragments
     typedef u32x4 Cols;               // NI columns
     const int l = lane_id(), i16 = l & 15, G = l >> 4;
     int group;
     unsigned tile;
-    if (!share_of(groups, shares, group, tile)) return;
-    const int c0 = (group * kWaves + threadIdx.x / kWave) * (16 * NI);
+    if (!share_of(block, groups, shares, group, tile)) return;
+    const int c0 = (group * (blockDim.x / kWave) + threadIdx.x / kWave) * (16 * NI);
     if (c0 >= d) return;
     bf16x8_t w[KS][NI];
     // column i of fragment ni is NI i + ni
@@ -233,24 +266,29 @@ __global__ __launch_bounds__(kThreads) void k_gate_dx(const float *__restrict__ 
 // 0..3 and 4..7 take the two 32-token halves of a step, wave w the 64 columns
 // from 64 (w mod 4).
 template <int MB>
-__global__ __launch_bounds__(kDwThreads) void k_gate_dw(const float *__restrict__ dl,
-                                                        const uint16_t *__restrict__ x, unsigned T,
-                                                        int d, int Ne, int groups, int col_groups,
-                                                        unsigned shares, unsigned per_share,
-                                                        float *__restrict__ part) {
+struct DwLds {
     typedef bf16x8_t Terms[2][2][MB][3][kWave];  // [buffer][half][expert block][term][lane]
     typedef f32x4 Sums[4][MB * 4][kWave];
-    __shared__ __attribute__((aligned(16))) char lds[sizeof(Terms) > sizeof(Sums) ? sizeof(Terms) : sizeof(Sums)];
+    static constexpr size_t kBytes = std::max(sizeof(Terms), sizeof(Sums));
+};
+template <int MB>
+__device__ __forceinline__ void gate_dw(unsigned block, const float *__restrict__ dl, unsigned T,
+                                        int d, int Ne, const DwArgs &A, char *lds) {
+    typedef typename DwLds<MB>::Terms Terms;
+    typedef typename DwLds<MB>::Sums Sums;
+    const auto *__restrict__ x = static_cast<const uint16_t *>(A.x);
+    float *__restrict__ part = A.out;
+    const int col_groups = A.col_groups;
     Terms &s_a = *reinterpret_cast<Terms *>(lds);
     Sums &s_sum = *reinterpret_cast<Sums *>(lds);
     const int l = lane_id(), i16 = l & 15, G = l >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), half = wv >> 2, cg = wv & 3;
     int group;
     unsigned share;
-    if (!share_of(groups, shares, group, share)) return;
+    if (!share_of(block, A.groups, A.shares, group, share)) return;
     const int c0 = group % col_groups * kDwCols + 64 * cg, e0 = group / col_groups * kDwExperts;
     const bool col_in = c0 < d;  // d is a multiple of 64
-    const unsigned t0 = share * per_share, t1 = min(T, t0 + per_share);
+    const unsigned t0 = share * A.per_share, t1 = min(T, t0 + A.per_share);
     f32x4 acc[MB][4];
 #pragma unroll
     for (int m = 0; m < MB; m++)
@@ -385,16 +423,20 @@ struct DxTile<float, MB, WN> {
 // token (expert) starts early enough not to, and leaves out what others do.
 // SMALL takes the rest, with clamped addresses.
 template <typename E, int MB, int WN, bool SMALL>
-__global__ __launch_bounds__(2 * WN *kWave, 4) void k_gate_dx_tile(
-    const float *__restrict__ dl, const E *__restrict__ wr, const E *dx_in, E *dx, unsigned T,
-    int d, int Ne, int groups, unsigned tiles) {
+__device__ __forceinline__ void gate_dx_tile(unsigned block, const float *__restrict__ dl, unsigned T,
+                                             int d, int Ne, const DxArgs &A,
+                                             DxTile<E, MB, WN> (&lds)[2]) {
+    const auto *__restrict__ wr = static_cast<const E *>(A.w_router);
+    const auto *dx_in = static_cast<const E *>(A.dx_in);
+    auto *dx = static_cast<E *>(A.dx);
+    const int groups = A.groups;
+    const unsigned tiles = A.shares;
     typedef DxTile<E, MB, WN> Tile;
     constexpr int kTokens = 32 * MB, kDepth = Tile::kDepth, kOwn = kDepth / 4;
     constexpr bool kBf16 = sizeof(E) == 2;
-    __shared__ Tile lds[2];
     int group;
     unsigned tile;
-    if (!share_of(groups, tiles, group, tile)) return;
+    if (!share_of(block, groups, tiles, group, tile)) return;
     const int tid = threadIdx.x, l = lane_id(), i16 = l & 15, G = l >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(tid / kWave), wm = wv / WN, wn = wv % WN;
     const int c0 = group * 64 * WN;
@@ -561,25 +603,54 @@ __global__ __launch_bounds__(2 * WN *kWave, 4) void k_gate_dx_tile(
         }
 }
 
+template <typename E, int MB, int WN, bool SMALL>
+__global__ __launch_bounds__(2 * WN *kWave, 4) void k_gate_dx_tile(const float *__restrict__ dl,
+                                                                   unsigned T, int d, int Ne,
+                                                                   const DxArgs dx) {
+    __shared__ DxTile<E, MB, WN> lds[2];
+    gate_dx_tile<E, MB, WN, SMALL>(blockIdx.x, dl, T, d, Ne, dx, lds);
+}
+
+// bf16, both products: those of dx in the form that DX names.
+enum DxKind { kRegsVec, kRegs, kTile, kSmallTile };
+template <int MB, int DX>
+__global__ __launch_bounds__(kBfThreads) void k_gate_bwd(const float *__restrict__ dl, unsigned T,
+                                                         int d, int Ne, const DwArgs dw,
+                                                         const DxArgs dx, bool dx_first) {
+    typedef DxTile<uint16_t, 4, 4> Tile;
+    constexpr bool kTiles = DX == kTile || DX == kSmallTile;
+    __shared__ __attribute__((aligned(16))) char
+        lds[kTiles ? std::max(DwLds<MB>::kBytes, 2 * sizeof(Tile)) : DwLds<MB>::kBytes];
+    bool is_dw;
+    const unsigned block = own_block(dw, dx, dx_first, is_dw);
+    if (is_dw)
+        gate_dw<MB>(block, dl, T, d, Ne, dw, lds);
+    else if constexpr (kTiles)
+        gate_dx_tile<uint16_t, 4, 4, DX == kSmallTile>(block, dl, T, d, Ne, dx,
+                                                       *reinterpret_cast<Tile(*)[2]>(lds));
+    else
+        gate_dx<(MB + 1) / 2, DX == kRegsVec>(block, dl, T, d, Ne, dx);
+}
+
 // fp32: a wave makes 64 experts x 64 columns of dW_r from a quarter of the
 // workgroup's tokens, 16 per step.  Expert 4 i + m is row i of block m and
 // column 4 i + q column i of block q, so that a lane's operands of 16 MFMAs
 // are one 16-byte piece of a token's dlogits and one of its x.  What lies
 // behind a token's last expert is read with it (its sums are not stored),
 // except near the end of the array.
-__global__ __launch_bounds__(kThreads) void k_gate_dw_f32(const float *__restrict__ dl,
-                                                          const float *__restrict__ x, unsigned T,
-                                                          int d, int Ne, int groups, int col_groups,
-                                                          unsigned shares, unsigned per_share,
-                                                          float *__restrict__ part) {
-    __shared__ f32x4 s_acc[kWaves / 2][16][kWave];
+typedef f32x4 DwSums[kWaves / 2][16][kWave];
+__device__ __forceinline__ void gate_dw_f32(unsigned block, const float *__restrict__ dl, unsigned T,
+                                            int d, int Ne, const DwArgs &A, DwSums &s_acc) {
+    const auto *__restrict__ x = static_cast<const float *>(A.x);
+    float *__restrict__ part = A.out;
+    const int col_groups = A.col_groups;
     int group;
     unsigned share;
-    if (!share_of(groups, shares, group, share)) return;
+    if (!share_of(block, A.groups, A.shares, group, share)) return;
     const int l = lane_id(), i16 = l & 15, G = l >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int c0 = group % col_groups * kDwColsF, e0 = group / col_groups * kDwExperts;
-    const unsigned t0 = share * per_share, t1 = min(T, t0 + per_share);
+    const unsigned t0 = share * A.per_share, t1 = min(T, t0 + A.per_share);
     const int col = min(c0 + 4 * i16, d - 4), exp = min(e0 + 4 * i16, Ne - 1);
     f32x4 acc[4][4];  // [m][q]
 #pragma unroll
@@ -650,6 +721,20 @@ __global__ __launch_bounds__(kThreads) void k_gate_dw_f32(const float *__restric
         }
 }
 
+template <bool SMALL>
+__global__ __launch_bounds__(kThreads) void k_gate_bwd_f32(const float *__restrict__ dl, unsigned T,
+                                                           int d, int Ne, const DwArgs dw,
+                                                           const DxArgs dx) {
+    typedef DxTile<float, 2, 2> Tile;
+    __shared__ __attribute__((aligned(16))) char lds[std::max(sizeof(DwSums), 2 * sizeof(Tile))];
+    bool is_dw;
+    const unsigned block = own_block(dw, dx, false, is_dw);
+    if (is_dw)
+        gate_dw_f32(block, dl, T, d, Ne, dw, *reinterpret_cast<DwSums *>(lds));
+    else
+        gate_dx_tile<float, 2, 2, SMALL>(block, dl, T, d, Ne, dx, *reinterpret_cast<Tile(*)[2]>(lds));
+}
+
 // dw = the sum of the token shares' partial sums: thread (i, q) adds shares q,
 // q + 4, ..., then the four are added in order.
 constexpr int kFoldOut = kThreads / 4;
@@ -673,95 +758,133 @@ __global__ __launch_bounds__(kThreads) void k_gate_dw_fold(const f32x4 *__restri
 
 }  // namespace
 
-// Token shares of dW_r, from the shape alone, so that sums do not depend on
-// the device's state: enough for one workgroup per CU (two in fp32, of half
-// the waves: T = 4096, d = 2048, 64 experts 20 us against 24, four 27), of two
-// steps each at least (128 tokens).  A share costs Ne x d fp32 written and
-// read, and several shares another launch: up to 256 tokens make one (a call
-// at T = 256, d = 128, 8 experts bf16: 12.1 us against 14.8, 9.6 against 10.0
-// in a graph; at T = 512 the longer share costs more, 13.7 against 11.0).
+// Token shares of dW_r: enough of them for a workgroup (two in fp32, of half
+// the waves) on every CU if that leaves 512 tokens to a share, for half as
+// many otherwise, beside dx's workgroups and with half the partial sums (each
+// Ne x d fp32, written and read); of 128 tokens at least, and of all up to
+// 256, which saves the launch that adds them.  From the shape alone, so that
+// a sum does not depend on the device or on what else a call computes.
+// Measured as one call at d = 2048, the larger count and half of it: bf16 T =
+// 4096, 8 to 64 experts 18 to 26 us against 16 to 21, T = 32768 78 to 90
+// against 81 to 97; fp32 T = 4096, 250 experts 88 against 86 (dW_r alone, T =
+// 32768: 85 against 101); T = 256, d = 128, one share against two 12.1 against
+// 14.8, T = 512 13.7 against 11.0.
+static unsigned gate_dw_full(int d, int Ne, int bf16) {
+    const unsigned groups = ceil_div(d, bf16 ? kDwCols : kDwColsF) * ceil_div(Ne, kDwExperts);
+    return ceil_div(bf16 ? 256 : 512, groups);
+}
+static bool gate_dw_long(int T, int d, int Ne, int bf16) {
+    return T / 512 >= static_cast<int>(gate_dw_full(d, Ne, bf16));
+}
 int gate_dw_shares(int T, int d, int Ne, int bf16) {
     if (T <= 256) return 1;
-    const unsigned cols = ceil_div(d, bf16 ? kDwCols : kDwColsF);
-    const unsigned want = ceil_div(bf16 ? 256 : 512, cols * ceil_div(Ne, kDwExperts));
-    return static_cast<int>(std::min(want, ceil_div(T, 128)));
+    const unsigned full = gate_dw_full(d, Ne, bf16);
+    return static_cast<int>(
+        std::min(gate_dw_long(T, d, Ne, bf16) ? full : ceil_div(full, 2), ceil_div(T, 128)));
 }
 
-hipError_t launch_gate_dx(const float *dl, const void *w_router, const void *dx_in, int T, int d,
-                          int Ne, int bf16, void *dx, hipStream_t s) {
-    // bf16: the register kernel holds up to 64 experts' weights; with more,
-    // tiles, large ones where there is one for every CU (130 experts, d = 2048:
-    // T = 4096 15.8 us against 16.0, T = 8192 25.7 against 30.5) and small ones
-    // below (T = 512 6.8 against 11.0).  fp32: small tiles, which the large
-    // ones beat by 5% at most (250 experts, T = 16384).
+hipError_t launch_gate_bwd(const float *dl, const void *x, const void *w_router, const void *dx_in,
+                           int T, int d, int Ne, int bf16, void *dx, float *part, float *dw,
+                           hipStream_t s) {
+    const size_t bytes = static_cast<size_t>(T) * d * (bf16 ? 2 : 4);
+    const auto xa = reinterpret_cast<uintptr_t>(x), da = reinterpret_cast<uintptr_t>(dx);
+    if (dx && dw && xa < da + bytes && da < xa + bytes) {
+        // dx lies in x: it is written when dW_r has read it
+        const hipError_t e = launch_gate_bwd(dl, x, nullptr, nullptr, T, d, Ne, bf16, nullptr, part, dw, s);
+        if (e != hipSuccess) return e;
+        return launch_gate_bwd(dl, nullptr, w_router, dx_in, T, d, Ne, bf16, dx, nullptr, nullptr, s);
+    }
+    DwArgs W = {};
+    if (dw) {
+        W.x = x;
+        W.shares = gate_dw_shares(T, d, Ne, bf16);
+        W.out = W.shares > 1 ? part : dw;
+        // whole steps; the last shares may then be empty, and sum to zero
+        W.per_share = ceil_div(ceil_div(T, W.shares), 64) * 64;
+        W.col_groups = ceil_div(d, bf16 ? kDwCols : kDwColsF);
+        W.groups = W.col_groups * static_cast<int>(ceil_div(Ne, kDwExperts));
+        W.blocks = whole_xcds(share_grid(W.groups, W.shares));
+    }
+    DxArgs X = {w_router, dx_in, dx, 0, 0, 0};
+    using std::integral_constant;
+    typedef integral_constant<int, 2> I2;
+    typedef integral_constant<int, 4> I4;
+    // dx in tiles of 32 MB x 64 WN; true: smaller than a tile
     const auto tiles_of = [&](auto e, auto mb, auto wn) {
+        constexpr int MB = decltype(mb)::value, WN = decltype(wn)::value;
+        X.groups = ceil_div(d, 64 * WN);
+        X.shares = ceil_div(T, 32 * MB);
+        X.blocks = whole_xcds(share_grid(X.groups, X.shares));
+        return T < 32 * MB || Ne < DxTile<decltype(e), MB, WN>::kDepth;
+    };
+    const auto tiles_alone = [&](auto e, auto mb, auto wn) {
         typedef decltype(e) E;
         constexpr int MB = decltype(mb)::value, WN = decltype(wn)::value;
-        const int groups = ceil_div(d, 64 * WN);
-        const unsigned tiles = ceil_div(T, 32 * MB), grid = share_grid(groups, tiles);
-        const auto *w = static_cast<const E *>(w_router), *in = static_cast<const E *>(dx_in);
-        auto *out = static_cast<E *>(dx);
-        if (T < 32 * MB || Ne < DxTile<E, MB, WN>::kDepth)
-            k_gate_dx_tile<E, MB, WN, true>
-                <<<grid, 2 * WN * kWave, 0, s>>>(dl, w, in, out, T, d, Ne, groups, tiles);
+        if (tiles_of(e, mb, wn))
+            k_gate_dx_tile<E, MB, WN, true><<<X.blocks, 2 * WN * kWave, 0, s>>>(dl, T, d, Ne, X);
         else
-            k_gate_dx_tile<E, MB, WN, false>
-                <<<grid, 2 * WN * kWave, 0, s>>>(dl, w, in, out, T, d, Ne, groups, tiles);
-        return hipGetLastError();
+            k_gate_dx_tile<E, MB, WN, false><<<X.blocks, 2 * WN * kWave, 0, s>>>(dl, T, d, Ne, X);
     };
-    using std::integral_constant;
-    if (!bf16) return tiles_of(float{}, integral_constant<int, 2>{}, integral_constant<int, 2>{});
-    if (Ne > 64 && static_cast<int64_t>(ceil_div(T, 128)) * ceil_div(d, 256) >= 256)
-        return tiles_of(uint16_t{}, integral_constant<int, 4>{}, integral_constant<int, 4>{});
-    if (Ne > 64)
-        return tiles_of(uint16_t{}, integral_constant<int, 2>{}, integral_constant<int, 2>{});
-    const bool vec = Ne % 4 == 0 && reinterpret_cast<uintptr_t>(dl) % 16 == 0;
-    auto run = [&](auto ks) {
-        constexpr int KS = decltype(ks)::value;
-        // waves walk over enough token tiles to pay for their W_r fragments
-        const unsigned cols = ceil_div(d, kWaves * kDxCols);
-        const unsigned shares = std::min(ceil_div(512, cols), ceil_div(T, 16));
-        const unsigned grid = share_grid(cols, shares);
-        const auto *w = static_cast<const uint16_t *>(w_router);
-        const auto *in = static_cast<const uint16_t *>(dx_in);
-        auto *out = static_cast<uint16_t *>(dx);
-        if (vec)
-            k_gate_dx<KS, true><<<grid, kThreads, 0, s>>>(dl, w, in, out, T, d, Ne, cols, shares);
-        else
-            k_gate_dx<KS, false><<<grid, kThreads, 0, s>>>(dl, w, in, out, T, d, Ne, cols, shares);
+    // Long shares of dW_r are the finer work and follow dx's workgroups, which
+    // each walk over many tiles (T = 32768, d = 2048, 30 experts: 83 us against
+    // 90); few of them come first.
+    const bool dx_first = Ne <= 64 && gate_dw_long(T, d, Ne, bf16);
+    const auto both = [&](auto mb, auto kind, int threads) {
+        k_gate_bwd<decltype(mb)::value, decltype(kind)::value>
+            <<<W.blocks + X.blocks, threads, 0, s>>>(dl, T, d, Ne, W, X, dx_first);
     };
-    if (Ne <= 32)
-        run(integral_constant<int, 1>{});
-    else
-        run(integral_constant<int, 2>{});
-    return hipGetLastError();
-}
-
-hipError_t launch_gate_dw(const float *dl, const void *x, int T, int d, int Ne, int bf16,
-                          float *part, float *dw, hipStream_t s) {
-    const int shares = gate_dw_shares(T, d, Ne, bf16);
-    // whole steps; the last shares may then be empty, and sum to zero
-    const unsigned per = ceil_div(ceil_div(T, shares), 64) * 64;
-    const int cols = ceil_div(d, bf16 ? kDwCols : kDwColsF);
-    const int groups = cols * static_cast<int>(ceil_div(Ne, kDwExperts));
-    const unsigned grid = share_grid(groups, shares);
-    float *out = shares > 1 ? part : dw;
-    if (bf16) {
-        const auto *xb = static_cast<const uint16_t *>(x);
-        if (Ne <= 16)
-            k_gate_dw<1><<<grid, kDwThreads, 0, s>>>(dl, xb, T, d, Ne, groups, cols, shares, per, out);
-        else if (Ne <= 32)
-            k_gate_dw<2><<<grid, kDwThreads, 0, s>>>(dl, xb, T, d, Ne, groups, cols, shares, per, out);
+    if (!bf16) {
+        // dx alone has more waves on a CU in its own kernel (T = 4096, d = 2048:
+        // 8 experts 16 us against 21, 250 47 against 49)
+        if (!dw)
+            tiles_alone(float{}, I2{}, I2{});
+        else if (dx && tiles_of(float{}, I2{}, I2{}))
+            k_gate_bwd_f32<true><<<W.blocks + X.blocks, kThreads, 0, s>>>(dl, T, d, Ne, W, X);
         else
-            k_gate_dw<4><<<grid, kDwThreads, 0, s>>>(dl, xb, T, d, Ne, groups, cols, shares, per, out);
+            k_gate_bwd_f32<false><<<W.blocks + X.blocks, kThreads, 0, s>>>(dl, T, d, Ne, W, X);
+    } else if (dx && Ne > 64) {
+        // W_r no longer fits a wave's registers.  dx alone: large tiles where
+        // there is one for every CU (130 experts, d = 2048: T = 4096 15.8 us
+        // against 16.0, T = 8192 25.7 against 30.5) and small ones below
+        // (T = 512 6.8 against 11.0).
+        if (!dw) {
+            if (static_cast<int64_t>(ceil_div(T, 128)) * ceil_div(d, 256) >= 256)
+                tiles_alone(uint16_t{}, I4{}, I4{});
+            else
+                tiles_alone(uint16_t{}, I2{}, I2{});
+        } else if (tiles_of(uint16_t{}, I4{}, I4{})) {
+            both(I4{}, integral_constant<int, kSmallTile>{}, kBfThreads);
+        } else {
+            both(I4{}, integral_constant<int, kTile>{}, kBfThreads);
+        }
     } else {
-        k_gate_dw_f32<<<grid, kThreads, 0, s>>>(dl, static_cast<const float *>(x), T, d, Ne, groups, cols,
-                                                shares, per, out);
+        // dx alone in smaller workgroups, for the same waves on more CUs
+        // (T = 256, d = 2048, 64 experts: 4.5 us against 5.9)
+        const int threads = dw ? kBfThreads : kThreads;
+        if (dx) {
+            // waves walk over enough token tiles to pay for their W_r fragments
+            X.groups = ceil_div(d, threads / kWave * kDxCols);
+            X.shares = std::min(ceil_div(2048 / (threads / kWave), X.groups), ceil_div(T, 16));
+            X.blocks = whole_xcds(share_grid(X.groups, X.shares));
+        }
+        const bool vec = Ne % 4 == 0 && reinterpret_cast<uintptr_t>(dl) % 16 == 0;
+        const auto run = [&](auto mb) {
+            if (vec)
+                both(mb, integral_constant<int, kRegsVec>{}, threads);
+            else
+                both(mb, integral_constant<int, kRegs>{}, threads);
+        };
+        if (Ne <= 16)
+            run(integral_constant<int, 1>{});
+        else if (Ne <= 32)
+            run(I2{});
+        else
+            run(I4{});
     }
-    if (shares > 1) {
+    if (W.shares > 1) {
         const size_t n4 = static_cast<size_t>(Ne) * d / 4;
         k_gate_dw_fold<<<ceil_div(n4, kFoldOut), kThreads, 0, s>>>(
-            reinterpret_cast<const f32x4 *>(part), shares, n4, reinterpret_cast<f32x4 *>(dw));
+            reinterpret_cast<const f32x4 *>(part), W.shares, n4, reinterpret_cast<f32x4 *>(dw));
     }
     return hipGetLastError();
 }

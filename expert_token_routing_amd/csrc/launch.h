@@ -256,12 +256,12 @@ hipError_t launch_balance_back(const float *logits, const uint8_t *valid, const 
 
 // --- gate projection, backward (gate_bwd.hip) ---
 // dx = dx_in + dl w_router (dx_in may be NULL);  dw = dl^T x through
-// gate_dw_shares x Ne x d partial sums in part.
+// gate_dw_shares x Ne x d partial sums in part.  NULL dx or dw: not computed.
+// dx may lie in x.
 int gate_dw_shares(int T, int d, int Ne, int bf16);
-hipError_t launch_gate_dx(const float *dl, const void *w_router, const void *dx_in, int T, int d,
-                          int Ne, int bf16, void *dx, hipStream_t s);
-hipError_t launch_gate_dw(const float *dl, const void *x, int T, int d, int Ne, int bf16,
-                          float *part, float *dw, hipStream_t s);
+hipError_t launch_gate_bwd(const float *dl, const void *x, const void *w_router, const void *dx_in,
+                           int T, int d, int Ne, int bf16, void *dx, float *part, float *dw,
+                           hipStream_t s);
 
 // --- optimizer step (adamw.hip) ---
 constexpr int64_t kAdamwMaxElements = 1ll << 33;  // of one tensor
