@@ -168,8 +168,10 @@ __global__ __launch_bounds__(kThreads) void k_adamw(Table tab, AdamwStep st) {
         const float gj = g[j] * gs;
         m[j] = fmaf(st.beta1, m[j], st.one_b1 * gj);
         v[j] = fmaf(st.beta2, v[j], st.one_b2 * gj * gj);
-        // hardware square root and reciprocal: 2^-23 relative of the step each
-        root[j] = __builtin_amdgcn_sqrtf(v[j]);
+        // hardware square root and reciprocal: 2^-23 relative of the step each;
+        // they take no subnormal value (eps keeps the divisor a normal one)
+        const bool low = v[j] < 0x1p-96f;
+        root[j] = __builtin_amdgcn_sqrtf(low ? 0x1p64f * v[j] : v[j]) * (low ? 0x1p-32f : 1.f);
         p[j] = fmaf(decay, p[j], -rate * (m[j] * __builtin_amdgcn_rcpf(fmaf(root[j], c2_rsqrt, st.eps))));
         copy[j] = f32_to_bf16_bits(p[j]);
     }

@@ -1,6 +1,7 @@
 // C ABI of the Occult MoE-layer library: argument checks, workspace layout,
 // and the stage sequence of the layer (declarations and contracts in occ.h).
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 #include <vector>
@@ -321,6 +322,12 @@ bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p)
 template <typename... P>
 bool rows_aligned(P... p) {
     return (aligned_to(p, 16) && ...);
+}
+
+// Whether this output (or NULL) is none of these arrays.
+template <typename... P>
+bool apart(const void *out, P... p) {
+    return !out || ((out != static_cast<const void *>(p)) && ...);
 }
 
 int row_chunks(const occ_layer_desc &D) { return static_cast<int>(D.d * elem_bytes(D) / 16); }
@@ -700,7 +707,9 @@ occ_status occ_block_norm(const occ_layer_desc *desc, const occ_norm_desc *opt, 
     OCC_TRY(check_norm(desc, opt));
     if (!x || !gate_fits(*opt, gate) || !w_pre != !h) return OCC_ERR_INVALID_ARG;
     if (y ? !r : r || w_post || gate || !h) return OCC_ERR_INVALID_ARG;
-    if (!rows_aligned(x, y, w_post, w_pre, r, h)) return OCC_ERR_INVALID_ARG;
+    if (!rows_aligned(x, y, w_post, w_pre, r, h) || !apart(r, h, w_post, gate, w_pre) ||
+        !apart(h, w_post, gate, w_pre))
+        return OCC_ERR_INVALID_ARG;
     OCC_HIP(launch_block_norm(x, y, w_post, gate, w_pre, desc->T, desc->d,
                               desc->dtype == OCC_BF16, opt->gate, opt->eps, opt->scale, r, h,
                               static_cast<hipStream_t>(stream)));
@@ -722,6 +731,12 @@ occ_status occ_block_norm_backward(const occ_layer_desc *desc, const occ_norm_de
     if (!rows_aligned(dr, dh, r, y, w_post, w_pre, dx, dy) || !aligned_to(dw_post, 4) ||
         !aligned_to(dgate, 4) || !aligned_to(dw_pre, 4))
         return OCC_ERR_INVALID_ARG;
+    if (!apart(dx, dy, w_post, gate, w_pre, dw_post, dgate, dw_pre) ||
+        !apart(dy, w_post, gate, w_pre, dw_post, dgate, dw_pre) ||
+        !apart(dw_post, dr, dh, r, y, w_post, gate, w_pre, dgate, dw_pre) ||
+        !apart(dw_pre, dr, dh, r, y, w_post, gate, w_pre, dgate) ||
+        !apart(dgate, dr, dh, r, y, w_post, w_pre, opt->gate == OCC_GATE_TOKEN ? nullptr : gate))
+        return OCC_ERR_INVALID_ARG;
     OCC_TRY(check_ws(*desc, workspace, ws_bytes, block_ws_bytes(*desc)));
     OCC_HIP(launch_block_norm_back(dr, dh, r, y, w_post, gate, w_pre, desc->T, desc->d,
                                    desc->dtype == OCC_BF16, opt->gate, opt->eps, opt->scale, dx,
@@ -737,7 +752,8 @@ occ_status occ_balance_loss(const occ_layer_desc *desc, const occ_balance_desc *
     OCC_TRY(check_desc(desc));
     if (!logits || !ids || !counts || !probs || !loss) return OCC_ERR_INVALID_ARG;
     if (!aligned_to(logits, 4) || !aligned_to(ids, 4) || !aligned_to(counts, 4) ||
-        !aligned_to(probs, 4) || !aligned_to(loss, 4))
+        !aligned_to(probs, 4) || !aligned_to(loss, 4) || !apart(counts, logits, ids, valid, probs, loss) ||
+        !apart(probs, logits, ids, valid, loss) || !apart(loss, logits, ids, valid))
         return OCC_ERR_INVALID_ARG;
     PlaceTab tab;
     OCC_TRY(balance_tab(*desc, opt, placement_host, &tab));
@@ -755,7 +771,7 @@ occ_status occ_balance_backward(const occ_layer_desc *desc, const occ_balance_de
     OCC_TRY(check_desc(desc));
     if (!logits || !counts || !dlogits || !std::isfinite(dloss)) return OCC_ERR_INVALID_ARG;
     if (!aligned_to(logits, 4) || !aligned_to(counts, 4) || !aligned_to(dlogits_in, 4) ||
-        !aligned_to(dlogits, 4))
+        !aligned_to(dlogits, 4) || !apart(dlogits, valid, counts))
         return OCC_ERR_INVALID_ARG;
     PlaceTab tab;
     OCC_TRY(balance_tab(*desc, opt, placement_host, &tab));
@@ -772,7 +788,8 @@ occ_status occ_gate_backward(const occ_layer_desc *desc, const float *dlogits, c
     if (!dlogits || (!dx && !dw_router)) return OCC_ERR_INVALID_ARG;
     if (dx ? !w_router : !!dx_in) return OCC_ERR_INVALID_ARG;
     if (dw_router && !x) return OCC_ERR_INVALID_ARG;
-    if (!aligned_to(dlogits, 4) || !rows_aligned(x, w_router, dx_in, dx, dw_router))
+    if (!aligned_to(dlogits, 4) || !rows_aligned(x, w_router, dx_in, dx, dw_router) ||
+        !apart(dx, dlogits, w_router) || !apart(dw_router, dlogits, x, w_router, dx_in, dx))
         return OCC_ERR_INVALID_ARG;
     if (dw_router) OCC_TRY(check_ws(*desc, workspace, ws_bytes, block_ws_bytes(*desc)));
     const int bf16 = desc->dtype == OCC_BF16;
@@ -791,15 +808,17 @@ occ_status occ_adamw_step(const occ_adamw_desc *opt, const occ_adamw_tensor *ten
     if ((opt->state != OCC_ADAMW_32BIT && opt->state != OCC_ADAMW_8BIT) ||
         (opt->grad_dtype != OCC_F32 && opt->grad_dtype != OCC_BF16) || !ranged(opt->lr, 0., false) ||
         !ranged(opt->beta1, 0., false) || opt->beta1 >= 1. || !ranged(opt->beta2, 0., false) ||
-        opt->beta2 >= 1. || !(static_cast<float>(opt->eps) > 0.f) || !std::isfinite(opt->eps) ||
+        opt->beta2 >= 1. || !(static_cast<float>(opt->eps) >= FLT_MIN) || !std::isfinite(opt->eps) ||
         !ranged(opt->weight_decay, 0., false) || !std::isfinite(opt->grad_scale) || opt->step < 1 ||
         !aligned_to(dynamic, 4))
         return OCC_ERR_INVALID_ARG;
     const bool q8 = opt->state == OCC_ADAMW_8BIT, gb = opt->grad_dtype == OCC_BF16;
     const size_t ms = q8 ? 1 : 4;
     std::vector<AdamwTensor> list;
+    std::vector<const void *> written;  // each once
     try {
         list.reserve(count);
+        written.reserve(static_cast<size_t>(count) * 3);
     } catch (...) {
         return OCC_ERR_UNSUPPORTED;
     }
@@ -823,7 +842,11 @@ occ_status occ_adamw_step(const occ_adamw_desc *opt, const occ_adamw_tensor *ten
             return OCC_ERR_INVALID_ARG;
         list.push_back({t.n, t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.p_out, t.m_out, t.v_out,
                         t.m_scale_out, t.v_scale_out, t.p_bf16, fits(4)});
+        written.insert(written.end(), {t.p_out, t.m_out, t.v_out});
     }
+    std::sort(written.begin(), written.end());
+    if (std::adjacent_find(written.begin(), written.end()) != written.end())
+        return OCC_ERR_INVALID_ARG;
     AdamwStep st;
     const double step = static_cast<double>(opt->step);
     st.lr = static_cast<float>(opt->lr);

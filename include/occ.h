@@ -416,9 +416,12 @@ occ_status occ_moe_backward(const occ_layer_desc *desc, const void *dy, const vo
  * The operators below take the layer's descriptor, of which each uses the
  * fields it names; the pointer, stream and error rules are the same.  Row
  * tensors (T x d) and weights handed to them must be 16-byte aligned, other
- * arrays aligned to their elements (INVALID_ARG otherwise).  An output may be
- * the very same array as an input of the same type and shape; otherwise
- * outputs overlap nothing.  All of them are deterministic: no atomic
+ * arrays aligned to their elements (INVALID_ARG otherwise).  An output of rows
+ * may be the very same array as an input of the same rows: r or h as x or y,
+ * dx or dy as dr, dh, r or y, a token gate's dgate as gate, dlogits as logits
+ * or dlogits_in, occ_gate_backward's dx as x or dx_in.  Otherwise outputs
+ * overlap nothing (INVALID_ARG where they start like another array of the
+ * call).  All of them are deterministic: no atomic
  * additions of floating-point values, sums in an order fixed by the sizes. */
 
 /* Bytes of device workspace that occ_block_norm_backward, occ_balance_loss
@@ -572,7 +575,7 @@ typedef struct occ_adamw_desc {
     int32_t grad_dtype;  /* occ_dtype of the gradients */
     double lr;           /* >= 0 */
     double beta1, beta2; /* in [0, 1) */
-    double eps;          /* > 0 */
+    double eps;          /* >= FLT_MIN */
     double weight_decay; /* >= 0, decoupled */
     double grad_scale;   /* gradients are multiplied by it (1 / loss scale, a clip factor) */
     int64_t step;        /* 1 for the first step */
@@ -582,7 +585,9 @@ typedef struct occ_adamw_desc {
  * it is the new value of (the usual step in place) or another one; m_scale
  * and v_scale (ceil(n / OCC_ADAMW_BLOCK) fp32) only with 8-bit states, NULL
  * otherwise.  p is fp32; p_bf16 is NULL or receives the new p rounded to
- * bf16, the copy that the layer computes with. */
+ * bf16, the copy that the layer computes with.  Within a call each p_out, m_out
+ * and v_out is another array (a tensor listed twice would be updated twice at
+ * once). */
 typedef struct occ_adamw_tensor {
     int64_t n;
     const float *p;
@@ -605,8 +610,8 @@ typedef struct occ_adamw_tensor {
  * A gradient that is not finite makes its element's p, m and v so (with 8-bit
  * states its whole block's); tensors aligned to 16 bytes are faster.
  * Errors: INVALID_ARG (a value out of the ranges above, a missing or
- * superfluous pointer, an array not aligned to its elements), UNSUPPORTED
- * (n > 2^33). */
+ * superfluous pointer, an array not aligned to its elements, the same p_out,
+ * m_out or v_out twice), UNSUPPORTED (n > 2^33). */
 occ_status occ_adamw_step(const occ_adamw_desc *opt, const occ_adamw_tensor *tensors_host,
                           int32_t count, const float *dynamic, void *stream);
 

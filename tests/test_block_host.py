@@ -164,6 +164,12 @@ def test_norm_refuses_pointers(L, over):
     assert norm_status(L, **over) == INV
 
 
+@pytest.mark.parametrize("over", [dict(r=fake(6)), dict(r=fake(3)), dict(h=fake(3)),
+                                  dict(h=fake(4))])
+def test_norm_refuses_an_output_in_another_array(L, over):
+    assert norm_status(L, **over) == INV
+
+
 @pytest.mark.parametrize("kind", [1, 2])
 def test_norm_refuses_a_missing_gate(L, kind):
     assert norm_status(L, opt=occ.NormDesc(eps=1e-6, scale=1.0, gate=kind)) == INV
@@ -207,6 +213,16 @@ def norm_back_status(L, desc=None, opt=None, **over):
 ])
 def test_norm_backward_refuses_pointers(L, over, code):
     assert norm_back_status(L, **over) == code
+
+
+@pytest.mark.parametrize("over", [
+    dict(dx=fake(8)), dict(dx=fake(6)), dict(dy=fake(5)), dict(dw_post=fake(5)),
+    dict(dw_pre=fake(5)), dict(dw_post=fake(10)), dict(dw_pre=fake(7)), dict(dw_pre=fake(2)),
+    dict(dgate=fake(12)), dict(dgate=fake(9)),
+])
+def test_norm_backward_refuses_an_output_in_another_array(L, over):
+    opt = occ.NormDesc(eps=1e-6, scale=1.0, gate=1)
+    assert norm_back_status(L, opt=opt, **{**dict(gate=fake(12), dgate=fake(13)), **over}) == INV
 
 
 def test_norm_backward_refuses_a_gate_without_its_gradient(L):
@@ -276,6 +292,17 @@ def test_balance_refuses_coefficients_placements_and_workspaces(L):
     assert balance_status(L, ws_bytes=16) == WS
 
 
+@pytest.mark.parametrize("over", [dict(counts=fake(4)), dict(counts=fake(2)), dict(probs=fake(1)),
+                                  dict(loss=fake(3)), dict(loss=fake(4)), dict(valid=fake(5))])
+def test_balance_refuses_an_output_in_another_array(L, over):
+    assert balance_status(L, **over) == INV
+
+
+@pytest.mark.parametrize("over", [dict(dlogits=fake(2)), dict(valid=fake(4))])
+def test_balance_backward_refuses_an_output_in_another_array(L, over):
+    assert balance_back_status(L, **over) == INV
+
+
 def gate_status(L, **over):
     a = dict(dlogits=fake(1), x=fake(2), w_router=fake(3), dx_in=fake(4), dx=fake(5),
              dw=fake(6), ws=fake(7), ws_bytes=BIG)
@@ -290,6 +317,8 @@ def gate_status(L, **over):
     (dict(w_router=NULL), INV), (dict(x=NULL), INV),
     (dict(x=ctypes.c_void_p(0x1008)), INV), (dict(dw=ctypes.c_void_p(0x1004)), INV),
     (dict(dlogits=ctypes.c_void_p(0x1002)), INV),
+    (dict(dx=fake(1)), INV), (dict(dx=fake(3)), INV), (dict(dx=fake(6)), INV),
+    *[(dict(dw=fake(n)), INV) for n in (1, 2, 3, 4)],
     (dict(ws=NULL), WS), (dict(ws_bytes=16), WS), (dict(ws=ctypes.c_void_p(0x1010)), WS),
 ])
 def test_gate_backward_refuses(L, over, code):
@@ -351,6 +380,23 @@ def test_adamw_refuses_counts_and_dynamic(L):
     desc = occ.AdamwDesc(**ADAM)
     assert L.occ_adamw_step(ctypes.byref(desc), None, 1, NULL, NULL) == INV
     assert L.occ_adamw_step(None, None, 0, NULL, NULL) == INV
+
+
+@pytest.mark.parametrize("eps,code", [(1.1e-38, INV), (1e-45, INV), (1.2e-38, occ.OCC_OK)])
+def test_adamw_takes_an_eps_that_is_a_normal_number(L, eps, code):
+    assert adam_status(L, opt=dict(eps=eps), count=0) == code
+
+
+@pytest.mark.parametrize("second", [dict(), dict(m=0x7000, m_out=0x7000, v=0x8000, v_out=0x8000),
+                                    dict(p=0x6000, p_out=0x6000, v=0x8000, v_out=0x8000),
+                                    dict(p=0x6000, p_out=0x6000, m=0x4000, m_out=0x4000)])
+def test_adamw_refuses_an_array_written_twice(L, second):
+    one = dict(n=8, p=0x1000, g=0x2000, m=0x3000, v=0x4000, p_out=0x1000, m_out=0x3000,
+               v_out=0x4000)
+    rows = (occ.AdamwTensor * 2)(occ.AdamwTensor(**one), occ.AdamwTensor(**{**one, **second}))
+    desc = occ.AdamwDesc(**ADAM)
+    assert L.occ_adamw_step(ctypes.byref(desc), rows, 2, NULL, NULL) == INV
+    assert adam_status(L, tensor=dict(v_out=0x3000)) == INV
 
 
 def test_binding_refuses_host_tensors_and_tables_that_do_not_fit(L):

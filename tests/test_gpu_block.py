@@ -209,6 +209,30 @@ def test_norm_in_place_and_repeated_bitwise():
         assert torch.equal(dr, out["dx"]) and torch.equal(dh, out["dy"])
 
 
+@pytest.mark.parametrize("dtype,T,d", [(BF16, 3001, 128), (BF16, 1100, 2048), (F32, 900, 4096)])
+@pytest.mark.parametrize("form", ["token", "channel"])
+def test_norm_outputs_over_any_input_of_the_same_rows(form, dtype, T, d):
+    t, grads, opt = norm_inputs(dtype, T, d, form, seed=5)
+    r, h = run_norm(t, opt, dtype)
+    want = run_norm_back(t, grads, r, opt, dtype)
+    desc, ws = layer(T, d, dtype=dtype), occ.alloc_block_workspace(layer(T, d, dtype=dtype))
+    for r_at, h_at in (("y", "x"), ("x", None), (None, "x"), ("y", None), (None, "y")):
+        rows = {"x": t["x"].clone(), "y": t["y"].clone()}
+        r2, h2 = rows.get(r_at, nan_like((T, d), dtype)), rows.get(h_at, nan_like((T, d), dtype))
+        occ.occ_block_norm(desc, opt, rows["x"], rows["y"], t["w_post"], t["gate"], t["w_pre"], r2, h2)
+        assert torch.equal(r2, r) and torch.equal(h2, h), (r_at, h_at)
+    for dx_at, dy_at in (("dh", "dr"), ("r", "y"), ("y", "r"), ("r", "dh")):
+        rows = {"dr": grads["dr"].clone(), "dh": grads["dh"].clone(), "r": r.clone(), "y": t["y"].clone()}
+        gate = t["gate"].clone()
+        dgate = gate if form == "token" else nan_like((d,))
+        dw = [nan_like((d,)) for _ in range(2)]
+        occ.occ_block_norm_backward(desc, opt, rows["dr"], rows["dh"], rows["r"], rows["y"],
+                                    t["w_post"], gate, t["w_pre"], rows[dx_at], rows[dy_at], dw[0],
+                                    dgate, dw[1], ws)
+        got = dict(dx=rows[dx_at], dy=rows[dy_at], dw_post=dw[0], dgate=dgate, dw_pre=dw[1])
+        assert all(torch.equal(got[key], want[key]) for key in got), (dx_at, dy_at)
+
+
 # -------------------------------------------------------------- router losses
 
 COEF = (0.3, 0.2, 0.05)
@@ -532,6 +556,25 @@ def test_adamw_over_more_tensors_than_a_launch_holds_some_empty(bits):
     for b, t in zip(before, full):
         if t["p"].numel():
             check_adam(b, after_of(t), bits)
+
+
+def test_adamw_steps_from_gradients_whose_squares_are_subnormal():
+    """v from 2^-106 down to 2^-134: products and sums round to steps of 2^-149 there, which two
+    roundings move by 2^-149 together, and the root halves what that is of v."""
+    n, g = 5000, gen(19)
+    a = {**ADAM, "eps": 1e-30, "step": 1, "grad_scale": 1.0}
+    size = torch.exp2(-51 - 13.5 * torch.rand(n, generator=g, device="cuda"))
+    t = dict(p=1e-3 * randn(g, n), g=size * torch.sign(randn(g, n)),
+             m=torch.zeros(n, device="cuda"), v=torch.zeros(n, device="cuda"))
+    b = {key: v.clone() for key, v in t.items()}
+    opt = adam_desc(32, F32, **{key: a[key] for key in ("eps", "step", "grad_scale")})
+    occ.occ_adamw_step(opt, occ.AdamwTensors(opt, [t]))
+    p, m, v, _ = ref.adamw(b["p"].double(), b["g"].double(), b["m"].double(), b["v"].double(), a)
+    assert (v < 2.0 ** -104).all() and (v > 2.0 ** -136).all()
+    assert ((t["v"].double() - v).abs() <= 6 * U * v + 2.0 ** -149).all()
+    step = a["lr"]  # from zero moments each step is lr in size
+    assert ((t["p"].double() - p).abs() <=
+            2 * U * p.abs() + step * (24 * U + 2.0 ** -150 / v) * (1 + 1e-2)).all()
 
 
 def test_adamw_first_steps_from_zero_states_follow_64_bits():
