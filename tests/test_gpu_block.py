@@ -675,6 +675,57 @@ def test_adamw_largest_sizes_reach_the_last_element():
     assert (t["m"][at].float() == 448).all()
 
 
+# Arrays of more than 2^31 elements, zero but for their last rows: the sums over the tokens are
+# those rows', and what lies in front of them stays zero.
+LAST = 1000
+
+
+def behind_zeros(T, v):
+    out = torch.zeros(T, *v.shape[1:], dtype=v.dtype, device="cuda")
+    out[-v.shape[0]:] = v
+    return out
+
+
+def only_last(full):
+    """The last rows of an array whose other rows are zero (looked at in pieces)."""
+    for part in full[:-LAST].split(1 << 17):
+        assert not part.any()
+    return full[-LAST:]
+
+
+@pytest.mark.parametrize("dtype,T,d", [(BF16, 1100003, 2048), (BF16, 300001, 8192),
+                                       (F32, 530003, 4096)])
+def test_norm_rows_behind_two_to_the_31_elements(dtype, T, d):
+    t, grads, opt = norm_inputs(dtype, LAST, d, "channel", seed=d)
+    full = {key: behind_zeros(T, v) if v.dim() == 2 else v for key, v in t.items()}
+    r, h = run_norm(full, opt, dtype)
+    check_norm(t, opt, only_last(r), only_last(h))
+    big = {key: behind_zeros(T, v) for key, v in grads.items()}
+    out = run_norm_back(full, big, r, opt, dtype)
+    small = {key: only_last(v) if v.dim() == 2 else v for key, v in out.items()}
+    check_norm_back(t, grads, r[-LAST:], opt, small)
+
+
+@pytest.mark.parametrize("dtype,T,d,Ne", [(BF16, 1100003, 2048, 60), (BF16, 1100003, 2048, 100),
+                                          (F32, 530003, 4096, 70)])
+def test_gate_backward_rows_behind_two_to_the_31_elements(dtype, T, d, Ne):
+    dl, x, w, dx_in = gate_inputs(dtype, LAST, d, Ne, seed=Ne)
+    desc = layer(T, d, Ne=Ne, dtype=dtype)
+    dx, dw = nan_like((T, d), dtype), nan_like((Ne, d))
+    occ.occ_gate_backward(desc, behind_zeros(T, dl), behind_zeros(T, x), w,
+                          behind_zeros(T, dx_in), dx, dw, occ.alloc_block_workspace(desc))
+    check_gate(dl, x, w, dx_in, only_last(dx), dw, LAST, Ne, dtype)
+
+
+def test_balance_rows_behind_two_to_the_31_elements():
+    T, Ne, k, Nd = (1 << 24) + 7, 129, 4, 3
+    logits, ids, _, place, group = balance_inputs(LAST, Ne, k, Nd, "none", seed=3)
+    valid = behind_zeros(T, torch.ones(LAST, dtype=torch.bool, device="cuda"))
+    got = run_balance(T, Ne, k, Nd, behind_zeros(T, logits), behind_zeros(T, ids), valid,
+                      place, None)
+    check_balance(logits, ids, None, group, k, None, (*got[:3], only_last(got[3])))
+
+
 # ------------------------------------------------- streams, graphs, together
 
 def test_operators_on_a_side_stream():
