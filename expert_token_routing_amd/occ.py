@@ -414,19 +414,30 @@ def _device(t: torch.Tensor | None) -> int:
     return -1 if t is None else t.get_device()
 
 
+def _current(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the current stream's handle without an object around it (0.1 us instead of 1.1, where a small
+# call takes 7)
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", _current)
+
+
 def _queue(what: str, fn, index: int, stream, *args):
     """fn(*args, stream) with device `index` as the current one."""
     if index < 0:
         raise OccError(OCC_ERR_INVALID_ARG, what)
     if stream is None:
-        stream = torch.cuda.current_stream(index)
+        stream = _current(index)
     elif stream.device.index != index:
         raise ValueError(f"{what}: tensors on cuda:{index}, stream on {stream.device}")
+    else:
+        stream = stream.cuda_stream
     if torch.cuda.current_device() == index:
-        status = fn(*args, stream.cuda_stream)
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(index):
-            status = fn(*args, stream.cuda_stream)
+            status = fn(*args, stream)
     if status != OCC_OK:
         raise OccError(status, what)
 
