@@ -12,8 +12,8 @@
 // Bound by latency at a training step's smaller batches and by reading the
 // logits (4 T Ne bytes each way) at the largest.  A token's softmax takes a
 // team of 16, 32 or 64 lanes, the fewest that hold its logits as at most four
-// per lane (expert l + L i with lane l), so that a wave works on up to four
-// tokens and reduces over a team in 4 to 6 lane exchanges.  The forward adds
+// per lane (consecutive ones, one vector, or expert l + L i with lane l), so
+// that a wave works on up to four tokens and reduces over a team in 4 to 6 lane exchanges.  The forward adds
 // p in registers over a workgroup's tokens and counts in LDS with integer
 // atomics (whose order changes nothing); each workgroup leaves its sums in
 // the workspace and one workgroup adds them, in a fixed order and in fp64.
@@ -21,8 +21,9 @@
 // backward's coefficients) and a step ahead of their softmax.  exp and log are
 // the hardware's base-2 ones behind a product with log2 e or ln 2: an error
 // of u |l - max| in p beside expf's, the size that the rounding of l - max has.
-// Measured at T = 65536, Ne = 60 (mask, k = 4): 8.6 + 5.6 us forward, 11.7 us
-// backward for 47 MB; at T = 512, Ne = 64: 10.2 and 4.6 us.
+// Measured at T = 65536, Ne = 60 (mask, k = 4): 6.4 + 5.8 us forward, 10.1 us
+// backward for 48 MB (10.8 with a load for each logit); at T = 512, Ne = 64:
+// 7.8 and 4.0 us.
 #include <algorithm>
 
 #include "launch.h"
@@ -33,17 +34,36 @@ namespace {
 constexpr int kBalThreads = 1024;
 constexpr int kBalWaves = kBalThreads / kWave;
 constexpr int kBackThreads = 512;
-constexpr int kTokens = 2;  // tokens that a forward team has in flight
 
-// A token's logits, expert l + L i in x[i] and -inf behind Ne.
-template <int L, int NI>
-__device__ __forceinline__ void team_load(const float *__restrict__ row, bool in, int l, int Ne,
+// Loads come a step ahead of their use and are unconditional, so that none
+// waits for another: what lies behind the last expert or token is the last
+// one's again, and left out when it is used.  A wave's tokens share a scalar
+// base; `row` is the token's distance from it.
+template <int L, int NI, bool VEC>
+__device__ __forceinline__ int expert(int l, int i) {
+    return VEC ? NI * l + i : l + L * i;
+}
+template <int L, int NI, bool VEC>
+__device__ __forceinline__ void team_load(const float *base, unsigned row, int l, int Ne,
                                           float (&x)[NI]) {
+    const char *at = reinterpret_cast<const char *>(base);
+    if constexpr (VEC) {
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(at + 4 * (row * Ne + min(4 * l, Ne - 4)));
 #pragma unroll
-    for (int i = 0; i < NI; i++) {
-        const int e = l + L * i;
-        x[i] = in && e < Ne ? row[e] : -INFINITY;
+        for (int i = 0; i < 4; i++) x[i] = v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; i++)
+            x[i] = *reinterpret_cast<const float *>(at + 4 * (row * Ne + min(l + L * i, Ne - 1)));
     }
+}
+
+// A token's logits: -inf behind Ne, and everywhere when the token does not
+// count.
+template <int L, int NI, bool VEC>
+__device__ __forceinline__ void team_mask(bool in, int l, int Ne, float (&x)[NI]) {
+#pragma unroll
+    for (int i = 0; i < NI; i++) x[i] = in && expert<L, NI, VEC>(l, i) < Ne ? x[i] : -INFINITY;
 }
 
 // Their softmax in place (0 behind Ne); returns their log-sum-exp.  A row of
@@ -62,11 +82,13 @@ __device__ __forceinline__ float team_softmax(float (&p)[NI]) {
         s += p[i];
     }
     s = group_sum<L>(s);
+    // s is 0 or in [1, 256]: the hardware's reciprocal and logarithm (2^-23
+    // relative each) need no care for subnormal values
     const bool none = s == 0.f;
-    const float inv = none ? 0.f : 1.f / s;
+    const float inv = none ? 0.f : __builtin_amdgcn_rcpf(s);
 #pragma unroll
     for (int i = 0; i < NI; i++) p[i] *= inv;
-    return none ? 0.f : shift + __logf(s);
+    return none ? 0.f : fmaf(__builtin_amdgcn_logf(s), 0x1.62e43p-1f, shift);
 }
 
 // One workgroup's part: prob sums (Ne floats), z sum, then counts (Ne) and
@@ -139,7 +161,7 @@ __device__ __forceinline__ void finish(double p, int c, int shares, int Ne, int 
 
 // Workgroup b's tokens are [b per_block, ...).  A single workgroup finishes;
 // of several each leaves its sums in part.
-template <int L, int NI>
+template <int L, int NI, bool VEC>
 __global__ __launch_bounds__(kBalThreads) void k_balance(const float *__restrict__ logits,
                                                          const int32_t *__restrict__ ids,
                                                          const uint8_t *__restrict__ valid,
@@ -156,15 +178,14 @@ __global__ __launch_bounds__(kBalThreads) void k_balance(const float *__restrict
     const int l = threadIdx.x % L, team = threadIdx.x / L;
     const int w = threadIdx.x / kWave, lane = lane_id();
 
-    float p[kTokens][NI];
-    bool in[kTokens];
+    float pn[NI];
+    uint8_t ok;
+    const float *base = logits + static_cast<size_t>(t0) * Ne;
+    const uint8_t *mask = valid ? valid : reinterpret_cast<const uint8_t *>(logits);
     auto load = [&](unsigned t) {
-#pragma unroll
-        for (int u = 0; u < kTokens; u++) {
-            const unsigned tu = t + u * kTeams;
-            in[u] = tu < t1 && (!valid || valid[tu]);
-            team_load<L, NI>(logits + static_cast<size_t>(tu) * Ne, in[u], l, Ne, p[u]);
-        }
+        t = min(t, t1 - 1);
+        ok = mask[t];
+        team_load<L, NI, VEC>(base, t - t0, l, Ne, pn);
     };
     load(t0 + team);
 
@@ -191,24 +212,24 @@ __global__ __launch_bounds__(kBalThreads) void k_balance(const float *__restrict
     float acc[NI], z = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; i++) acc[i] = 0.f;
-    for (unsigned t = t0 + team; t < t1;) {
+    for (unsigned t = t0 + team; t < t1; t += kTeams) {
+        float p[NI];
 #pragma unroll
-        for (int u = 0; u < kTokens; u++) {
-            // a token that does not count is a row of -inf: p = 0, lse = 0
-            const float lse = team_softmax<L, NI>(p[u]);
+        for (int i = 0; i < NI; i++) p[i] = pn[i];
+        team_mask<L, NI, VEC>(!valid || ok, l, Ne, p);
+        load(t + kTeams);
+        // a token that does not count is a row of -inf: p = 0, lse = 0
+        const float lse = team_softmax<L, NI>(p);
 #pragma unroll
-            for (int i = 0; i < NI; i++) acc[i] += p[u][i];
-            z = fmaf(lse, lse, z);
-        }
-        t += kTeams * kTokens;
-        load(t);
+        for (int i = 0; i < NI; i++) acc[i] += p[i];
+        z = fmaf(lse, lse, z);
     }
     // the teams of a wave, then the waves in order
 #pragma unroll
     for (int i = 0; i < NI; i++) {
         if constexpr (L <= 16) acc[i] += __shfl_xor(acc[i], 16);
         if constexpr (L <= 32) acc[i] += __shfl_xor(acc[i], 32);
-        const int e = l + L * i;
+        const int e = expert<L, NI, VEC>(l, i);
         if (lane < L && e < Ne) s_w[w][e] = acc[i];
     }
     if constexpr (L <= 16) z += __shfl_xor(z, 16);
@@ -247,7 +268,7 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_final(const float *__re
     finish(p, c, shares, Ne, k, tab, o);
 }
 
-template <int L, int NI>
+template <int L, int NI, bool VEC>
 __global__ __launch_bounds__(kBackThreads) void k_balance_back(
     const float *logits, const uint8_t *__restrict__ valid, const int32_t *__restrict__ counts,
     PlaceTab tab, unsigned T, int Ne, int k, float cb, float cg, float cz, float dloss,
@@ -256,20 +277,20 @@ __global__ __launch_bounds__(kBackThreads) void k_balance_back(
     __shared__ float s_f[kMaxNe], s_c[kMaxNe];
     const int l = threadIdx.x % L;
     const unsigned stride = gridDim.x * kTeams;
-    float p[NI], g[NI];
-    bool in;
-    auto load = [&](unsigned t) {
+    float pn[NI], gn[NI];
+    uint8_t ok;
+    const uint8_t *mask = valid ? valid : reinterpret_cast<const uint8_t *>(logits);
+    const float *into = dlogits_in ? dlogits_in : logits;
+    const unsigned team = threadIdx.x / L;
+    auto load = [&](unsigned t) {  // t: the workgroup's first token
+        t = min(t, T - 1);
+        const unsigned row = min(team, T - 1 - t);
         const size_t base = static_cast<size_t>(t) * Ne;
-        in = t < T && (!valid || valid[t]);
-        team_load<L, NI>(logits + base, in, l, Ne, p);
-#pragma unroll
-        for (int i = 0; i < NI; i++) {
-            const int e = l + L * i;
-            g[i] = dlogits_in && t < T && e < Ne ? dlogits_in[base + e] : 0.f;
-        }
+        ok = mask[t + row];
+        team_load<L, NI, VEC>(logits + base, row, l, Ne, pn);
+        team_load<L, NI, VEC>(into + base, row, l, Ne, gn);
     };
-    const unsigned first = blockIdx.x * kTeams + threadIdx.x / L;
-    load(first);  // in flight while the workgroup makes its coefficients
+    load(blockIdx.x * kTeams);  // in flight while the workgroup makes its coefficients
     const int n = counts[Ne];
     for (int e = threadIdx.x; e < Ne; e += kBackThreads)
         s_f[e] = n ? static_cast<float>(counts[e]) * Ne / (static_cast<float>(k) * n) : 0.f;
@@ -287,58 +308,86 @@ __global__ __launch_bounds__(kBackThreads) void k_balance_back(
     __syncthreads();
     float c[NI];
 #pragma unroll
-    for (int i = 0; i < NI; i++) c[i] = l + L * i < Ne ? s_c[l + L * i] : 0.f;
+    for (int i = 0; i < NI; i++) {
+        const int e = expert<L, NI, VEC>(l, i);
+        c[i] = e < Ne ? s_c[e] : 0.f;
+    }
     const float up = n ? dloss / n : 0.f;
-    for (unsigned t = first; t < T;) {
-        float dot = 0.f;
+    for (unsigned t = blockIdx.x * kTeams; t < T; t += stride) {
+        float p[NI], g[NI], dot = 0.f;
+        const bool in = !valid || ok;
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            p[i] = pn[i];
+            g[i] = dlogits_in ? gn[i] : 0.f;
+        }
+        team_mask<L, NI, VEC>(in, l, Ne, p);
+        load(t + stride);
         const float lse = team_softmax<L, NI>(p);
 #pragma unroll
         for (int i = 0; i < NI; i++) dot = fmaf(c[i], p[i], dot);
         const float add = 2.f * cz * lse - group_sum<L>(dot);
+        // a token that does not count keeps what came in
 #pragma unroll
-        for (int i = 0; i < NI; i++) {
-            const int e = l + L * i;
-            // a token that does not count keeps what came in
-            if (e < Ne)
-                dlogits[static_cast<size_t>(t) * Ne + e] =
-                    in ? fmaf(up * p[i], c[i] + add, g[i]) : g[i];
+        for (int i = 0; i < NI; i++) g[i] = in ? fmaf(up * p[i], c[i] + add, g[i]) : g[i];
+        if (t + team >= T) continue;
+        float *to = dlogits + static_cast<size_t>(t + team) * Ne;
+        if constexpr (VEC) {
+            if (4 * l < Ne) *reinterpret_cast<f32x4 *>(to + 4 * l) = f32x4{g[0], g[1], g[2], g[3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < NI; i++)
+                if (l + L * i < Ne) to[l + L * i] = g[i];
         }
-        t += stride;
-        load(t);
     }
 }
 
-// f(L, NI): the smallest team that holds Ne logits.
+// f(L, NI, VEC): the smallest team that holds Ne logits, four consecutive
+// ones to a lane where they can be moved as one vector.
 template <typename F>
-void by_experts(int Ne, F f) {
+void by_experts(int Ne, bool aligned, F f) {
     using std::integral_constant;
+    typedef integral_constant<int, 4> I4;
+    const bool vec = aligned && Ne % 4 == 0;
+    const auto four = [&](auto L) {
+        if (vec)
+            f(L, I4{}, std::true_type{});
+        else
+            f(L, I4{}, std::false_type{});
+    };
     if (Ne <= 16)
-        f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+        f(integral_constant<int, 16>{}, integral_constant<int, 1>{}, std::false_type{});
     else if (Ne <= 32)
-        f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+        f(integral_constant<int, 16>{}, integral_constant<int, 2>{}, std::false_type{});
     else if (Ne <= 64)
-        f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+        four(integral_constant<int, 16>{});
     else if (Ne <= 128)
-        f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+        four(integral_constant<int, 32>{});
     else
-        f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+        four(integral_constant<int, 64>{});
+}
+bool vector_aligned(const float *a, const float *b = nullptr, const float *c = nullptr) {
+    return (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+            reinterpret_cast<uintptr_t>(c)) % 16 == 0;
 }
 
-// Forward workgroups at most: one per CU (at T = 65536, Ne = 60 8.6 us and 5.7
-// for the sum of the parts; two per CU 8.6 and 7.9, half as many 12.6 and 4.5).
+// Forward workgroups at most: one per CU (at T = 65536, Ne = 60 6.4 us and 5.8
+// for the sum of the parts; half as many 8.3 and 4.7).
 constexpr int kBalBlocks = 256;
-// Batches of at most this many logits take one workgroup, which finishes too:
-// at T = 512, Ne = 64 it takes 10 us where 16 workgroups and their sum take 4
-// + 3 and the gap between two launches, and the host saves a launch (3.3 us).
-constexpr int64_t kOneBlock = 32768;
-// Backward workgroups at most: four per CU (11.6 us at T = 65536; two 11.8,
-// eight 13.6).
+// Up to this many tokens for each of its teams a batch takes one workgroup,
+// which finishes too: at T = 512, Ne = 64 a call of 9.2 us, where several
+// workgroups and their sum take 13.1 since the host launches twice (captured:
+// 7.6 against 6.7); with twice the tokens 11.8 against 12.9 (11.1 and 7.0).
+constexpr int kOneBlockSteps = 8;
+// Backward workgroups at most: four per CU (10.1 us at T = 65536; two 10.2,
+// eight 12.2).
 constexpr unsigned kBackBlocks = 1024;
 
 }  // namespace
 
 static int balance_blocks(int T, int Ne) {
-    if (static_cast<int64_t>(T) * Ne <= kOneBlock) return 1;
+    const int team = Ne <= 64 ? 16 : Ne <= 128 ? 32 : 64;  // as in by_experts
+    if (T <= kOneBlockSteps * (kBalThreads / team)) return 1;
     return static_cast<int>(std::min(ceil_div(T, 64), static_cast<unsigned>(kBalBlocks)));
 }
 
@@ -352,8 +401,8 @@ hipError_t launch_balance(const float *logits, const int32_t *ids, const uint8_t
     const int Ne = tab.Ne;
     const unsigned per = ceil_div(T, balance_blocks(T, Ne)), grid = ceil_div(T, per);
     const BalanceOut o{cb, cg, cz, counts, probs, loss};
-    by_experts(Ne, [&](auto L, auto NI) {
-        k_balance<decltype(L)::value, decltype(NI)::value>
+    by_experts(Ne, vector_aligned(logits), [&](auto L, auto NI, auto VEC) {
+        k_balance<decltype(L)::value, decltype(NI)::value, decltype(VEC)::value>
             <<<grid, kBalThreads, 0, s>>>(logits, ids, valid, T, Ne, k, per, part, tab, o);
     });
     if (grid > 1)
@@ -366,11 +415,12 @@ hipError_t launch_balance_back(const float *logits, const uint8_t *valid, const 
                                float dloss, const float *dlogits_in, float *dlogits,
                                hipStream_t s) {
     const int Ne = tab.Ne;
-    by_experts(Ne, [&](auto L, auto NI) {
+    by_experts(Ne, vector_aligned(logits, dlogits_in, dlogits), [&](auto L, auto NI, auto VEC) {
         constexpr int kTeams = kBackThreads / decltype(L)::value;
         const unsigned grid = std::min(ceil_div(T, kTeams), kBackBlocks);
-        k_balance_back<decltype(L)::value, decltype(NI)::value><<<grid, kBackThreads, 0, s>>>(
-            logits, valid, counts, tab, T, Ne, k, cb, cg, cz, dloss, dlogits_in, dlogits);
+        k_balance_back<decltype(L)::value, decltype(NI)::value, decltype(VEC)::value>
+            <<<grid, kBackThreads, 0, s>>>(logits, valid, counts, tab, T, Ne, k, cb, cg, cz, dloss,
+                                           dlogits_in, dlogits);
     });
     return hipGetLastError();
 }

@@ -103,14 +103,20 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 
 // Reduction over aligned groups of L lanes (2, 4, ..., 64) by an associative
-// and commutative f; every lane of a group gets its result.
+// and commutative f; every lane of a group gets its result.  Every lane of a
+// row has a partner, so that a step can be one instruction (no value to keep).
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
-template <int L, typename F>
-__device__ __forceinline__ float group_reduce(float v, F f) {
-    if constexpr (L >= 2) v = f(v, dpp_f<kDppXor1, 0xf>(v, v));
-    if constexpr (L >= 4) v = f(v, dpp_f<kDppXor2, 0xf>(v, v));
-    if constexpr (L >= 8) v = f(v, dpp_f<kDppHalfMirror, 0xf>(v, v));
-    if constexpr (L >= 16) v = f(v, dpp_f<kDppMirror, 0xf>(v, v));
+template <int CTRL, typename V>
+__device__ __forceinline__ V dpp_partner(V v) {
+    return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf,
+                                                             0xf, true));
+}
+template <int L, typename V, typename F>
+__device__ __forceinline__ V group_reduce(V v, F f) {
+    if constexpr (L >= 2) v = f(v, dpp_partner<kDppXor1>(v));
+    if constexpr (L >= 4) v = f(v, dpp_partner<kDppXor2>(v));
+    if constexpr (L >= 8) v = f(v, dpp_partner<kDppHalfMirror>(v));
+    if constexpr (L >= 16) v = f(v, dpp_partner<kDppMirror>(v));
     if constexpr (L >= 32) v = f(v, __shfl_xor(v, 16));
     if constexpr (L >= 64) v = f(v, __shfl_xor(v, 32));
     return v;
@@ -119,9 +125,14 @@ template <int L>
 __device__ __forceinline__ float group_sum(float v) {
     return group_reduce<L>(v, [](float a, float b) { return a + b; });
 }
+// As integers in the order of the floats (fmaxf first makes its operands
+// canonical, an instruction more a step); of a NaN either the NaN or the
+// largest other value.
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
-    return group_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+    const auto key = [](int b) { return b ^ ((b >> 31) & 0x7fffffff); };
+    return __int_as_float(key(group_reduce<L>(key(__float_as_int(v)),
+                                              [](int a, int b) { return max(a, b); })));
 }
 
 // Wave-wide arg-max of (value, index): larger value wins, ties to the lower

@@ -337,6 +337,21 @@ def test_balance_ignores_ids_out_of_range_and_counts_repeats():
     assert int(got[0][:Ne].sum()) == T * k - 3
 
 
+@pytest.mark.parametrize("T,Ne", [(513, 64), (700, 100), (300, 252), (9, 36)])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_balance_with_and_without_whole_vectors(offset, T, Ne):
+    """Every fourth expert count with logits and dlogits on and off a vector's border."""
+    logits, ids, valid, place, group = balance_inputs(T, Ne, 4, 1, "some", seed=Ne)
+    into, out = (torch.empty(T * Ne + offset, device="cuda")[offset:].view(T, Ne) for _ in range(2))
+    into.copy_(randn(gen(2), T, Ne))
+    own = torch.empty(T * Ne + offset, device="cuda")[offset:].view(T, Ne).copy_(logits)
+    got = run_balance(T, Ne, 4, 1, own, ids, valid, place, into)
+    check_balance(logits, ids, valid, group, 4, into, got)
+    desc, opt = layer(T, Ne=Ne, k=4), occ.BalanceDesc(balance=COEF[0], group=COEF[1], z=COEF[2])
+    occ.occ_balance_backward(desc, opt, own, valid, place, got[0], 0.5, into, out)
+    check_balance(logits, ids, valid, group, 4, into, (*got[:3], out))
+
+
 def test_balance_in_place_uint8_mask_and_no_placement():
     T, Ne, k = 300, 60, 4
     logits, ids, valid, place, group = balance_inputs(T, Ne, k, 1, "some", seed=6)
