@@ -632,15 +632,19 @@ __global__ __launch_bounds__(kBfThreads) void k_gate_bwd(const float *__restrict
         gate_dx<(MB + 1) / 2, DX == kRegsVec>(block, dl, T, d, Ne, dx);
 }
 
-// fp32: a wave makes 64 experts x 64 columns of dW_r from a quarter of the
-// workgroup's tokens, 16 per step.  Expert 4 i + m is row i of block m and
-// column 4 i + q column i of block q, so that a lane's operands of 16 MFMAs
-// are one 16-byte piece of a token's dlogits and one of its x.  What lies
-// behind a token's last expert is read with it (its sums are not stored),
-// except near the end of the array.
-typedef f32x4 DwSums[kWaves / 2][16][kWave];
+// fp32: a wave makes 16 MB experts x 64 columns of dW_r from a quarter of the
+// workgroup's tokens, 16 per step.  Expert MB i + m is row i of block m and
+// column 4 i + q column i of block q, so that a lane's operands of 4 MB MFMAs
+// are one piece of a token's dlogits and one of its x, of 16 bytes (MB = 4).
+// Fewer experts take fewer blocks (8 experts, d = 2048: T = 256 6.9 us a call
+// against 11.4 with four, T = 32768 163 against 181).
+// What lies behind a token's last expert is read with it (its sums are not
+// stored), except near the end of the array.
+template <int MB>
+using DwSums = f32x4[kWaves / 2][4 * MB][kWave];
+template <int MB>
 __device__ __forceinline__ void gate_dw_f32(unsigned block, const float *__restrict__ dl, unsigned T,
-                                            int d, int Ne, const DwArgs &A, DwSums &s_acc) {
+                                            int d, int Ne, const DwArgs &A, DwSums<MB> &s_acc) {
     const auto *__restrict__ x = static_cast<const float *>(A.x);
     float *__restrict__ part = A.out;
     const int col_groups = A.col_groups;
@@ -651,43 +655,46 @@ __device__ __forceinline__ void gate_dw_f32(unsigned block, const float *__restr
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int c0 = group % col_groups * kDwColsF, e0 = group / col_groups * kDwExperts;
     const unsigned t0 = share * A.per_share, t1 = min(T, t0 + A.per_share);
-    const int col = min(c0 + 4 * i16, d - 4), exp = min(e0 + 4 * i16, Ne - 1);
-    f32x4 acc[4][4];  // [m][q]
+    const int col = min(c0 + 4 * i16, d - 4), exp = min(e0 + MB * i16, Ne - 1);
+    typedef float Experts __attribute__((ext_vector_type(MB), aligned(4)));
+    f32x4 acc[MB][4];  // [m][q]
 #pragma unroll
-    for (int m = 0; m < 4; m++)
+    for (int m = 0; m < MB; m++)
 #pragma unroll
         for (int q = 0; q < 4; q++) acc[m][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-    f32x4 an[4], bn[4];  // the next step's tokens t + 4 u + G
+    Experts an[4];
+    f32x4 bn[4];  // the next step's tokens t + 4 u + G
     auto load = [&](unsigned t) {
-        // 3 values behind a row lie in the next three at most
-        const bool inside = t + 16 + 3 <= T;
+        // MB - 1 values behind a row lie in the next rows, as many at most
+        const bool inside = t + 16 + MB - 1 <= T;
 #pragma unroll
         for (int u = 0; u < 4; u++) {
             const size_t tu = min(t + 4 * u + G, T - 1);
             const float *row = dl + tu * Ne;
             if (inside) {
-                an[u] = *reinterpret_cast<const f32x4_unaligned *>(row + exp);
+                an[u] = *reinterpret_cast<const Experts *>(row + exp);
             } else {
 #pragma unroll
-                for (int m = 0; m < 4; m++) an[u][m] = row[min(exp + m, Ne - 1)];
+                for (int m = 0; m < MB; m++) an[u][m] = row[min(exp + m, Ne - 1)];
             }
             bn[u] = *reinterpret_cast<const f32x4 *>(x + tu * d + col);
         }
     };
     load(t0 + 16 * wv);
     for (unsigned t = t0 + 16 * wv; t < t1; t += 16 * kWaves) {
-        f32x4 a[4], b[4];
+        Experts a[4];
+        f32x4 b[4];
 #pragma unroll
         for (int u = 0; u < 4; u++) {
             // tokens behind the share count nothing
-            a[u] = t + 4 * u + G < t1 ? an[u] : f32x4{0.f, 0.f, 0.f, 0.f};
+            a[u] = t + 4 * u + G < t1 ? an[u] : Experts{};
             b[u] = bn[u];
         }
         load(t + 16 * kWaves);
 #pragma unroll
         for (int u = 0; u < 4; u++)
 #pragma unroll
-            for (int m = 0; m < 4; m++)
+            for (int m = 0; m < MB; m++)
 #pragma unroll
                 for (int q = 0; q < 4; q++)
                     acc[m][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[u][m], b[u][q], acc[m][q], 0, 0, 0);
@@ -696,41 +703,41 @@ __device__ __forceinline__ void gate_dw_f32(unsigned block, const float *__restr
     for (int half = kWaves / 2; half > 0; half >>= 1) {
         if (wv >= half && wv < 2 * half)
 #pragma unroll
-            for (int m = 0; m < 4; m++)
+            for (int m = 0; m < MB; m++)
 #pragma unroll
                 for (int q = 0; q < 4; q++) s_acc[wv - half][m * 4 + q][l] = acc[m][q];
         __syncthreads();
         if (wv < half)
 #pragma unroll
-            for (int m = 0; m < 4; m++)
+            for (int m = 0; m < MB; m++)
 #pragma unroll
                 for (int q = 0; q < 4; q++) acc[m][q] += s_acc[wv][m * 4 + q][l];
         __syncthreads();
     }
     if (wv || c0 + 4 * i16 >= d) return;
-    // lane: experts e0 + 4 (4 G + v) + m, columns c0 + 4 i16 + q
+    // lane: experts e0 + MB (4 G + v) + m, columns c0 + 4 i16 + q
     float *out = part + static_cast<size_t>(share) * Ne * d;
 #pragma unroll
-    for (int m = 0; m < 4; m++)
+    for (int m = 0; m < MB; m++)
 #pragma unroll
         for (int v = 0; v < 4; v++) {
-            const int e = e0 + 16 * G + 4 * v + m;
+            const int e = e0 + MB * (4 * G + v) + m;
             if (e < Ne)
                 *reinterpret_cast<f32x4 *>(out + static_cast<size_t>(e) * d + col) =
                     f32x4{acc[m][0][v], acc[m][1][v], acc[m][2][v], acc[m][3][v]};
         }
 }
 
-template <bool SMALL>
+template <int MB, bool SMALL>
 __global__ __launch_bounds__(kThreads) void k_gate_bwd_f32(const float *__restrict__ dl, unsigned T,
                                                            int d, int Ne, const DwArgs dw,
                                                            const DxArgs dx) {
     typedef DxTile<float, 2, 2> Tile;
-    __shared__ __attribute__((aligned(16))) char lds[std::max(sizeof(DwSums), 2 * sizeof(Tile))];
+    __shared__ __attribute__((aligned(16))) char lds[std::max(sizeof(DwSums<MB>), 2 * sizeof(Tile))];
     bool is_dw;
     const unsigned block = own_block(dw, dx, false, is_dw);
     if (is_dw)
-        gate_dw_f32(block, dl, T, d, Ne, dw, *reinterpret_cast<DwSums *>(lds));
+        gate_dw_f32<MB>(block, dl, T, d, Ne, dw, *reinterpret_cast<DwSums<MB> *>(lds));
     else
         gate_dx_tile<float, 2, 2, SMALL>(block, dl, T, d, Ne, dx, *reinterpret_cast<Tile(*)[2]>(lds));
 }
@@ -807,6 +814,7 @@ hipError_t launch_gate_bwd(const float *dl, const void *x, const void *w_router,
     }
     DxArgs X = {w_router, dx_in, dx, 0, 0, 0};
     using std::integral_constant;
+    typedef integral_constant<int, 1> I1;
     typedef integral_constant<int, 2> I2;
     typedef integral_constant<int, 4> I4;
     // dx in tiles of 32 MB x 64 WN; true: smaller than a tile
@@ -836,12 +844,21 @@ hipError_t launch_gate_bwd(const float *dl, const void *x, const void *w_router,
     if (!bf16) {
         // dx alone has more waves on a CU in its own kernel (T = 4096, d = 2048:
         // 8 experts 16 us against 21, 250 47 against 49)
+        const auto run = [&](auto mb) {
+            constexpr int MB = decltype(mb)::value;
+            if (dx && tiles_of(float{}, I2{}, I2{}))
+                k_gate_bwd_f32<MB, true><<<W.blocks + X.blocks, kThreads, 0, s>>>(dl, T, d, Ne, W, X);
+            else
+                k_gate_bwd_f32<MB, false><<<W.blocks + X.blocks, kThreads, 0, s>>>(dl, T, d, Ne, W, X);
+        };
         if (!dw)
             tiles_alone(float{}, I2{}, I2{});
-        else if (dx && tiles_of(float{}, I2{}, I2{}))
-            k_gate_bwd_f32<true><<<W.blocks + X.blocks, kThreads, 0, s>>>(dl, T, d, Ne, W, X);
+        else if (Ne <= 16)
+            run(I1{});
+        else if (Ne <= 32)
+            run(I2{});
         else
-            k_gate_bwd_f32<false><<<W.blocks + X.blocks, kThreads, 0, s>>>(dl, T, d, Ne, W, X);
+            run(I4{});
     } else if (dx && Ne > 64) {
         // W_r no longer fits a wave's registers.  dx alone: large tiles where
         // there is one for every CU (130 experts, d = 2048: T = 4096 15.8 us
@@ -875,7 +892,7 @@ hipError_t launch_gate_bwd(const float *dl, const void *x, const void *w_router,
                 both(mb, integral_constant<int, kRegs>{}, threads);
         };
         if (Ne <= 16)
-            run(integral_constant<int, 1>{});
+            run(I1{});
         else if (Ne <= 32)
             run(I2{});
         else
