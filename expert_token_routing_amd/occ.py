@@ -500,11 +500,11 @@ def _mask(valid, T: int, index: int):
 
 
 def _place(desc: LayerDesc, placement):
-    """The placement as host int32 and its address, or Nones."""
+    """The placement as host int32 in bytes (the library reads it within the call; an array's
+    address costs 1 us more), or None."""
     if placement is None:
-        return None, None
-    L = _host_i32(placement, "placement", (desc.Nd, desc.Ne // max(desc.Nd, 1)))
-    return L, L.ctypes.data
+        return None
+    return _host_i32(placement, "placement", (desc.Nd, desc.Ne // max(desc.Nd, 1))).tobytes()
 
 
 def occ_balance_loss(desc: LayerDesc, opt: BalanceDesc, logits, ids, valid, placement, counts,
@@ -512,7 +512,7 @@ def occ_balance_loss(desc: LayerDesc, opt: BalanceDesc, logits, ids, valid, plac
     """Router losses [sum, balance, group, z], mean probabilities, and the counts (Ne, then the
     valid tokens)."""
     T, Ne, f32, i32, i = desc.T, desc.Ne, torch.float32, torch.int32, _device(logits)
-    L, place = _place(desc, placement)
+    place = _place(desc, placement)
     _queue("occ_balance_loss", lib().occ_balance_loss, i, stream, desc, opt,
            _addr(logits, "logits", f32, (T, Ne), i), _addr(ids, "ids", i32, (T, desc.k), i),
            _mask(valid, T, i), place, _addr(counts, "counts", i32, (Ne + 1,), i),
@@ -524,7 +524,7 @@ def occ_balance_backward(desc: LayerDesc, opt: BalanceDesc, logits, valid, place
                          dloss: float, dlogits_in, dlogits, stream=None):
     """dlogits = dlogits_in + dloss times the losses' gradient in the logits."""
     T, Ne, f32, i = desc.T, desc.Ne, torch.float32, _device(logits)
-    L, place = _place(desc, placement)
+    place = _place(desc, placement)
     _queue("occ_balance_backward", lib().occ_balance_backward, i, stream, desc, opt,
            _addr(logits, "logits", f32, (T, Ne), i), _mask(valid, T, i), place,
            _addr(counts, "counts", torch.int32, (Ne + 1,), i), dloss,
