@@ -342,7 +342,7 @@ size_t block_ws_bytes(const occ_layer_desc &D) {
 
 occ_status check_norm(const occ_layer_desc *desc, const occ_norm_desc *opt) {
     OCC_TRY(check_desc(desc));
-    if (!opt || !std::isfinite(opt->eps) || opt->eps <= 0.f || !std::isfinite(opt->scale) ||
+    if (!opt || !std::isfinite(opt->eps) || opt->eps < FLT_MIN || !std::isfinite(opt->scale) ||
         opt->gate < OCC_GATE_NONE || opt->gate > OCC_GATE_TOKEN)
         return OCC_ERR_INVALID_ARG;
     return OCC_OK;

@@ -441,7 +441,7 @@ typedef enum occ_block_gate {
 } occ_block_gate;
 
 typedef struct occ_norm_desc {
-    float eps;    /* > 0, added to the mean square */
+    float eps;    /* >= FLT_MIN, added to the mean square */
     float scale;  /* residual scale of the block's output */
     int32_t gate; /* occ_block_gate */
 } occ_norm_desc;
@@ -463,8 +463,8 @@ typedef struct occ_norm_desc {
  *   w_pre      d (dtype), or NULL together with h (behind the last block).
  *   r (out)    T x d (dtype), needed with y.
  *   h (out)    T x d (dtype).
- * Errors: INVALID_ARG for a missing or superfluous pointer, eps <= 0, a scale
- * or eps that is not finite. */
+ * Errors: INVALID_ARG for a missing or superfluous pointer, eps < FLT_MIN, a
+ * scale or eps that is not finite. */
 occ_status occ_block_norm(const occ_layer_desc *desc, const occ_norm_desc *opt, const void *x,
                           const void *y, const void *w_post, const void *gate, const void *w_pre,
                           void *r, void *h, void *stream);

@@ -186,6 +186,12 @@ def test_norm_refuses_options(L, bad):
     assert norm_back_status(L, opt=opt) == INV
 
 
+@pytest.mark.parametrize("eps", [1e-45, 1.1e-38])
+def test_norm_refuses_an_eps_below_the_normal_numbers(L, eps):
+    opt = occ.NormDesc(eps=eps, scale=1.0, gate=0)
+    assert norm_status(L, opt=opt) == INV and norm_back_status(L, opt=opt) == INV
+
+
 def test_norm_refuses_shapes(L):
     assert norm_status(L, desc=occ.desc_of(W.OLMOE, T=0)) == INV
     assert norm_status(L, desc=occ.desc_of(W.OLMOE, d=2000)) == UNS

@@ -176,6 +176,31 @@ def test_norm_rows_of_zeros_and_of_extreme_size():
     check_norm_back(t, grads, r, opt, out)
 
 
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (BF16, 256), (BF16, 2048), (BF16, 8192), (F32, 48),
+                                     (F32, 4096)])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_norm_backward_of_few_rows(form, dtype, d):
+    """From one row to more than a single workgroup takes: 1, 2, 4, 8, ... rows and one more."""
+    for T in (1, 2, 4, 5, 8, 9, 16, 17, 32, 33, 64, 65, 128, 129, 256, 257):
+        t, grads, opt = norm_inputs(dtype, T, d, form, seed=T)
+        r, h = run_norm(t, opt, dtype)
+        check_norm(t, opt, r, h)
+        kept = r if r is not None else t["x"]
+        check_norm_back(t, grads, kept, opt, run_norm_back(t, grads, kept, opt, dtype))
+
+
+def test_norm_with_the_smallest_eps():
+    t, _, _ = norm_inputs(F32, 5, 1040, "channel", seed=2)
+    t["x"][1:3] = 0
+    t["y"][2:4] = 0
+    t["x"][4] *= 1e-18
+    opt = occ.NormDesc(eps=2.0 ** -126, scale=SCALE, gate=1)
+    r, h = run_norm(t, opt, F32)
+    want_r, want_h, mag = ref.block_norm(**t, kind=1, eps=opt.eps, scale=SCALE)
+    check(r, want_r, mag, 64, "r")
+    assert (h[2] == 0).all() and h.isfinite().all()
+
+
 def test_norm_keeps_what_is_not_finite_in_its_row():
     t, grads, opt = norm_inputs(BF16, 40, 2048, "token", seed=2)
     clean_r, clean_h = run_norm(t, opt, BF16)
