@@ -15,12 +15,14 @@
 // keep), and cuts them into pieces of kPiece elements; a workgroup finds its
 // tensor from its number and moves one piece with 16-byte accesses, four
 // elements per lane.  A wave's 64 lanes then hold the 256 elements of one
-// 8-bit block, whose largest magnitude is a wave maximum.  Every lane has all
-// its loads in flight at once and the workgroups cross the tensors in order:
-// pieces of 4 elements per lane measure 2105 us for 403 M elements in fp32
-// (5.7 TB/s), of 8 2297, of 16 2250, of 32 2319.  8 bits, 35 M elements:
-// 128 us (4.9 TB/s; with IEEE square roots and divisions 140); six small
-// tensors 4.4 us.
+// 8-bit block, whose largest magnitude is a wave maximum.  The workgroups cross
+// the tensors in order: pieces of 4 elements per lane measure 2110 us for 403 M
+// elements in fp32 (5.7 TB/s; 2050 to 2190 with the addresses), of 8 2297, of 16
+// 2250, of 32 2319.  All of a lane's loads are in flight at once (one behind
+// the other, 8 bits 127 us for 35 M elements against 114, 5.5 TB/s, six small
+// tensors 4.3 us against 3.4; 403 M in fp32 2 to 3% faster).  Workgroups of
+// 1024 threads: small tensors 40% slower, the largest 3% either way.  IEEE
+// square roots and divisions cost 8 bits 10%.
 #include "launch.h"
 
 namespace occ {
@@ -42,24 +44,27 @@ struct Table {
 };
 static_assert(sizeof(Table) + sizeof(AdamwStep) <= 4096, "kernel arguments");
 
-// Four consecutive values from element i of n; whole when they may be moved
-// as one vector.
-template <typename V, typename E>
-__device__ __forceinline__ void load4(const void *p, int64_t i, int64_t n, bool whole, E (&v)[4]) {
-    const E *q = static_cast<const E *>(p) + i;
-    if (whole) {
-        const V x = *reinterpret_cast<const V *>(q);
+// Four consecutive values from element i of n, as one vector (WHOLE) or each by
+// itself, zero behind the end.  No load is under a condition, so that all of a
+// lane's are in flight at once.
+template <bool WHOLE, typename V, typename E>
+__device__ __forceinline__ void load4(const void *p, int64_t i, int64_t n, E (&v)[4]) {
+    const E *q = static_cast<const E *>(p);
+    if constexpr (WHOLE) {
+        const V x = *reinterpret_cast<const V *>(q + i);
 #pragma unroll
         for (int j = 0; j < 4; j++) v[j] = reinterpret_cast<const E *>(&x)[j];
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; j++) v[j] = i + j < n ? q[j] : static_cast<E>(0);
+        for (int j = 0; j < 4; j++) v[j] = q[min(i + j, n - 1)];
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = i + j < n ? v[j] : static_cast<E>(0);
     }
 }
-template <typename V, typename E>
-__device__ __forceinline__ void store4(void *p, int64_t i, int64_t n, bool whole, const E (&v)[4]) {
+template <bool WHOLE, typename V, typename E>
+__device__ __forceinline__ void store4(void *p, int64_t i, int64_t n, const E (&v)[4]) {
     E *q = static_cast<E *>(p) + i;
-    if (whole) {
+    if constexpr (WHOLE) {
         V x;
 #pragma unroll
         for (int j = 0; j < 4; j++) reinterpret_cast<E *>(&x)[j] = v[j];
@@ -107,19 +112,37 @@ __device__ __forceinline__ uint32_t quantise(const float (&v)[4], const float (&
     return to_e4m3(c);
 }
 
-template <bool Q8, bool GBF16>
-__global__ __launch_bounds__(kThreads) void k_adamw(Table tab, AdamwStep st) {
-    int a = 0;
-    for (int hi = tab.count; hi - a > 1;) {  // the last tensor with first <= blockIdx.x
-        const int mid = (a + hi) >> 1;
-        if (tab.first[mid] <= blockIdx.x)
-            a = mid;
-        else
-            hi = mid;
-    }
-    const AdamwTensor &T = tab.t[a];
+template <bool Q8, bool GBF16, bool WHOLE>
+__device__ __forceinline__ void update(const AdamwTensor &T, int64_t i, const AdamwStep &st) {
     const int64_t n = T.n;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x - tab.first[a]) * kPiece;
+    float p[4], g[4], m[4], v[4];
+    load4<WHOLE, f32x4, float>(T.p, i, n, p);
+    if constexpr (GBF16) {
+        typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+        uint16_t gb[4];
+        load4<WHOLE, u16x4, uint16_t>(T.g, i, n, gb);
+#pragma unroll
+        for (int j = 0; j < 4; j++) g[j] = bf16_bits_to_f32(gb[j]);
+    } else {
+        load4<WHOLE, f32x4, float>(T.g, i, n, g);
+    }
+    const int64_t qb = i / kQBlock;
+    if constexpr (Q8) {
+        typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
+        uint8_t mc[4], vc[4];
+        load4<WHOLE, u8x4, uint8_t>(T.m, i, n, mc);
+        load4<WHOLE, u8x4, uint8_t>(T.v, i, n, vc);
+        // a lane behind the end holds zeros; its block exists (the wave's first lane's does)
+        from_e4m3(mc[0] | mc[1] << 8 | mc[2] << 16 | static_cast<uint32_t>(mc[3]) << 24,
+                  T.m_scale[qb], m);
+        from_e4m3(vc[0] | vc[1] << 8 | vc[2] << 16 | static_cast<uint32_t>(vc[3]) << 24,
+                  T.v_scale[qb], v);
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] *= v[j];
+    } else {
+        load4<WHOLE, f32x4, float>(T.m, i, n, m);
+        load4<WHOLE, f32x4, float>(T.v, i, n, v);
+    }
     float lr = st.lr, c1 = st.c1, c2_rsqrt = st.c2_rsqrt, gs = st.grad_scale;
     if (st.dynamic) {
         lr = st.dynamic[0];
@@ -129,38 +152,6 @@ __global__ __launch_bounds__(kThreads) void k_adamw(Table tab, AdamwStep st) {
         c2_rsqrt = 1.f / sqrtf(-expm1f(step * st.log_b2));
     }
     const float decay = fmaf(-lr, st.weight_decay, 1.f), rate = lr / c1;
-    const int64_t i = i0 + threadIdx.x * 4;
-    // a wave whose elements all lie behind the tensor's end has nothing to do
-    if (i0 + (threadIdx.x & ~(kWave - 1)) * 4 >= n) return;
-    const bool whole = T.aligned && i + 4 <= n;
-    float p[4], g[4], m[4], v[4];
-    load4<f32x4, float>(T.p, i, n, whole, p);
-    if constexpr (GBF16) {
-        typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
-        uint16_t gb[4];
-        load4<u16x4, uint16_t>(T.g, i, n, whole, gb);
-#pragma unroll
-        for (int j = 0; j < 4; j++) g[j] = bf16_bits_to_f32(gb[j]);
-    } else {
-        load4<f32x4, float>(T.g, i, n, whole, g);
-    }
-    const int64_t qb = i / kQBlock;
-    if constexpr (Q8) {
-        typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
-        uint8_t mc[4], vc[4];
-        load4<u8x4, uint8_t>(T.m, i, n, whole, mc);
-        load4<u8x4, uint8_t>(T.v, i, n, whole, vc);
-        // a lane behind the end holds zeros; its block exists (the wave's first lane's does)
-        from_e4m3(mc[0] | mc[1] << 8 | mc[2] << 16 | static_cast<uint32_t>(mc[3]) << 24,
-                  T.m_scale[qb], m);
-        from_e4m3(vc[0] | vc[1] << 8 | vc[2] << 16 | static_cast<uint32_t>(vc[3]) << 24,
-                  T.v_scale[qb], v);
-#pragma unroll
-        for (int j = 0; j < 4; j++) v[j] *= v[j];
-    } else {
-        load4<f32x4, float>(T.m, i, n, whole, m);
-        load4<f32x4, float>(T.v, i, n, whole, v);
-    }
     float root[4];
     uint16_t copy[4];
 #pragma unroll
@@ -175,10 +166,10 @@ __global__ __launch_bounds__(kThreads) void k_adamw(Table tab, AdamwStep st) {
         p[j] = fmaf(decay, p[j], -rate * (m[j] * __builtin_amdgcn_rcpf(fmaf(root[j], c2_rsqrt, st.eps))));
         copy[j] = f32_to_bf16_bits(p[j]);
     }
-    store4<f32x4, float>(T.p_out, i, n, whole, p);
+    store4<WHOLE, f32x4, float>(T.p_out, i, n, p);
     if (T.p_bf16) {
         typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
-        store4<u16x4, uint16_t>(T.p_bf16, i, n, whole, copy);
+        store4<WHOLE, u16x4, uint16_t>(T.p_bf16, i, n, copy);
     }
     if constexpr (Q8) {
         typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
@@ -188,16 +179,38 @@ __global__ __launch_bounds__(kThreads) void k_adamw(Table tab, AdamwStep st) {
                                static_cast<uint8_t>(qm >> 16), static_cast<uint8_t>(qm >> 24)};
         const uint8_t vc[4] = {static_cast<uint8_t>(qv), static_cast<uint8_t>(qv >> 8),
                                static_cast<uint8_t>(qv >> 16), static_cast<uint8_t>(qv >> 24)};
-        store4<u8x4, uint8_t>(T.m_out, i, n, whole, mc);
-        store4<u8x4, uint8_t>(T.v_out, i, n, whole, vc);
+        store4<WHOLE, u8x4, uint8_t>(T.m_out, i, n, mc);
+        store4<WHOLE, u8x4, uint8_t>(T.v_out, i, n, vc);
         if (lane_id() == 0) {
             T.m_scale_out[qb] = um;
             T.v_scale_out[qb] = uv;
         }
     } else {
-        store4<f32x4, float>(T.m_out, i, n, whole, m);
-        store4<f32x4, float>(T.v_out, i, n, whole, v);
+        store4<WHOLE, f32x4, float>(T.m_out, i, n, m);
+        store4<WHOLE, f32x4, float>(T.v_out, i, n, v);
     }
+}
+
+// A whole piece of a tensor moves in vectors, a tensor's last one and pieces of
+// arrays off the vectors' borders value by value.
+template <bool Q8, bool GBF16>
+__global__ __launch_bounds__(kThreads) void k_adamw(Table tab, AdamwStep st) {
+    int a = 0;
+    for (int hi = tab.count; hi - a > 1;) {  // the last tensor with first <= blockIdx.x
+        const int mid = (a + hi) >> 1;
+        if (tab.first[mid] <= blockIdx.x)
+            a = mid;
+        else
+            hi = mid;
+    }
+    const AdamwTensor &T = tab.t[a];
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x - tab.first[a]) * kPiece;
+    // a wave whose elements all lie behind the tensor's end has nothing to do
+    if (i0 + (threadIdx.x & ~(kWave - 1)) * 4 >= T.n) return;
+    if (T.aligned && i0 + kPiece <= T.n)
+        update<Q8, GBF16, true>(T, i0 + threadIdx.x * 4, st);
+    else
+        update<Q8, GBF16, false>(T, i0 + threadIdx.x * 4, st);
 }
 
 }  // namespace
