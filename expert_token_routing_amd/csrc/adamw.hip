@@ -19,10 +19,12 @@
 // the tensors in order: pieces of 4 elements per lane measure 2110 us for 403 M
 // elements in fp32 (5.7 TB/s; 2050 to 2190 with the addresses), of 8 2297, of 16
 // 2250, of 32 2319.  All of a lane's loads are in flight at once (one behind
-// the other, 8 bits 127 us for 35 M elements against 114, 5.5 TB/s, six small
-// tensors 4.3 us against 3.4; 403 M in fp32 2 to 3% faster).  Workgroups of
-// 1024 threads: small tensors 40% slower, the largest 3% either way.  IEEE
-// square roots and divisions cost 8 bits 10%.
+// the other, 8 bits 127 us for 35 M elements against 112, 5.6 TB/s), but for
+// the largest fp32 states.  Workgroups of 1024 threads: small tensors 40%
+// slower, the largest 3% either way.  IEEE square roots and divisions cost 8
+// bits 10%.
+#include <type_traits>
+
 #include "launch.h"
 
 namespace occ {
@@ -112,11 +114,25 @@ __device__ __forceinline__ uint32_t quantise(const float (&v)[4], const float (&
     return to_e4m3(c);
 }
 
-template <bool Q8, bool GBF16, bool WHOLE>
+// STAGED: one load of a lane behind the other.  Waves fill the memory's queues
+// either way; above kStagedElements the four streams disturb each other less
+// (fp32, 403 M elements 2125 us against 2215, 268 M 1414 against 1476; 134 M 700
+// and 699, 34 M 194 against 190, six small tensors 4.3 against 3.6).
+constexpr uint64_t kStagedElements = 1ull << 27;
+template <bool STAGED>
+__device__ __forceinline__ void stage_end() {
+    if constexpr (STAGED) {
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+template <bool Q8, bool GBF16, bool STAGED, bool WHOLE>
 __device__ __forceinline__ void update(const AdamwTensor &T, int64_t i, const AdamwStep &st) {
     const int64_t n = T.n;
     float p[4], g[4], m[4], v[4];
     load4<WHOLE, f32x4, float>(T.p, i, n, p);
+    stage_end<STAGED>();
     if constexpr (GBF16) {
         typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
         uint16_t gb[4];
@@ -126,6 +142,7 @@ __device__ __forceinline__ void update(const AdamwTensor &T, int64_t i, const Ad
     } else {
         load4<WHOLE, f32x4, float>(T.g, i, n, g);
     }
+    stage_end<STAGED>();
     const int64_t qb = i / kQBlock;
     if constexpr (Q8) {
         typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
@@ -141,6 +158,7 @@ __device__ __forceinline__ void update(const AdamwTensor &T, int64_t i, const Ad
         for (int j = 0; j < 4; j++) v[j] *= v[j];
     } else {
         load4<WHOLE, f32x4, float>(T.m, i, n, m);
+        stage_end<STAGED>();
         load4<WHOLE, f32x4, float>(T.v, i, n, v);
     }
     float lr = st.lr, c1 = st.c1, c2_rsqrt = st.c2_rsqrt, gs = st.grad_scale;
@@ -193,7 +211,7 @@ __device__ __forceinline__ void update(const AdamwTensor &T, int64_t i, const Ad
 
 // A whole piece of a tensor moves in vectors, a tensor's last one and pieces of
 // arrays off the vectors' borders value by value.
-template <bool Q8, bool GBF16>
+template <bool Q8, bool GBF16, bool STAGED>
 __global__ __launch_bounds__(kThreads) void k_adamw(Table tab, AdamwStep st) {
     int a = 0;
     for (int hi = tab.count; hi - a > 1;) {  // the last tensor with first <= blockIdx.x
@@ -208,9 +226,9 @@ __global__ __launch_bounds__(kThreads) void k_adamw(Table tab, AdamwStep st) {
     // a wave whose elements all lie behind the tensor's end has nothing to do
     if (i0 + (threadIdx.x & ~(kWave - 1)) * 4 >= T.n) return;
     if (T.aligned && i0 + kPiece <= T.n)
-        update<Q8, GBF16, true>(T, i0 + threadIdx.x * 4, st);
+        update<Q8, GBF16, STAGED, true>(T, i0 + threadIdx.x * 4, st);
     else
-        update<Q8, GBF16, false>(T, i0 + threadIdx.x * 4, st);
+        update<Q8, GBF16, STAGED, false>(T, i0 + threadIdx.x * 4, st);
 }
 
 }  // namespace
@@ -233,14 +251,23 @@ hipError_t launch_adamw(const AdamwTensor *tensors, int count, const AdamwStep &
         }
         if (tab.count == 0) continue;
         const unsigned grid = static_cast<unsigned>(blocks);
-        if (q8 && grad_bf16)
-            k_adamw<true, true><<<grid, kThreads, 0, s>>>(tab, st);
-        else if (q8)
-            k_adamw<true, false><<<grid, kThreads, 0, s>>>(tab, st);
-        else if (grad_bf16)
-            k_adamw<false, true><<<grid, kThreads, 0, s>>>(tab, st);
+        const bool staged = blocks * kPiece > kStagedElements;
+        const auto run = [&](auto q, auto g, auto staging) {
+            k_adamw<decltype(q)::value, decltype(g)::value, decltype(staging)::value>
+                <<<grid, kThreads, 0, s>>>(tab, st);
+        };
+        const auto by_grad = [&](auto q, auto staging) {
+            if (grad_bf16)
+                run(q, std::true_type{}, staging);
+            else
+                run(q, std::false_type{}, staging);
+        };
+        if (q8)
+            by_grad(std::true_type{}, std::false_type{});
+        else if (staged)
+            by_grad(std::false_type{}, std::true_type{});
         else
-            k_adamw<false, false><<<grid, kThreads, 0, s>>>(tab, st);
+            by_grad(std::false_type{}, std::false_type{});
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -699,6 +699,26 @@ def test_adamw_dynamic_values_replace_the_descriptors():
     check_adam(before, after_of(tensors[0]), 32, dict(a, lr=float(np.float32(a["lr"]))))
 
 
+@pytest.mark.parametrize("grad", [F32, BF16], ids=["gf32", "gbf16"])
+@pytest.mark.parametrize("offset", [0, 1], ids=["aligned", "unaligned"])
+def test_adamw_many_elements_in_fp32(offset, grad):
+    """Around 2^27 elements in a launch: the last of two tensors is checked, and both their ends."""
+    for first in ((1 << 27) - 3000, 1 << 27):
+        big, small = (adam_inputs([n], 32, grad, seed=3, offset=offset)[0] for n in (2048, 1999))
+        wide = {}
+        for key, v in big.items():
+            buf = torch.zeros(first + offset, dtype=v.dtype, device="cuda")[offset:]
+            buf[:1000], buf[-1048:] = v[:1000], v[1000:]
+            wide[key] = buf
+        before = [{key: v.clone() for key, v in t.items()} for t in (big, small)]
+        opt = adam_desc(32, grad)
+        occ.occ_adamw_step(opt, occ.AdamwTensors(opt, [wide, small]))
+        ends = {key: torch.cat([wide[key][:1000], wide[key][-1048:]]) for key in ("p", "m", "v")}
+        check_adam(before[0], ends, 32)
+        check_adam(before[1], small, 32)
+        assert not wide["p"][1000:-1048].any() and not wide["v"][1000:-1048].any()
+
+
 def test_adamw_largest_sizes_reach_the_last_element():
     """Offsets beyond 2^31 bytes: a tensor of 2^30 + 3 elements with 8-bit states."""
     n = (1 << 30) + 3
