@@ -418,26 +418,26 @@ struct DxTile<float, MB, WN> {
     };
 };
 
-// One workgroup per tile.  Without SMALL there are a tile's tokens and a
-// step's experts at least: a tile (a step) that would reach past the last
-// token (expert) starts early enough not to, and leaves out what others do.
-// SMALL takes the rest, with clamped addresses.
+// One tile by the 2 WN waves of thread tid; all threads of a workgroup, with
+// tiles or without, meet the same barriers.  Without SMALL there are a tile's
+// tokens and a step's experts at least: a tile (a step) that would reach past
+// the last token (expert) starts early enough not to, and leaves out what
+// others do.  SMALL takes the rest, with clamped addresses.
 template <typename E, int MB, int WN, bool SMALL>
-__device__ __forceinline__ void gate_dx_tile(unsigned block, const float *__restrict__ dl, unsigned T,
-                                             int d, int Ne, const DxArgs &A,
+__device__ __forceinline__ void gate_dx_tile(unsigned block, int tid, const float *__restrict__ dl,
+                                             unsigned T, int d, int Ne, const DxArgs &A,
                                              DxTile<E, MB, WN> (&lds)[2]) {
     const auto *__restrict__ wr = static_cast<const E *>(A.w_router);
     const auto *dx_in = static_cast<const E *>(A.dx_in);
     auto *dx = static_cast<E *>(A.dx);
-    const int groups = A.groups;
-    const unsigned tiles = A.shares;
     typedef DxTile<E, MB, WN> Tile;
     constexpr int kTokens = 32 * MB, kDepth = Tile::kDepth, kOwn = kDepth / 4;
     constexpr bool kBf16 = sizeof(E) == 2;
     int group;
     unsigned tile;
-    if (!share_of(block, groups, tiles, group, tile)) return;
-    const int tid = threadIdx.x, l = lane_id(), i16 = l & 15, G = l >> 4;
+    const bool mine = share_of(block, A.groups, A.shares, group, tile);
+    if (!mine) tile = 0;  // computed once more and not stored
+    const int l = lane_id(), i16 = l & 15, G = l >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(tid / kWave), wm = wv / WN, wn = wv % WN;
     const int c0 = group * 64 * WN;
     const unsigned first = tile * kTokens, t0 = SMALL ? first : min(first, T - kTokens);
@@ -586,7 +586,7 @@ __device__ __forceinline__ void gate_dx_tile(unsigned block, const float *__rest
             }
         }
     }
-    if (c >= d) return;
+    if (c >= d || !mine) return;
     E *to = dx + static_cast<size_t>(t0) * d;
 #pragma unroll
     for (int m = 0; m < MB; m++)
@@ -608,28 +608,35 @@ __global__ __launch_bounds__(2 * WN *kWave, 4) void k_gate_dx_tile(const float *
                                                                    unsigned T, int d, int Ne,
                                                                    const DxArgs dx) {
     __shared__ DxTile<E, MB, WN> lds[2];
-    gate_dx_tile<E, MB, WN, SMALL>(blockIdx.x, dl, T, d, Ne, dx, lds);
+    gate_dx_tile<E, MB, WN, SMALL>(blockIdx.x, threadIdx.x, dl, T, d, Ne, dx, lds);
 }
 
-// bf16, both products: those of dx in the form that DX names.
-enum DxKind { kRegsVec, kRegs, kTile, kSmallTile };
+// bf16, both products: those of dx in the form that DX names.  A pair of
+// small tiles lies dx.blocks apart, on one XCD.
+enum DxKind { kRegsVec, kRegs, kTile, kPair, kSmallPair };
 template <int MB, int DX>
 __global__ __launch_bounds__(kBfThreads) void k_gate_bwd(const float *__restrict__ dl, unsigned T,
                                                          int d, int Ne, const DwArgs dw,
                                                          const DxArgs dx, bool dx_first) {
     typedef DxTile<uint16_t, 4, 4> Tile;
-    constexpr bool kTiles = DX == kTile || DX == kSmallTile;
-    __shared__ __attribute__((aligned(16))) char
-        lds[kTiles ? std::max(DwLds<MB>::kBytes, 2 * sizeof(Tile)) : DwLds<MB>::kBytes];
+    typedef DxTile<uint16_t, 2, 2> Half;
+    constexpr size_t kTileBytes = DX >= kPair ? 4 * sizeof(Half) : DX >= kTile ? 2 * sizeof(Tile) : 0;
+    __shared__ __attribute__((aligned(16))) char lds[std::max(DwLds<MB>::kBytes, kTileBytes)];
     bool is_dw;
     const unsigned block = own_block(dw, dx, dx_first, is_dw);
-    if (is_dw)
+    if (is_dw) {
         gate_dw<MB>(block, dl, T, d, Ne, dw, lds);
-    else if constexpr (kTiles)
-        gate_dx_tile<uint16_t, 4, 4, DX == kSmallTile>(block, dl, T, d, Ne, dx,
-                                                       *reinterpret_cast<Tile(*)[2]>(lds));
-    else
+    } else if constexpr (DX >= kPair) {
+        const int half = threadIdx.x / (kBfThreads / 2);
+        gate_dx_tile<uint16_t, 2, 2, DX == kSmallPair>(
+            block + half * dx.blocks, threadIdx.x % (kBfThreads / 2), dl, T, d, Ne, dx,
+            reinterpret_cast<Half(*)[2]>(lds)[half]);
+    } else if constexpr (DX >= kTile) {
+        gate_dx_tile<uint16_t, 4, 4, false>(block, threadIdx.x, dl, T, d, Ne, dx,
+                                            *reinterpret_cast<Tile(*)[2]>(lds));
+    } else {
         gate_dx<(MB + 1) / 2, DX == kRegsVec>(block, dl, T, d, Ne, dx);
+    }
 }
 
 // fp32: a wave makes 16 MB experts x 64 columns of dW_r from a quarter of the
@@ -739,7 +746,8 @@ __global__ __launch_bounds__(kThreads) void k_gate_bwd_f32(const float *__restri
     if (is_dw)
         gate_dw_f32<MB>(block, dl, T, d, Ne, dw, *reinterpret_cast<DwSums<MB> *>(lds));
     else
-        gate_dx_tile<float, 2, 2, SMALL>(block, dl, T, d, Ne, dx, *reinterpret_cast<Tile(*)[2]>(lds));
+        gate_dx_tile<float, 2, 2, SMALL>(block, threadIdx.x, dl, T, d, Ne, dx,
+                                         *reinterpret_cast<Tile(*)[2]>(lds));
 }
 
 // dw = the sum of the token shares' partial sums: thread (i, q) adds shares q,
@@ -817,7 +825,7 @@ hipError_t launch_gate_bwd(const float *dl, const void *x, const void *w_router,
     typedef integral_constant<int, 1> I1;
     typedef integral_constant<int, 2> I2;
     typedef integral_constant<int, 4> I4;
-    // dx in tiles of 32 MB x 64 WN; true: smaller than a tile
+    // dx in tiles of 32 MB x 64 WN; true: fewer tokens or experts than one takes
     const auto tiles_of = [&](auto e, auto mb, auto wn) {
         constexpr int MB = decltype(mb)::value, WN = decltype(wn)::value;
         X.groups = ceil_div(d, 64 * WN);
@@ -825,13 +833,12 @@ hipError_t launch_gate_bwd(const float *dl, const void *x, const void *w_router,
         X.blocks = whole_xcds(share_grid(X.groups, X.shares));
         return T < 32 * MB || Ne < DxTile<decltype(e), MB, WN>::kDepth;
     };
-    const auto tiles_alone = [&](auto e, auto mb, auto wn) {
+    const auto small_tiles_alone = [&](auto e) {
         typedef decltype(e) E;
-        constexpr int MB = decltype(mb)::value, WN = decltype(wn)::value;
-        if (tiles_of(e, mb, wn))
-            k_gate_dx_tile<E, MB, WN, true><<<X.blocks, 2 * WN * kWave, 0, s>>>(dl, T, d, Ne, X);
+        if (tiles_of(e, I2{}, I2{}))
+            k_gate_dx_tile<E, 2, 2, true><<<X.blocks, 4 * kWave, 0, s>>>(dl, T, d, Ne, X);
         else
-            k_gate_dx_tile<E, MB, WN, false><<<X.blocks, 2 * WN * kWave, 0, s>>>(dl, T, d, Ne, X);
+            k_gate_dx_tile<E, 2, 2, false><<<X.blocks, 4 * kWave, 0, s>>>(dl, T, d, Ne, X);
     };
     // Long shares of dW_r are the finer work and follow dx's workgroups, which
     // each walk over many tiles (T = 32768, d = 2048, 30 experts: 83 us against
@@ -852,7 +859,7 @@ hipError_t launch_gate_bwd(const float *dl, const void *x, const void *w_router,
                 k_gate_bwd_f32<MB, false><<<W.blocks + X.blocks, kThreads, 0, s>>>(dl, T, d, Ne, W, X);
         };
         if (!dw)
-            tiles_alone(float{}, I2{}, I2{});
+            small_tiles_alone(float{});
         else if (Ne <= 16)
             run(I1{});
         else if (Ne <= 32)
@@ -860,19 +867,32 @@ hipError_t launch_gate_bwd(const float *dl, const void *x, const void *w_router,
         else
             run(I4{});
     } else if (dx && Ne > 64) {
-        // W_r no longer fits a wave's registers.  dx alone: large tiles where
-        // there is one for every CU (130 experts, d = 2048: T = 4096 15.8 us
-        // against 16.0, T = 8192 25.7 against 30.5) and small ones below
-        // (T = 512 6.8 against 11.0).
+        // W_r no longer fits a wave's registers.  Large tiles where there is one
+        // for every CU (130 experts, d = 2048, dx alone: T = 4096 15.8 us against
+        // 16.0, T = 8192 25.7 against 30.5) and small ones below (T = 512 6.8
+        // against 11.0); beside dW_r, whose registers leave a CU one workgroup,
+        // for every fourth, and two small ones to a workgroup (250 experts: T =
+        // 64 12.2 against 18.4, T = 512 16.2 against 17.8, T = 2048 27.8 against
+        // 22.9).  (d is at most 8192: a large tile is full.)
+        const bool large =
+            static_cast<int64_t>(ceil_div(T, 128)) * ceil_div(d, 256) >= (dw ? 64 : 256);
         if (!dw) {
-            if (static_cast<int64_t>(ceil_div(T, 128)) * ceil_div(d, 256) >= 256)
-                tiles_alone(uint16_t{}, I4{}, I4{});
-            else
-                tiles_alone(uint16_t{}, I2{}, I2{});
-        } else if (tiles_of(uint16_t{}, I4{}, I4{})) {
-            both(I4{}, integral_constant<int, kSmallTile>{}, kBfThreads);
-        } else {
+            if (large) {
+                tiles_of(uint16_t{}, I4{}, I4{});
+                k_gate_dx_tile<uint16_t, 4, 4, false><<<X.blocks, 8 * kWave, 0, s>>>(dl, T, d, Ne, X);
+            } else {
+                small_tiles_alone(uint16_t{});
+            }
+        } else if (large) {
+            tiles_of(uint16_t{}, I4{}, I4{});
             both(I4{}, integral_constant<int, kTile>{}, kBfThreads);
+        } else {
+            const bool small = tiles_of(uint16_t{}, I2{}, I2{});
+            X.blocks = whole_xcds(ceil_div(X.blocks, 2));
+            if (small)
+                both(I4{}, integral_constant<int, kSmallPair>{}, kBfThreads);
+            else
+                both(I4{}, integral_constant<int, kPair>{}, kBfThreads);
         }
     } else {
         // dx alone in smaller workgroups, for the same waves on more CUs

@@ -401,7 +401,8 @@ GATE_SHAPES = [(BF16, T, d, Ne) for T, d, Ne in
                 (127, 2048, 33), (128, 64, 60), (129, 2112, 64), (300, 512, 65), (1000, 256, 100),
                 (257, 128, 128), (90, 576, 130), (513, 2048, 256), (3000, 128, 60),
                 (40000, 64, 30), (8200, 1024, 70), (5000, 1984, 67), (40, 8192, 200),
-                (128, 320, 66), (3000, 8192, 20)]] + \
+                (128, 320, 66), (3000, 8192, 20), (1100, 2048, 90), (64, 2048, 250), (63, 128, 129),
+                (1000, 2048, 65), (129, 8192, 96), (130, 128, 250)]] + \
               [(F32, T, d, Ne) for T, d, Ne in
                [(1, 16, 1), (5, 48, 3), (63, 80, 8), (64, 128, 17), (65, 272, 60), (300, 64, 64),
                 (1000, 144, 65), (130, 1024, 129), (77, 336, 256), (20000, 32, 8), (700, 4096, 31), (64, 16, 16), (9, 64, 250)]]
