@@ -386,7 +386,7 @@ __device__ __forceinline__ void gate_dw(unsigned block, const float *__restrict_
 }
 
 // dx for every fp32 shape and for bf16 with more than 64 experts: tiles of
-// 32 MB tokens x 64 WN columns by 2 WN waves (128 x 256 or 64 x 128), the
+// 32 MB tokens x 64 WN columns by 2 WN waves (32 x 64 to 128 x 256), the
 // experts contracted in steps of kDepth through LDS (two buffers; the next
 // step's operands are in flight in registers).  Wave (wm, wn) of 2 x WN makes
 // 16 MB tokens x 64 columns; column 4 i + ni of those is column i of fragment
@@ -613,7 +613,7 @@ __global__ __launch_bounds__(2 * WN *kWave, 4) void k_gate_dx_tile(const float *
 
 // bf16, both products: those of dx in the form that DX names.  A pair of
 // small tiles lies dx.blocks apart, on one XCD.
-enum DxKind { kRegsVec, kRegs, kTile, kPair, kSmallPair };
+enum DxKind { kRegsVec, kRegs, kTile, kSmallTile, kPair, kSmallPair };
 template <int MB, int DX>
 __global__ __launch_bounds__(kBfThreads) void k_gate_bwd(const float *__restrict__ dl, unsigned T,
                                                          int d, int Ne, const DwArgs dw,
@@ -735,19 +735,28 @@ __device__ __forceinline__ void gate_dw_f32(unsigned block, const float *__restr
         }
 }
 
-template <int MB, bool SMALL>
+// fp32, both products.
+template <int MB, int DX>
 __global__ __launch_bounds__(kThreads) void k_gate_bwd_f32(const float *__restrict__ dl, unsigned T,
                                                            int d, int Ne, const DwArgs dw,
                                                            const DxArgs dx) {
     typedef DxTile<float, 2, 2> Tile;
-    __shared__ __attribute__((aligned(16))) char lds[std::max(sizeof(DwSums<MB>), 2 * sizeof(Tile))];
+    typedef DxTile<float, 1, 1> Half;
+    __shared__ __attribute__((aligned(16))) char
+        lds[std::max(sizeof(DwSums<MB>), DX >= kPair ? 4 * sizeof(Half) : 2 * sizeof(Tile))];
     bool is_dw;
     const unsigned block = own_block(dw, dx, false, is_dw);
-    if (is_dw)
+    if (is_dw) {
         gate_dw_f32<MB>(block, dl, T, d, Ne, dw, *reinterpret_cast<DwSums<MB> *>(lds));
-    else
-        gate_dx_tile<float, 2, 2, SMALL>(block, threadIdx.x, dl, T, d, Ne, dx,
-                                         *reinterpret_cast<Tile(*)[2]>(lds));
+    } else if constexpr (DX >= kPair) {
+        const int half = threadIdx.x / (kThreads / 2);
+        gate_dx_tile<float, 1, 1, DX == kSmallPair>(
+            block + half * dx.blocks, threadIdx.x % (kThreads / 2), dl, T, d, Ne, dx,
+            reinterpret_cast<Half(*)[2]>(lds)[half]);
+    } else {
+        gate_dx_tile<float, 2, 2, DX == kSmallTile>(block, threadIdx.x, dl, T, d, Ne, dx,
+                                                    *reinterpret_cast<Tile(*)[2]>(lds));
+    }
 }
 
 // dw = the sum of the token shares' partial sums: thread (i, q) adds shares q,
@@ -849,23 +858,46 @@ hipError_t launch_gate_bwd(const float *dl, const void *x, const void *w_router,
             <<<W.blocks + X.blocks, threads, 0, s>>>(dl, T, d, Ne, W, X, dx_first);
     };
     if (!bf16) {
-        // dx alone has more waves on a CU in its own kernel (T = 4096, d = 2048:
-        // 8 experts 16 us against 21, 250 47 against 49)
-        const auto run = [&](auto mb) {
-            constexpr int MB = decltype(mb)::value;
-            if (dx && tiles_of(float{}, I2{}, I2{}))
-                k_gate_bwd_f32<MB, true><<<W.blocks + X.blocks, kThreads, 0, s>>>(dl, T, d, Ne, W, X);
-            else
-                k_gate_bwd_f32<MB, false><<<W.blocks + X.blocks, kThreads, 0, s>>>(dl, T, d, Ne, W, X);
+        const auto both_f32 = [&](auto mb, auto kind) {
+            k_gate_bwd_f32<decltype(mb)::value, decltype(kind)::value>
+                <<<W.blocks + X.blocks, kThreads, 0, s>>>(dl, T, d, Ne, W, X);
         };
-        if (!dw)
-            small_tiles_alone(float{});
-        else if (Ne <= 16)
+        const auto run = [&](auto mb) {
+            if (dx && tiles_of(float{}, I2{}, I2{}))
+                both_f32(mb, integral_constant<int, kSmallTile>{});
+            else
+                both_f32(mb, integral_constant<int, kTile>{});
+        };
+        // Fewer 64 x 128 tiles than CUs: 32 x 64 (dx alone, d = 2048, 250 experts:
+        // T = 64 10.0 us against 14.9, T = 512 14.9 against 16.1, T = 2048 28.9
+        // against 27.4), beside dW_r a pair of them with several groups of
+        // experts (T = 64 12.2 against 15.2; 64 experts 7.5 against 7.2).
+        const bool few = static_cast<int64_t>(ceil_div(T, 64)) * ceil_div(d, 128) < 256;
+        if (!dw) {
+            // dx alone has more waves on a CU in its own kernel (T = 4096, d =
+            // 2048: 8 experts 16 us against 21, 250 47 against 49)
+            if (few) {
+                if (tiles_of(float{}, I1{}, I1{}))
+                    k_gate_dx_tile<float, 1, 1, true><<<X.blocks, 2 * kWave, 0, s>>>(dl, T, d, Ne, X);
+                else
+                    k_gate_dx_tile<float, 1, 1, false><<<X.blocks, 2 * kWave, 0, s>>>(dl, T, d, Ne, X);
+            } else {
+                small_tiles_alone(float{});
+            }
+        } else if (Ne <= 16) {
             run(I1{});
-        else if (Ne <= 32)
+        } else if (Ne <= 32) {
             run(I2{});
-        else
+        } else if (dx && few && Ne > kDwExperts) {
+            const bool small = tiles_of(float{}, I1{}, I1{});
+            X.blocks = whole_xcds(ceil_div(X.blocks, 2));
+            if (small)
+                both_f32(I4{}, integral_constant<int, kSmallPair>{});
+            else
+                both_f32(I4{}, integral_constant<int, kPair>{});
+        } else {
             run(I4{});
+        }
     } else if (dx && Ne > 64) {
         // W_r no longer fits a wave's registers.  Large tiles where there is one
         // for every CU (130 experts, d = 2048, dx alone: T = 4096 15.8 us against

@@ -405,7 +405,9 @@ GATE_SHAPES = [(BF16, T, d, Ne) for T, d, Ne in
                 (1000, 2048, 65), (129, 8192, 96), (130, 128, 250)]] + \
               [(F32, T, d, Ne) for T, d, Ne in
                [(1, 16, 1), (5, 48, 3), (63, 80, 8), (64, 128, 17), (65, 272, 60), (300, 64, 64),
-                (1000, 144, 65), (130, 1024, 129), (77, 336, 256), (20000, 32, 8), (700, 4096, 31), (64, 16, 16), (9, 64, 250)]]
+                (1000, 144, 65), (130, 1024, 129), (77, 336, 256), (20000, 32, 8), (700, 4096, 31), (64, 16, 16), (9, 64, 250),
+                (31, 2048, 70), (33, 80, 100), (500, 2048, 250), (600, 4096, 66), (1100, 2048, 9),
+                (1040, 2048, 40)]]
 
 
 def gate_inputs(dtype, T, d, Ne, seed):
