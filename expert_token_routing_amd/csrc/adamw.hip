@@ -92,12 +92,15 @@ __device__ __forceinline__ uint32_t to_e4m3(const float (&v)[4]) {
 }
 
 // The wave's 256 values as codes, and their unit.  keep[j]: a value that is
-// not zero keeps a code that is not.
+// not zero keeps a code that is not.  One value that is not finite makes the
+// unit so and with it all 256: an infinity is the largest magnitude, a NaN,
+// which a maximum passes over, is looked for by itself.
 template <bool KEEP>
 __device__ __forceinline__ uint32_t quantise(const float (&v)[4], const float (&keep)[4],
                                              float &unit) {
-    const float top = wave_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])),
-                                     fmaxf(fabsf(v[2]), fabsf(v[3]))));
+    float top = wave_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])),
+                               fmaxf(fabsf(v[2]), fabsf(v[3]))));
+    if (__any(__builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3]))) top = NAN;
     unit = 0.f;
     float c[4] = {0.f, 0.f, 0.f, 0.f};
     if (!(top < kSmallest)) {
@@ -106,7 +109,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&v)[4], const float (&
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             c[j] = v[j] * per;
-            // NaN (from a gradient that is not finite) passes both
+            // NaN passes both
             c[j] = c[j] > kE4m3Max ? kE4m3Max : c[j] < -kE4m3Max ? -kE4m3Max : c[j];
             if (KEEP && keep[j] > 0.f && c[j] < kE4m3Min) c[j] = kE4m3Min;
         }
