@@ -816,9 +816,10 @@ occ_status occ_adamw_step(const occ_adamw_desc *opt, const occ_adamw_tensor *ten
     const size_t ms = q8 ? 1 : 4;
     std::vector<AdamwTensor> list;
     std::vector<const void *> written;  // each once
+    constexpr int kOutputs = 6;
     try {
         list.reserve(count);
-        written.reserve(static_cast<size_t>(count) * 3);
+        written.reserve(static_cast<size_t>(count) * kOutputs);
     } catch (...) {
         return OCC_ERR_UNSUPPORTED;
     }
@@ -842,11 +843,26 @@ occ_status occ_adamw_step(const occ_adamw_desc *opt, const occ_adamw_tensor *ten
             return OCC_ERR_INVALID_ARG;
         list.push_back({t.n, t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.p_out, t.m_out, t.v_out,
                         t.m_scale_out, t.v_scale_out, t.p_bf16, fits(4)});
-        written.insert(written.end(), {t.p_out, t.m_out, t.v_out});
+        for (const void *out : {static_cast<const void *>(t.p_out), static_cast<const void *>(t.m_out),
+                                static_cast<const void *>(t.v_out),
+                                static_cast<const void *>(t.m_scale_out),
+                                static_cast<const void *>(t.v_scale_out),
+                                static_cast<const void *>(t.p_bf16)})
+            if (out) written.push_back(out);
     }
     std::sort(written.begin(), written.end());
     if (std::adjacent_find(written.begin(), written.end()) != written.end())
         return OCC_ERR_INVALID_ARG;
+    // an array that is read is written by its own new value or not at all
+    const auto kept = [&](const void *in, const void *own) {
+        return !in || in == own || !std::binary_search(written.begin(), written.end(), in);
+    };
+    for (const AdamwTensor &t : list)
+        if (!kept(t.p, t.p_out) || !kept(t.g, nullptr) || !kept(t.m, t.m_out) ||
+            !kept(t.v, t.v_out) || !kept(t.m_scale, t.m_scale_out) ||
+            !kept(t.v_scale, t.v_scale_out))
+            return OCC_ERR_INVALID_ARG;
+    if (!kept(dynamic, nullptr)) return OCC_ERR_INVALID_ARG;
     AdamwStep st;
     const double step = static_cast<double>(opt->step);
     st.lr = static_cast<float>(opt->lr);

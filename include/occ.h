@@ -585,9 +585,9 @@ typedef struct occ_adamw_desc {
  * it is the new value of (the usual step in place) or another one; m_scale
  * and v_scale (ceil(n / OCC_ADAMW_BLOCK) fp32) only with 8-bit states, NULL
  * otherwise.  p is fp32; p_bf16 is NULL or receives the new p rounded to
- * bf16, the copy that the layer computes with.  Within a call each p_out, m_out
- * and v_out is another array (a tensor listed twice would be updated twice at
- * once). */
+ * bf16, the copy that the layer computes with.  Beyond that, what a call writes
+ * is no other array of the call, of this tensor or another one (a tensor listed
+ * twice would be updated twice at once). */
 typedef struct occ_adamw_tensor {
     int64_t n;
     const float *p;
@@ -610,8 +610,8 @@ typedef struct occ_adamw_tensor {
  * A gradient that is not finite makes its element's p, m and v so (with 8-bit
  * states its whole block's); tensors aligned to 16 bytes are faster.
  * Errors: INVALID_ARG (a value out of the ranges above, a missing or
- * superfluous pointer, an array not aligned to its elements, the same p_out,
- * m_out or v_out twice), UNSUPPORTED (n > 2^33). */
+ * superfluous pointer, an array not aligned to its elements, an output that
+ * starts like another array than its own old value), UNSUPPORTED (n > 2^33). */
 occ_status occ_adamw_step(const occ_adamw_desc *opt, const occ_adamw_tensor *tensors_host,
                           int32_t count, const float *dynamic, void *stream);
 

@@ -1,0 +1,68 @@
+"""Refusals of the operators around the layer on the host (no GPU): arrays that a call writes and
+that start like another array of the call."""
+import ctypes
+
+import pytest
+
+from expert_token_routing_amd import occ
+from test_block_host import ADAM, INV, L, NULL  # noqa: F401
+
+# A tensor of its own arrays, and one of 8-bit states; written in place unless told otherwise.
+ROW = dict(n=8, p=0x1000, g=0x2000, m=0x3000, v=0x4000, p_out=0x1000, m_out=0x3000, v_out=0x4000)
+UNITS = dict(m_scale=0x5000, v_scale=0x6000, m_scale_out=0x5000, v_scale_out=0x6000)
+
+
+def other(row):
+    """The same tensor somewhere else."""
+    return {key: v if key == "n" else v + 0x100000 for key, v in row.items()}
+
+
+def adam_rows(L, rows, dynamic=NULL, **opt):
+    table = (occ.AdamwTensor * len(rows))(*[occ.AdamwTensor(**r) for r in rows])
+    desc = occ.AdamwDesc(**{**ADAM, **opt})
+    return L.occ_adamw_step(ctypes.byref(desc), table, len(rows), dynamic, NULL)
+
+
+@pytest.mark.parametrize("over", [
+    dict(p_bf16=0x1000), dict(p_bf16=0x2000), dict(p_bf16=0x3000), dict(p_bf16=0x4000),
+    dict(p_out=0x2000), dict(m_out=0x2000), dict(v_out=0x2000),      # over the gradient
+    dict(p_out=0x3000, m_out=0x7000), dict(m_out=0x4000, v_out=0x7000),
+    dict(v_out=0x1000, p_out=0x7000),                                 # over another one's old value
+], ids=str)
+def test_adamw_refuses_an_output_in_another_array(L, over):
+    assert adam_rows(L, [{**ROW, **over}]) == INV
+    assert adam_rows(L, [other(ROW), {**ROW, **over}]) == INV
+
+
+@pytest.mark.parametrize("over", [
+    dict(m_scale_out=0x6000, v_scale_out=0x6000), dict(m_scale_out=0x1000), dict(v_scale_out=0x3000),
+    dict(m_scale_out=0x6000, v_scale_out=0x7000), dict(v_scale_out=0x2000), dict(p_bf16=0x5000),
+    dict(p_bf16=0x6000), dict(p_out=0x5000), dict(m_out=0x6000),
+], ids=str)
+def test_adamw_refuses_units_in_another_array(L, over):
+    row = {**ROW, **UNITS}
+    assert adam_rows(L, [{**row, **over}], state=1) == INV
+    assert adam_rows(L, [{**row, **over}, other(row)], state=1) == INV
+
+
+@pytest.mark.parametrize("name", ["p", "g", "m", "v", "m_scale", "v_scale"])
+@pytest.mark.parametrize("out", ["p_out", "m_out", "v_out", "m_scale_out", "v_scale_out", "p_bf16"])
+def test_adamw_refuses_an_output_in_an_array_of_another_tensor(L, out, name):
+    row = {**ROW, **UNITS}
+    second = {**other(row), out: row[name]}
+    assert adam_rows(L, [row, second], state=1) == INV
+    assert adam_rows(L, [second, row], state=1) == INV
+    # out of place: no output of the first tensor stands in the way
+    away = {**row, **{key: v + 0x200000 for key, v in row.items() if key.endswith("_out")}}
+    assert adam_rows(L, [away, second], state=1) == INV
+
+
+@pytest.mark.parametrize("out", ["m_scale_out", "v_scale_out", "p_bf16"])
+def test_adamw_refuses_units_and_copies_written_by_two_tensors(L, out):
+    row = {**ROW, **UNITS, "p_bf16": 0x7000}
+    assert adam_rows(L, [row, {**other(row), out: row[out]}], state=1) == INV
+
+
+def test_adamw_refuses_an_output_in_the_dynamic_values(L):
+    assert adam_rows(L, [{**ROW, "p_bf16": 0x7000}], dynamic=ctypes.c_void_p(0x7000)) == INV
+    assert adam_rows(L, [ROW], dynamic=ctypes.c_void_p(0x1000)) == INV
