@@ -735,7 +735,8 @@ occ_status occ_block_norm_backward(const occ_layer_desc *desc, const occ_norm_de
         !apart(dy, w_post, gate, w_pre, dw_post, dgate, dw_pre) ||
         !apart(dw_post, dr, dh, r, y, w_post, gate, w_pre, dgate, dw_pre) ||
         !apart(dw_pre, dr, dh, r, y, w_post, gate, w_pre, dgate) ||
-        !apart(dgate, dr, dh, r, y, w_post, w_pre, opt->gate == OCC_GATE_TOKEN ? nullptr : gate))
+        !apart(dgate, dr, dh, r, y, w_post, w_pre, opt->gate == OCC_GATE_TOKEN ? nullptr : gate) ||
+        !apart(workspace, dr, dh, r, y, w_post, gate, w_pre, dx, dy, dw_post, dgate, dw_pre))
         return OCC_ERR_INVALID_ARG;
     OCC_TRY(check_ws(*desc, workspace, ws_bytes, block_ws_bytes(*desc)));
     OCC_HIP(launch_block_norm_back(dr, dh, r, y, w_post, gate, w_pre, desc->T, desc->d,
@@ -753,7 +754,8 @@ occ_status occ_balance_loss(const occ_layer_desc *desc, const occ_balance_desc *
     if (!logits || !ids || !counts || !probs || !loss) return OCC_ERR_INVALID_ARG;
     if (!aligned_to(logits, 4) || !aligned_to(ids, 4) || !aligned_to(counts, 4) ||
         !aligned_to(probs, 4) || !aligned_to(loss, 4) || !apart(counts, logits, ids, valid, probs, loss) ||
-        !apart(probs, logits, ids, valid, loss) || !apart(loss, logits, ids, valid))
+        !apart(probs, logits, ids, valid, loss) || !apart(loss, logits, ids, valid) ||
+        !apart(workspace, logits, ids, valid, counts, probs, loss))
         return OCC_ERR_INVALID_ARG;
     PlaceTab tab;
     OCC_TRY(balance_tab(*desc, opt, placement_host, &tab));
@@ -789,7 +791,8 @@ occ_status occ_gate_backward(const occ_layer_desc *desc, const float *dlogits, c
     if (dx ? !w_router : !!dx_in) return OCC_ERR_INVALID_ARG;
     if (dw_router && !x) return OCC_ERR_INVALID_ARG;
     if (!aligned_to(dlogits, 4) || !rows_aligned(x, w_router, dx_in, dx, dw_router) ||
-        !apart(dx, dlogits, w_router) || !apart(dw_router, dlogits, x, w_router, dx_in, dx))
+        !apart(dx, dlogits, w_router) || !apart(dw_router, dlogits, x, w_router, dx_in, dx) ||
+        (dw_router && !apart(workspace, dlogits, x, w_router, dx_in, dx, dw_router)))
         return OCC_ERR_INVALID_ARG;
     if (dw_router) OCC_TRY(check_ws(*desc, workspace, ws_bytes, block_ws_bytes(*desc)));
     const int bf16 = desc->dtype == OCC_BF16;

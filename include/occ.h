@@ -419,9 +419,9 @@ occ_status occ_moe_backward(const occ_layer_desc *desc, const void *dy, const vo
  * arrays aligned to their elements (INVALID_ARG otherwise).  An output of rows
  * may be the very same array as an input of the same rows: r or h as x or y,
  * dx or dy as dr, dh, r or y, a token gate's dgate as gate, dlogits as logits
- * or dlogits_in, occ_gate_backward's dx as x or dx_in.  Otherwise outputs
- * overlap nothing (INVALID_ARG where they start like another array of the
- * call).  All of them are deterministic: no atomic
+ * or dlogits_in, occ_gate_backward's dx as x or dx_in.  Otherwise outputs and
+ * the workspace overlap nothing (INVALID_ARG where they start like another
+ * array of the call).  All of them are deterministic: no atomic
  * additions of floating-point values, sums in an order fixed by the sizes. */
 
 /* Bytes of device workspace that occ_block_norm_backward, occ_balance_loss

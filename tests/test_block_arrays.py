@@ -1,11 +1,12 @@
-"""Refusals of the operators around the layer on the host (no GPU): arrays that a call writes and
-that start like another array of the call."""
+"""Refusals of the operators around the layer on the host (no GPU): arrays that a call writes, its
+workspace among them, and that start like another array of the call."""
 import ctypes
 
 import pytest
 
 from expert_token_routing_amd import occ
-from test_block_host import ADAM, INV, L, NULL  # noqa: F401
+from test_block_host import (ADAM, INV, L, NULL, balance_status, fake, gate_status,  # noqa: F401
+                             norm_back_status)
 
 # A tensor of its own arrays, and one of 8-bit states; written in place unless told otherwise.
 ROW = dict(n=8, p=0x1000, g=0x2000, m=0x3000, v=0x4000, p_out=0x1000, m_out=0x3000, v_out=0x4000)
@@ -66,3 +67,21 @@ def test_adamw_refuses_units_and_copies_written_by_two_tensors(L, out):
 def test_adamw_refuses_an_output_in_the_dynamic_values(L):
     assert adam_rows(L, [{**ROW, "p_bf16": 0x7000}], dynamic=ctypes.c_void_p(0x7000)) == INV
     assert adam_rows(L, [ROW], dynamic=ctypes.c_void_p(0x1000)) == INV
+
+
+@pytest.mark.parametrize("name", ["dr", "dh", "r", "y", "w_post", "w_pre", "gate", "dx", "dy",
+                                  "dw_post", "dw_pre", "dgate"])
+def test_norm_backward_refuses_a_workspace_in_another_array(L, name):
+    opt = occ.NormDesc(eps=1e-6, scale=1.0, gate=1)
+    arrays = dict(gate=fake(12), dgate=fake(13))
+    assert norm_back_status(L, opt=opt, **{**arrays, name: fake(11)}) == INV
+
+
+@pytest.mark.parametrize("name", ["logits", "ids", "valid", "counts", "probs", "loss"])
+def test_balance_refuses_a_workspace_in_another_array(L, name):
+    assert balance_status(L, **{name: fake(6)}) == INV
+
+
+@pytest.mark.parametrize("name", ["dlogits", "x", "w_router", "dx_in", "dx", "dw"])
+def test_gate_backward_refuses_a_workspace_in_another_array(L, name):
+    assert gate_status(L, **{name: fake(7)}) == INV
