@@ -805,14 +805,14 @@ occ_status occ_gate_backward(const occ_layer_desc *desc, const float *dlogits, c
 occ_status occ_adamw_step(const occ_adamw_desc *opt, const occ_adamw_tensor *tensors_host,
                           int32_t count, const float *dynamic, void *stream) {
     if (!opt || count < 0 || (count > 0 && !tensors_host)) return OCC_ERR_INVALID_ARG;
-    const auto ranged = [](double v, double lo, bool open) {
-        return std::isfinite(v) && (open ? v > lo : v >= lo);
-    };
+    // as the fp32 values that the kernel computes with
+    const auto finite = [](double v) { return std::isfinite(static_cast<float>(v)); };
+    const auto ranged = [&](double v) { return finite(v) && v >= 0.; };
     if ((opt->state != OCC_ADAMW_32BIT && opt->state != OCC_ADAMW_8BIT) ||
-        (opt->grad_dtype != OCC_F32 && opt->grad_dtype != OCC_BF16) || !ranged(opt->lr, 0., false) ||
-        !ranged(opt->beta1, 0., false) || opt->beta1 >= 1. || !ranged(opt->beta2, 0., false) ||
-        opt->beta2 >= 1. || !(static_cast<float>(opt->eps) >= FLT_MIN) || !std::isfinite(opt->eps) ||
-        !ranged(opt->weight_decay, 0., false) || !std::isfinite(opt->grad_scale) || opt->step < 1 ||
+        (opt->grad_dtype != OCC_F32 && opt->grad_dtype != OCC_BF16) || !ranged(opt->lr) ||
+        !ranged(opt->beta1) || opt->beta1 >= 1. || !ranged(opt->beta2) || opt->beta2 >= 1. ||
+        !(static_cast<float>(opt->eps) >= FLT_MIN) || !finite(opt->eps) ||
+        !ranged(opt->weight_decay) || !finite(opt->grad_scale) || opt->step < 1 ||
         !aligned_to(dynamic, 4))
         return OCC_ERR_INVALID_ARG;
     const bool q8 = opt->state == OCC_ADAMW_8BIT, gb = opt->grad_dtype == OCC_BF16;

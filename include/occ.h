@@ -573,6 +573,7 @@ typedef enum occ_adamw_state { OCC_ADAMW_32BIT = 0, OCC_ADAMW_8BIT = 1 } occ_ada
 typedef struct occ_adamw_desc {
     int32_t state;       /* occ_adamw_state */
     int32_t grad_dtype;  /* occ_dtype of the gradients */
+    /* within fp32's range, as which the kernel takes them */
     double lr;           /* >= 0 */
     double beta1, beta2; /* in [0, 1) */
     double eps;          /* >= FLT_MIN */

@@ -1,11 +1,12 @@
 """Refusals of the operators around the layer on the host (no GPU): arrays that a call writes, its
-workspace among them, and that start like another array of the call."""
+workspace among them, and that start like another array of the call, and optimizer values beyond
+fp32."""
 import ctypes
 
 import pytest
 
 from expert_token_routing_amd import occ
-from test_block_host import (ADAM, INV, L, NULL, balance_status, fake, gate_status,  # noqa: F401
+from test_block_host import (ADAM, INV, L, NULL, adam_status, balance_status, fake, gate_status,  # noqa: F401
                              norm_back_status)
 
 # A tensor of its own arrays, and one of 8-bit states; written in place unless told otherwise.
@@ -85,3 +86,15 @@ def test_balance_refuses_a_workspace_in_another_array(L, name):
 @pytest.mark.parametrize("name", ["dlogits", "x", "w_router", "dx_in", "dx", "dw"])
 def test_gate_backward_refuses_a_workspace_in_another_array(L, name):
     assert gate_status(L, **{name: fake(7)}) == INV
+
+
+@pytest.mark.parametrize("opt", [dict(lr=1e39), dict(eps=1e39), dict(weight_decay=1e300),
+                                 dict(grad_scale=1e39), dict(grad_scale=-1e39)], ids=str)
+def test_adamw_refuses_values_beyond_fp32(L, opt):
+    assert adam_status(L, opt=opt, count=0) == INV
+
+
+@pytest.mark.parametrize("opt", [dict(lr=3e38), dict(eps=3e38), dict(weight_decay=3e38),
+                                 dict(grad_scale=-3e38), dict(lr=0.0), dict(lr=1e-60)], ids=str)
+def test_adamw_takes_the_values_that_fp32_holds(L, opt):
+    assert adam_status(L, opt=opt, count=0) == occ.OCC_OK
