@@ -4,10 +4,11 @@
 //
 // Mathematics (n(v) = v rstd(v), rstd = 1 / sqrt(mean v^2 + eps) by rows):
 //   r = x + s g w_post n(y),   h = w_pre n(r).
-// The gradient of <q, n(v)> in v is rstd q - v rstd^3 mean(q v), so a row's
+// The gradient of <q, n(v)> in v is rstd (q - n(v) mean(q n(v))), so a row's
 // backward needs three sums before dr' = dr + (gradient through h) is known
-// (r.r, (dh w_pre).r, y.y) and one after it ((dr' g w_post).y), which is also a
-// token gate's gradient.  The gradients of w_post and of a channel gate come
+// (r.r, (dh w_pre).r, y.y) and one after it ((dr' g w_post).n(y)), which is also
+// a token gate's gradient.  (With v rstd^3 mean(q v) behind rstd q a cube leaves
+// fp32 where rows and eps are small, and the gradient does not.)  The gradients of w_post and of a channel gate come
 // from one column sum, S = sum over rows of s g_token dr' n(y): gate S and
 // w_post S.
 //
@@ -365,36 +366,38 @@ __global__ __launch_bounds__(kBackBlock) void k_norm_back(NormBackArgs a, Column
         }
         row_sums<NT>(sums, slots, turn);
         const float rstd_r = rstd_of(sums[0], a.inv_d, a.eps);
-        const float back_r = sums[1] * a.inv_d * rstd_r * rstd_r * rstd_r;
+        const float mean_r = sums[1] * a.inv_d * rstd_r;  // of (dh w_pre) n(r)
         const float rstd_y = a.w_post ? rstd_of(sums[2], a.inv_d, a.eps) : 1.f;
-        const float to_y = a.scale * gt * rstd_y;
+        const float sg = a.scale * gt;
         // (without dh or y their terms are zero)
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            acc_r[i] = fmaf(dh[i] * rstd_r, r[i], acc_r[i]);
-            q[i] = fmaf(-back_r, r[i], fmaf(rstd_r, w[i], q[i]));
+            r[i] *= rstd_r;  // n(r)
+            acc_r[i] = fmaf(dh[i], r[i], acc_r[i]);
+            q[i] = fmaf(rstd_r, fmaf(-mean_r, r[i], w[i]), q[i]);
         }
         // q is dr', and then dr' gate_ch w_post
         const Rows rows(t0, kRows, a.T, bytes);
         store_chunk(rows.of(a.dx), sub * bytes + at, Chunk<E>::pack(q));
-        float dot[1] = {0.f};  // (dr' gate_ch w_post).y
+        float dot[1] = {0.f};  // (dr' gate_ch w_post).n(y)
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            acc_y[i] = fmaf(q[i] * to_y, y[i], acc_y[i]);
+            y[i] *= rstd_y;  // n(y)
+            acc_y[i] = fmaf(q[i] * sg, y[i], acc_y[i]);
             q[i] *= gw[i];
             dot[0] = fmaf(q[i], y[i], dot[0]);
         }
-        float back_y = 0.f;
+        float mean_y = 0.f;
         if (a.w_post || gate_tok) {
             row_sums<NT>(dot, slots, turn);
-            if (a.w_post) back_y = dot[0] * to_y * a.inv_d * rstd_y * rstd_y;
+            if (a.w_post) mean_y = dot[0] * a.inv_d;
             if (gate_tok)
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(a.scale * rstd_y * dot[0]),
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(a.scale * dot[0]),
                                                       Rows(t0, kRows, a.T, 4).of(a.dgate_tok),
                                                       c == 0 ? sub * 4 : kNowhere, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < N; i++) q[i] = fmaf(to_y, q[i], -y[i] * back_y);
+        for (int i = 0; i < N; i++) q[i] = sg * rstd_y * fmaf(-mean_y, y[i], q[i]);
         store_chunk(rows.of(a.dy), sub * bytes + at, Chunk<E>::pack(q));
     }
 
