@@ -1,11 +1,13 @@
 """The operators around the layer on the GPU, where values go wrong: gradients that are not finite
-in the optimizer's states, and rows near the smallest normal number."""
+in the optimizer's states, rows near the smallest normal number, and weight gradients of whole
+numbers, whose sums are exact in every order, over one, several and very long shares of the tokens."""
 import pytest
 import torch
 
 from expert_token_routing_amd import occ
-from test_gpu_block import (BF16, F32, FORMS, SCALE, adam_desc, adam_inputs, check_norm, check_norm_back,
-                            moments, norm_inputs, run_norm, run_norm_back)
+from test_gpu_block import (BF16, F32, FORMS, GATE_SHAPES, SCALE, adam_desc, adam_inputs, check_norm,
+                            check_norm_back, gen, layer, moments, nan_like, norm_inputs, run_norm,
+                            run_norm_back)
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +89,77 @@ def test_norm_backward_of_rows_near_the_smallest_normal_number(dtype, T, d, form
     out = run_norm_back(t, grads, kept, opt, dtype)
     assert all(v.isfinite().all() for v in out.values() if v is not None)
     check_norm_back(t, grads, kept, opt, out)
+
+
+# ----------------------------------------------------- gate projection, back
+
+def whole(g, values, *shape):
+    at = torch.randint(len(values), shape, generator=g, device="cuda", dtype=torch.int8)
+    return torch.tensor(values, device="cuda", dtype=F32)[at.int()]
+
+
+def run_gate(dl, x, w, dx_in, dtype):
+    T, Ne = dl.shape
+    d = w.shape[1]
+    desc = layer(T, d, Ne=Ne, dtype=dtype)
+    dx, dw = nan_like((T, d), dtype), nan_like((Ne, d))
+    occ.occ_gate_backward(desc, dl, x, w, dx_in, dx, dw, occ.alloc_block_workspace(desc))
+    return dx, dw
+
+
+# Token counts behind a border of the rule that makes shares of dW_r longer than 512 tokens, for one
+# and for several groups of experts, and batches of many shares.
+LONG_SHAPES = [(BF16, 4099, 8192, 60), (BF16, 4095, 8192, 60), (BF16, 4099, 4096, 130),
+               (BF16, 16500, 4096, 20), (BF16, 8191, 8192, 7), (BF16, 65521, 2048, 60),
+               (BF16, 33001, 2048, 250), (F32, 2600, 2048, 250), (F32, 4201, 4096, 33),
+               (F32, 8203, 2048, 60), (F32, 16399, 1024, 9), (F32, 33001, 512, 16)]
+
+
+@pytest.mark.parametrize("dtype,T,d,Ne", GATE_SHAPES + LONG_SHAPES,
+                         ids=[f"{'bf16' if s[0] == BF16 else 'f32'}-{s[1]}-{s[2]}-{s[3]}"
+                              for s in GATE_SHAPES + LONG_SHAPES])
+def test_gate_backward_of_whole_numbers_is_exact(dtype, T, d, Ne):
+    """dlogits of at most 9 bits and x of -1, 0, 1: sums below 2^24 (T x 257 <= 65521 x 257 =
+    16838897 > 2^24 only if every token counted with the largest; their mean is under a half of
+    it), so dW_r is exact in every order, and dx is the exact sum rounded once."""
+    g = gen(T + 3 * Ne)
+    dl = whole(g, [-257.0, -255.0, -3.0, 0.0, 1.0, 129.0, 257.0], T, Ne)
+    x, w = whole(g, [-1.0, 0.0, 1.0], T, d).to(dtype), whole(g, [-2.0, -1.0, 0.0, 1.0, 3.0], Ne, d).to(dtype)
+    dx_in = whole(g, [-100.0, 0.0, 7.0], T, d).to(dtype)
+    dx, dw = run_gate(dl, x, w, dx_in, dtype)
+    big = dl.double()
+    assert float((big.abs().t().contiguous() @ x.double().abs()).max()) < 2 ** 24
+    assert torch.equal(dw.double(), big.t().contiguous() @ x.double())
+    assert torch.equal(dx, (big @ w.double() + dx_in.double()).to(dtype))
+
+
+@pytest.mark.parametrize("dtype,T,d,Ne", [s for s in GATE_SHAPES if s[1] <= 250],
+                         ids=[f"{'bf16' if s[0] == BF16 else 'f32'}-{s[1]}-{s[2]}-{s[3]}"
+                              for s in GATE_SHAPES if s[1] <= 250])
+def test_gate_weight_gradient_keeps_all_bits_of_dlogits(dtype, T, d, Ne):
+    """dlogits of 17 bits (2^16 + 2^8 + 1) at most: 250 of them stay below 2^24."""
+    g = gen(T + 5 * Ne)
+    dl = whole(g, [-65793.0, -65537.0, -1.0, 257.0, 65793.0], T, Ne)
+    x, w = whole(g, [-1.0, 0.0, 1.0], T, d).to(dtype), whole(g, [-1.0, 1.0], Ne, d).to(dtype)
+    _, dw = run_gate(dl, x, w, None, dtype)
+    assert torch.equal(dw.double(), dl.double().t().contiguous() @ x.double())
+
+
+@pytest.mark.parametrize("dtype,T,d,Ne", [(BF16, 1100003, 2048, 60), (BF16, 1100003, 2048, 100),
+                                          (F32, 530003, 4096, 70)])
+def test_gate_backward_of_whole_numbers_in_arrays_of_more_than_2_to_the_31(dtype, T, d, Ne):
+    """Every token counts: dlogits up to 3, x up to 2, sums of at most 6 T < 2^24."""
+    g = gen(Ne)
+    dl = whole(g, [-3.0, -1.0, 0.0, 2.0, 3.0], T, Ne)
+    x = torch.empty(T, d, dtype=dtype, device="cuda")
+    for part in x.split(1 << 16):
+        part.copy_(whole(g, [-2.0, -1.0, 0.0, 1.0, 2.0], *part.shape))
+    w = whole(g, [-2.0, -1.0, 1.0, 2.0], Ne, d).to(dtype)
+    dx, dw = run_gate(dl, x, w, None, dtype)
+    want = torch.zeros(Ne, d, dtype=torch.float64, device="cuda")
+    wd = w.double()
+    for t in range(0, T, 1 << 16):
+        part = dl[t:t + (1 << 16)].double()
+        want += part.t().contiguous() @ x[t:t + (1 << 16)].double()
+        assert torch.equal(dx[t:t + (1 << 16)], (part @ wd).to(dtype)), t
+    assert torch.equal(dw.double(), want)
