@@ -5,9 +5,9 @@ import pytest
 import torch
 
 from expert_token_routing_amd import occ
-from test_gpu_block import (BF16, F32, FORMS, GATE_SHAPES, SCALE, adam_desc, adam_inputs, check_norm,
-                            check_norm_back, gen, layer, moments, nan_like, norm_inputs, run_norm,
-                            run_norm_back)
+from test_gpu_block import (BF16, F32, FORMS, GATE_SHAPES, LAST, SCALE, adam_desc, adam_inputs,
+                            behind_zeros, check_norm, check_norm_back, gen, layer, moments, nan_like,
+                            norm_inputs, only_last, run_norm, run_norm_back)
 
 pytestmark = pytest.mark.gpu
 
@@ -89,6 +89,20 @@ def test_norm_backward_of_rows_near_the_smallest_normal_number(dtype, T, d, form
     out = run_norm_back(t, grads, kept, opt, dtype)
     assert all(v.isfinite().all() for v in out.values() if v is not None)
     check_norm_back(t, grads, kept, opt, out)
+
+
+# Forward workgroups that walk on to another row (a launch holds 2^22 of them): the last rows lie
+# on both sides of that border, for rows of a wave's lanes and of several waves.
+@pytest.mark.parametrize("dtype,T,d", [(F32, (1 << 26) + 409, 16), (BF16, (1 << 23) + 409, 1024)])
+@pytest.mark.parametrize("form", ["sandwich", "first", "last"])
+def test_norm_rows_behind_the_last_workgroup(dtype, T, d, form):
+    t, _, opt = norm_inputs(dtype, LAST, d, form, seed=d)
+    full = {key: behind_zeros(T, v) if v is not None and v.dim() == 2 else v for key, v in t.items()}
+    r = full["x"] if full["y"] is not None else None  # in place
+    h = None if full["w_pre"] is None else full["x"] if r is None else full["y"]
+    occ.occ_block_norm(layer(T, d, dtype=dtype), opt, full["x"], full["y"], full["w_post"],
+                       full["gate"], full["w_pre"], r, h)
+    check_norm(t, opt, None if r is None else only_last(r), None if h is None else only_last(h))
 
 
 # ----------------------------------------------------- gate projection, back
