@@ -544,9 +544,10 @@ occ_status occ_balance_backward(const occ_layer_desc *desc, const occ_balance_de
  *   dx = dx_in + dlogits w_router,   dw_router = dlogits^T x
  * Uses T, d, Ne and dtype; sums are fp32.  With bf16 tensors the fp32 dlogits
  * enter the matrix cores as a sum of bf16 terms: two for dx (16 bits, below
- * the rounding of dx), three for dw_router (all 24 bits).  A value that is not
- * finite gives NaN or infinity where it contributes (an x value: in its
- * column of dw_router).
+ * the rounding of dx), three for dw_router (all 24 bits).  Terms are multiples
+ * of 2^-133, so values below 2^-110 keep fewer bits, and values from
+ * 2^128 (1 - 2^-9) on count as infinite.  A value that is not finite gives NaN
+ * or infinity where it contributes (an x value: in its column of dw_router).
  *   dlogits    T x Ne fp32.
  *   x          T x d (dtype); may be NULL without dw_router.
  *   w_router   Ne x d (dtype); may be NULL without dx.
@@ -566,7 +567,10 @@ occ_status occ_gate_backward(const occ_layer_desc *desc, const float *dlogits, c
  * the block's largest magnitude / 448 (the square root halves v's range of
  * exponents).  A v > 0 never rounds to 0 (its code is at least 2^-9), so
  * that a small v cannot leave m / eps; a block whose largest magnitude is
- * below 2^-100 is held as zeros.  Codes and units of zero start a run. */
+ * below 2^-100 is held as zeros.  Otherwise an element takes the code nearest
+ * to its quotient by the unit; that is formed in fp32, so a quotient as near to
+ * the middle of two codes as fp32's rounding may take either.  Codes and units
+ * of zero start a run. */
 #define OCC_ADAMW_BLOCK 256
 typedef enum occ_adamw_state { OCC_ADAMW_32BIT = 0, OCC_ADAMW_8BIT = 1 } occ_adamw_state;
 

@@ -4,10 +4,11 @@ numbers, whose sums are exact in every order, over one, several and very long sh
 import pytest
 import torch
 
+import block_reference as ref
 from expert_token_routing_amd import occ
-from test_gpu_block import (BF16, F32, FORMS, GATE_SHAPES, LAST, SCALE, adam_desc, adam_inputs,
-                            behind_zeros, check_norm, check_norm_back, gen, layer, moments, nan_like,
-                            norm_inputs, only_last, run_norm, run_norm_back)
+from test_gpu_block import (BF16, F32, FORMS, GATE_SHAPES, LAST, SCALE, U, adam_desc, adam_inputs,
+                            behind_zeros, check, check_norm, check_norm_back, gen, layer, moments,
+                            nan_like, norm_inputs, only_last, run_norm, run_norm_back)
 
 pytestmark = pytest.mark.gpu
 
@@ -157,6 +158,35 @@ def test_gate_weight_gradient_keeps_all_bits_of_dlogits(dtype, T, d, Ne):
     x, w = whole(g, [-1.0, 0.0, 1.0], T, d).to(dtype), whole(g, [-1.0, 1.0], Ne, d).to(dtype)
     _, dw = run_gate(dl, x, w, None, dtype)
     assert torch.equal(dw.double(), dl.double().t().contiguous() @ x.double())
+
+
+@pytest.mark.parametrize("Ne", [7, 60, 130])
+def test_gate_backward_of_the_smallest_and_largest_dlogits(Ne):
+    """bf16 terms are multiples of 2^-133, so that each of the smallest dlogits is off by half of
+    that at most, times x or w; the largest ones are exact below 2^128 (1 - 2^-9)."""
+    T, d, g = 150, 192, gen(Ne)
+    dl = torch.ldexp(1 + torch.rand(T, Ne, generator=g, device="cuda"),
+                     torch.randint(-126, -100, (T, Ne), generator=g, device="cuda").float())
+    x, w = (2.0 ** 40 * whole(g, [-2.0, -1.0, 1.0, 3.0], n, d).to(BF16) for n in (T, Ne))
+    dx, dw = run_gate(dl, x, w, None, BF16)
+    want_dx, mdx, want_dw, mdw = ref.gate_back(dl, x, w, None)
+    check(dx, want_dx, mdx + 2.0 ** -134 * w.double().abs().sum(0) / (264 * U), 264 + Ne, "dx")
+    check(dw, want_dw, mdw + 2.0 ** -134 * x.double().abs().sum(0) / (64 * U), 64 + T, "dw")
+    top = 2.0 ** 128 * (1 - 2.0 ** -9)
+    dl = torch.zeros(T, Ne, device="cuda")
+    at, e = torch.arange(0, T, 9, device="cuda"), torch.arange(0, T, 9, device="cuda") % Ne
+    dl[at, e] = top * (1 - 2.0 ** -24)  # the value below
+    x, w = (2.0 ** -60 * whole(g, [-2.0, -1.0, 1.0], n, d).to(BF16) for n in (T, Ne))
+    dx, dw = run_gate(dl, x, w, None, BF16)
+    want_dx, mdx, want_dw, mdw = ref.gate_back(dl, x, w, None)
+    check(dx, want_dx, mdx, 264 + Ne, "dx")
+    check(dw, want_dw, mdw, 64 + T, "dw")
+    dl[at[1], e[1]] = top
+    dx, dw = run_gate(dl, x, w, None, BF16)
+    rows = torch.ones(T, dtype=torch.bool, device="cuda")
+    rows[at[1]] = False
+    assert not dx[at[1]].isfinite().any() and not dw[e[1]].isfinite().any()
+    check(dx[rows], want_dx[rows], mdx[rows], 264 + Ne, "dx")
 
 
 @pytest.mark.parametrize("dtype,T,d,Ne", [(BF16, 1100003, 2048, 60), (BF16, 1100003, 2048, 100),
