@@ -34,11 +34,14 @@
 // start, its waits and its last workgroups lie under the other's work
 // (k_gate_bwd, k_gate_bwd_f32).  Against a launch for each: T = 256, d = 2048,
 // 64 experts 10.4 us against 14.6 (bf16), 11.7 against 17.2 (fp32); T = 8192
-// 31 against 39, 60 against 65; T = 32768 90 against 96, 202 against 201; 250
+// 30 against 39, 60 against 65; T = 32768 90 against 96, 202 against 201; 250
 // experts in bf16 T = 1024 19 against 28, T = 32768 218 against 209.
-// Measured at d = 2048 bf16: Ne = 60, T = 65536 164 us + 5 for the shares
-// (4.9 TB/s of 822 MB, with one bf16 term in place of three as long: the
-// memory bounds it); Ne = 64, T = 8192 27 + 4.7 us (3.3 TB/s of 104 MB).
+// Measured at d = 2048 bf16: Ne = 60, T = 65536 166 us + 5.4 for the shares
+// (4.8 TB/s of 822 MB, with one bf16 term in place of three as long: the
+// memory bounds it); Ne = 64, T = 8192 24.3 + 4.1 us (3.6 TB/s of 104 MB).
+// Above 64 experts the groups of dW_r each load and transpose x again: T = 8192,
+// Ne = 65 36 + 4.7 us, 130 56 + 4.8, 250 62 + 4.9 (83 to 105 MB read from HBM
+// against 85 at 64: the repeated work bounds them, not HBM).
 #include <algorithm>
 #include <type_traits>
 

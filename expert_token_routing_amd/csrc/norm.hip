@@ -21,21 +21,22 @@
 // a team of several waves adds its sums through LDS, and a row of up to 32
 // chunks takes 16 or 32 lanes of a wave (T = 65536, d = 128 forward 12 us, 24
 // with a wave to a row; backward 26 against 50).  At d = 2048 in bf16
-// (256 chunks), T = 65536 forward: 188 us with 128 threads a row, 211 with
-// 256, 200 with 64 (one wave, no barrier).
+// (256 chunks), T = 65536 forward, compared when loads and stores stood under
+// conditions: 188 us with 128 threads a row (186 now), 211 with 256, 200 with
+// 64 (one wave, no barrier).
 // The forward gives each row to a team of its own.  In the backward each
 // thread also keeps fp32 sums of its columns' weight gradients, so its teams
 // walk over rows with a fixed stride, the next row's loads issued before this
 // one's sums; a workgroup's sums go to the workspace once and a second kernel
 // adds the workgroups' in order, so results do not depend on timing.
 // Workgroups of 1024 threads, one per CU, leave the fewest such sums: 299 us
-// at T = 65536, d = 2048 against 313 with two of 256 threads.
+// at T = 65536, d = 2048 (297 now) against 313 with two of 256 threads.
 // A workgroup's row takes 1.6 us (1.2 of them the vector units'), 2.6 with
 // loads and stores under conditions, IEEE roots and divisions and values
 // rounded one by one.
-// Measured at d = 2048 bf16, all parts present: forward T = 65536 184 us
-// (5.8 TB/s of the bytes it cannot do without), one token 2.3; backward
-// T = 65536 299 us (5.4 TB/s), T = 8192 40.0 + 4.6 us (4.5 TB/s).
+// Measured at d = 2048 bf16, all parts present: forward T = 65536 186 us
+// (5.8 TB/s of the bytes it cannot do without), one token 2.2; backward
+// T = 65536 297 + 4.6 us (5.3 TB/s), T = 8192 39.6 + 4.7 us (4.5 TB/s).
 // Stores past the caches measure 3% faster alone and slower by 2 to 5% with
 // the kernel that reads their rows, so they are ordinary.
 #include <algorithm>
