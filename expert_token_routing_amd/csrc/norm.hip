@@ -8,9 +8,9 @@
 // backward needs three sums before dr' = dr + (gradient through h) is known
 // (r.r, (dh w_pre).r, y.y) and one after it ((dr' g w_post).n(y)), which is also
 // a token gate's gradient.  (With v rstd^3 mean(q v) behind rstd q a cube leaves
-// fp32 where rows and eps are small, and the gradient does not.)  The gradients of w_post and of a channel gate come
-// from one column sum, S = sum over rows of s g_token dr' n(y): gate S and
-// w_post S.
+// fp32 where rows and eps are small, and the gradient does not.)  The gradients
+// of w_post and of a channel gate come from one column sum, S = sum over rows of
+// s g_token dr' n(y): gate S and w_post S.
 //
 // Memory bound: the forward reads x and y and writes r and h once, the
 // backward reads dr, dh, r and y and writes dx and dy once.  A row stays in
