@@ -337,7 +337,8 @@ size_t block_ws_bytes(const occ_layer_desc &D) {
     const size_t d = D.d, bf16 = D.dtype == OCC_BF16;
     return align_up(std::max<size_t>(
         {norm_back_blocks(D.T, row_chunks(D)) * 2 * d * 4, balance_part_bytes(D.T, D.Ne),
-         static_cast<size_t>(gate_dw_shares(D.T, D.d, D.Ne, bf16)) * D.Ne * d * 4}));
+         static_cast<size_t>(gate_dw_shares(D.T, D.d, D.Ne, bf16)) * D.Ne * d * 4,
+         bias_part_bytes(D.T, D.Ne, D.k)}));
 }
 
 occ_status check_norm(const occ_layer_desc *desc, const occ_norm_desc *opt) {
@@ -366,6 +367,73 @@ occ_status balance_tab(const occ_layer_desc &D, const occ_balance_desc *opt, con
     int32_t order[kMaxNe];
     for (int e = 0; e < D.Ne; e++) order[e] = e;
     return make_tab(D, order, tab);
+}
+
+// The options of routing by scores, for this layer.
+occ_status check_score(const occ_layer_desc *desc, const occ_score_desc *opt) {
+    OCC_TRY(check_desc(desc));
+    if (!opt || desc->prune_rule != OCC_PRUNE_OFF || !std::isfinite(opt->scale) ||
+        opt->score < OCC_SCORE_SOFTMAX || opt->score > OCC_SCORE_SIGMOID ||
+        (opt->renormalise != 0 && opt->renormalise != 1))
+        return OCC_ERR_INVALID_ARG;
+    const int n = desc->Ne / desc->Nd;
+    if (opt->top_groups < 1 || opt->top_groups > desc->Nd ||
+        static_cast<int64_t>(opt->top_groups) * n < desc->k)
+        return OCC_ERR_INVALID_ARG;
+    if (opt->group_best < 1 || opt->group_best > 2 ||
+        (opt->top_groups < desc->Nd && opt->group_best > n))
+        return OCC_ERR_INVALID_ARG;
+    return OCC_OK;
+}
+
+// The 8-bit layer's buffers: the BRIM at the places that the layer's own
+// layout gives it, then the codes, scales and terms.
+struct Int8Layout {
+    Layout brim;
+    size_t epd_tok, xq, xs, h, hq, hs, y_epd, y_sh, total;
+};
+
+Int8Layout int8_layout(const occ_layer_desc &D) {
+    const size_t T = D.T, d = D.d, F = D.F, nepd = T * D.k, Fs = D.n_shared > 0 ? D.F_shared : 0;
+    Int8Layout L{};
+    L.brim = layout(D);
+    size_t o = L.brim.brim_end;
+    auto take = [&o](size_t bytes) {
+        const size_t r = o;
+        o = align_up(o + std::max<size_t>(bytes, 1));
+        return r;
+    };
+    L.epd_tok = take(nepd * 4);
+    L.xq = take(T * round_line(d));
+    L.xs = take(T * 4);
+    // the shared experts' hidden states go through the routed ones' buffers first
+    L.h = take(std::max(nepd * F, T * Fs) * 4);
+    L.hq = take(std::max(nepd * round_line(F), T * round_line(Fs)));
+    L.hs = take(nepd * 4);
+    L.y_epd = take(nepd * d * 2);
+    L.y_sh = take(D.n_shared * T * d * 2);
+    L.total = o;
+    return L;
+}
+
+occ_status check_int8(const occ_layer_desc *desc) {
+    OCC_TRY(check_desc(desc));
+    // K products of codes up to 127 stay below 2^31 up to K = 133144
+    constexpr int kMaxWidth = 131072;
+    if (desc->dtype != OCC_BF16 || (desc->flags & OCC_FLAG_TRAIN) || desc->F > kMaxWidth ||
+        (desc->n_shared > 0 && desc->F_shared > kMaxWidth))
+        return OCC_ERR_UNSUPPORTED;
+    return OCC_OK;
+}
+
+bool experts_given(const occ_int8_experts *e) {
+    return e && e->gate && e->up && e->down && e->gate_scale && e->up_scale && e->down_scale &&
+           rows_aligned(e->gate, e->up, e->down) && aligned_to(e->gate_scale, 4) &&
+           aligned_to(e->up_scale, 4) && aligned_to(e->down_scale, 4);
+}
+
+bool apart_from(const void *out, const occ_int8_experts *e) {
+    return !e || apart(out, e->gate, e->up, e->down, e->gate_scale, e->up_scale, e->down_scale);
 }
 
 }  // namespace
@@ -1195,6 +1263,198 @@ occ_status occ_moe_backward(const occ_layer_desc *desc, const void *dy, const vo
         OCC_HIP(launch_route_backward(logits, at<int32_t>(workspace, L.ids), bb.tok_epd, dw_part,
                                       L.dw_stride, L.dw_stride, D.T, D.Ne, D.k, dw, dlogits, s));
     OCC_TRY(mark(8));
+    return OCC_OK;
+}
+
+occ_status occ_route_scored(const occ_layer_desc *desc, const occ_score_desc *opt,
+                            const float *logits, const float *bias, const int32_t *placement_host,
+                            int32_t *ids, float *w, void *stream) {
+    OCC_TRY(check_score(desc, opt));
+    if (!logits || !ids || !w || !aligned_to(logits, 4) || !aligned_to(bias, 4) ||
+        !aligned_to(ids, 4) || !aligned_to(w, 4) || !apart(ids, logits, bias, w) ||
+        !apart(w, logits, bias))
+        return OCC_ERR_INVALID_ARG;
+    ScoreArgs a{};
+    if (placement_host) {
+        OCC_TRY(make_tab(*desc, placement_host, &a.tab));
+    } else {
+        if (opt->top_groups < desc->Nd) return OCC_ERR_INVALID_ARG;
+        a.tab.Nd = desc->Nd;
+        a.tab.n = desc->Ne / desc->Nd;
+    }
+    a.logits = logits;
+    a.bias = bias;
+    a.T = desc->T;
+    a.Ne = desc->Ne;
+    a.k = desc->k;
+    a.sigmoid = opt->score == OCC_SCORE_SIGMOID;
+    a.top_groups = opt->top_groups;
+    a.group_best = opt->group_best;
+    a.renormalise = opt->renormalise;
+    a.scale = opt->scale;
+    a.ids = ids;
+    a.w = w;
+    OCC_HIP(launch_route_scored(a, static_cast<hipStream_t>(stream)));
+    return OCC_OK;
+}
+
+occ_status occ_route_scored_backward(const occ_layer_desc *desc, const occ_score_desc *opt,
+                                     const float *logits, const int32_t *ids, const float *dw,
+                                     const float *dlogits_in, float *dlogits, void *stream) {
+    OCC_TRY(check_score(desc, opt));
+    if (!logits || !ids || !dw || !dlogits || !aligned_to(logits, 4) || !aligned_to(ids, 4) ||
+        !aligned_to(dw, 4) || !aligned_to(dlogits_in, 4) || !aligned_to(dlogits, 4) ||
+        !apart(dlogits, ids, dw))
+        return OCC_ERR_INVALID_ARG;
+    OCC_HIP(launch_route_scored_back(logits, ids, dw, dlogits_in, desc->T, desc->Ne, desc->k,
+                                     opt->score == OCC_SCORE_SIGMOID, opt->renormalise, opt->scale,
+                                     dlogits, static_cast<hipStream_t>(stream)));
+    return OCC_OK;
+}
+
+occ_status occ_route_bias_step(const occ_layer_desc *desc, float rate, const int32_t *ids,
+                               const uint8_t *valid, const float *bias_in, int32_t *counts,
+                               float *bias, void *workspace, size_t ws_bytes, void *stream) {
+    OCC_TRY(check_desc(desc));
+    if (!ids || !bias_in || !counts || !bias || !std::isfinite(rate) || !aligned_to(ids, 4) ||
+        !aligned_to(bias_in, 4) || !aligned_to(counts, 4) || !aligned_to(bias, 4) ||
+        !apart(counts, ids, valid, bias_in, bias) || !apart(bias, ids, valid) ||
+        !apart(workspace, ids, valid, bias_in, counts, bias))
+        return OCC_ERR_INVALID_ARG;
+    OCC_TRY(check_ws(*desc, workspace, ws_bytes, block_ws_bytes(*desc)));
+    OCC_HIP(launch_bias_step(ids, valid, desc->T, desc->k, desc->Ne, bias_in, rate, counts, bias,
+                             static_cast<int32_t *>(workspace), static_cast<hipStream_t>(stream)));
+    return OCC_OK;
+}
+
+occ_status occ_quantize_int8(int64_t rows, int32_t cols, int32_t dtype, const void *x, int8_t *q,
+                             float *scale, void *stream) {
+    if (rows < 1 || cols < 1 || (dtype != OCC_F32 && dtype != OCC_BF16) || !x || !q || !scale ||
+        !rows_aligned(x, q) || !aligned_to(scale, 4) || !apart(q, x, scale) || !apart(scale, x))
+        return OCC_ERR_INVALID_ARG;
+    if (cols % 16 || rows >= (1ll << 31)) return OCC_ERR_UNSUPPORTED;
+    OCC_HIP(launch_quantize_rows(x, dtype == OCC_BF16, static_cast<size_t>(rows), cols, q,
+                                 static_cast<size_t>(cols), scale, nullptr, 0, nullptr,
+                                 static_cast<hipStream_t>(stream)));
+    return OCC_OK;
+}
+
+occ_status occ_int8_workspace_size(const occ_layer_desc *desc, size_t *bytes_host) {
+    OCC_TRY(check_int8(desc));
+    if (!bytes_host) return OCC_ERR_INVALID_ARG;
+    *bytes_host = int8_layout(*desc).total;
+    return OCC_OK;
+}
+
+occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const int32_t *ids_in,
+                                const float *w_in, const int32_t *placement_host,
+                                const occ_int8_experts *experts_host,
+                                const occ_int8_experts *shared_host, void *y, void *workspace,
+                                size_t ws_bytes, void *stream) {
+    OCC_TRY(check_int8(desc));
+    const occ_layer_desc &D = *desc;
+    if (!x || !ids_in || !w_in || !y || !experts_given(experts_host) || !rows_aligned(x, y) ||
+        !aligned_to(ids_in, 4) || !aligned_to(w_in, 4) ||
+        (D.n_shared > 0 ? !experts_given(shared_host) : shared_host != nullptr) ||
+        !apart(y, x, ids_in, w_in) || !apart_from(y, experts_host) ||
+        !apart_from(y, shared_host) || !apart(workspace, x, ids_in, w_in, y) ||
+        !apart_from(workspace, experts_host) || !apart_from(workspace, shared_host))
+        return OCC_ERR_INVALID_ARG;
+    PlaceTab tab;
+    OCC_TRY(make_tab(D, placement_host, &tab));
+    const Int8Layout L = int8_layout(D);
+    OCC_TRY(check_ws(D, workspace, ws_bytes, L.total));
+
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const BrimBufs bb = brim_bufs(workspace, L.brim);
+    int32_t *ids = at<int32_t>(workspace, L.brim.ids);
+    float *w = at<float>(workspace, L.brim.w);
+    int32_t *epd_tok = at<int32_t>(workspace, L.epd_tok);
+    int8_t *xq = at<int8_t>(workspace, L.xq), *hq = at<int8_t>(workspace, L.hq);
+    float *xs = at<float>(workspace, L.xs), *hs = at<float>(workspace, L.hs);
+    float *h = at<float>(workspace, L.h);
+    uint16_t *y_epd = at<uint16_t>(workspace, L.y_epd), *y_sh = at<uint16_t>(workspace, L.y_sh);
+    const size_t T = D.T, d = D.d, nepd = T * D.k;
+    // the tile heights and their rule are the bf16 products'
+    const bool small = tile_rows(D) == kGemmBmBf16Small;
+    const auto gemm_up = small ? launch_gemm_up8_m128 : launch_gemm_up8;
+    const auto gemm_down = small ? launch_gemm_down8_m128 : launch_gemm_down8;
+    const size_t routed_tiles = (nepd + tile_rows(D) - 1) / tile_rows(D) + D.Ne + kBrimMaxFill;
+
+    OCC_HIP(launch_sanitize_ids(ids_in, w_in, D.T, D.k, D.Ne, ids, w, s));
+    OCC_HIP(launch_brim(ids, w, D.T, D.k, tab, tile_rows(D), fill_cols(D), 0, bb, s));
+    // the tokens' codes, and the token of each EPD row, so that a token's row
+    // is kept once and gathered by each of its experts
+    OCC_HIP(launch_quantize_rows(x, 1, T, D.d, xq, round_line(d), xs, bb.tok_epd, D.k, epd_tok, s));
+    for (int sx = 0; sx < D.n_shared; sx++) {
+        const size_t Fs = D.F_shared, wo = sx * Fs * d;
+        Up8Args up{};
+        up.A = xq;
+        up.a_scale = xs;
+        up.Wg = shared_host->gate + wo;
+        up.Wu = shared_host->up + wo;
+        up.sg = shared_host->gate_scale + sx * Fs;
+        up.su = shared_host->up_scale + sx * Fs;
+        up.out = h;
+        up.M = D.T;
+        up.K = D.d;
+        up.N = D.F_shared;
+        up.Ne = 1;
+        up.lda = static_cast<int>(round_line(d));
+        up.tab = tab;
+        OCC_HIP(gemm_up(up, 0, s));
+        OCC_HIP(launch_quantize_rows(h, 0, T, D.F_shared, hq, round_line(Fs), hs, nullptr, 0, nullptr, s));
+        Down8Args dn{};
+        dn.A = hq;
+        dn.a_scale = hs;
+        dn.W = shared_host->down + wo;
+        dn.sd = shared_host->down_scale + sx * d;
+        dn.out = y_sh + sx * T * d;
+        dn.M = D.T;
+        dn.K = D.F_shared;
+        dn.N = D.d;
+        dn.Ne = 1;
+        dn.lda = static_cast<int>(round_line(Fs));
+        dn.tab = tab;
+        OCC_HIP(gemm_down(dn, 0, s));
+    }
+    Up8Args up{};
+    up.A = xq;
+    up.a_rows = epd_tok;
+    up.a_scale = xs;
+    up.Wg = experts_host->gate;
+    up.Wu = experts_host->up;
+    up.sg = experts_host->gate_scale;
+    up.su = experts_host->up_scale;
+    up.seg_off = bb.epd_off;
+    up.tile_off = bb.tile_off;
+    up.row_w = bb.epd_w;
+    up.out = h;
+    up.M = D.T * D.k;
+    up.K = D.d;
+    up.N = D.F;
+    up.Ne = D.Ne;
+    up.lda = static_cast<int>(round_line(d));
+    up.tab = tab;
+    OCC_HIP(gemm_up(up, routed_tiles, s));
+    OCC_HIP(launch_quantize_rows(h, 0, nepd, D.F, hq, round_line(D.F), hs, nullptr, 0, nullptr, s));
+    Down8Args dn{};
+    dn.A = hq;
+    dn.a_scale = hs;
+    dn.W = experts_host->down;
+    dn.sd = experts_host->down_scale;
+    dn.seg_off = bb.epd_off;
+    dn.tile_off = bb.tile_off;
+    dn.out = y_epd;
+    dn.M = D.T * D.k;
+    dn.K = D.F;
+    dn.N = D.d;
+    dn.Ne = D.Ne;
+    dn.lda = static_cast<int>(round_line(D.F));
+    dn.tab = tab;
+    OCC_HIP(gemm_down(dn, routed_tiles, s));
+    OCC_HIP(launch_combine_rows(y_epd, bb.tok_epd, y_sh, D.n_shared, D.T, D.k, D.d,
+                                static_cast<uint16_t *>(y), s));
     return OCC_OK;
 }
 

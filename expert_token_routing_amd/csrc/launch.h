@@ -139,6 +139,72 @@ hipError_t launch_gemm_down_bf16_dense(const DownArgs &a, size_t max_m_tiles, hi
 hipError_t launch_gemm_up_f32(const UpArgs &a, size_t max_m_tiles, hipStream_t s);
 hipError_t launch_gemm_down_f32(const DownArgs &a, size_t max_m_tiles, hipStream_t s);
 
+// --- the layer with experts in 8-bit integers ---
+// Rows of K codes lie round_line(K) bytes apart, zeros behind K.
+inline size_t round_line(size_t k) { return (k + 127) / 128 * 128; }
+// (int8.hip) Rows of x (bf16 or fp32) as codes and a scale each: scale = a / 127,
+// code = rint(v * (127 / a)), a the row's largest magnitude; a row with a below
+// kInt8Tiny is held as zeros, one that is not finite gets a scale of NaN.  Rows
+// of q lie ldq bytes apart, with zeros in cols .. ldq (multiples of 16).  With
+// tok_epd also epd_tok[tok_epd[t k + j]] = t for every row t.
+constexpr float kInt8Tiny = 0x1p-100f;
+hipError_t launch_quantize_rows(const void *x, int bf16, size_t rows, int cols, int8_t *q,
+                                size_t ldq, float *scale, const int32_t *tok_epd, int k,
+                                int32_t *epd_tok, hipStream_t s);
+// y[t] = bf16( sum over j of y_epd[tok_epd[t k + j]] + sum over s of y_sh[s T + t] ), bf16
+// rows of d, fp32 sums in that order.
+hipError_t launch_combine_rows(const uint16_t *y_epd, const int32_t *tok_epd, const uint16_t *y_sh,
+                               int n_shared, int T, int k, int d, uint16_t *y, hipStream_t s);
+// (gemm_int8.hip) h[r, f] = w_r silu(g) u in fp32, g = (xs_r sg[e][f]) (xq_r . Wg[e][f]), row
+// r's codes and xs at a_rows[r] (or r); segments and tiles as in UpArgs.  lda in bytes.
+struct Up8Args {
+    const int8_t *A;
+    const int32_t *a_rows;
+    const float *a_scale;
+    const int8_t *Wg, *Wu;
+    const float *sg, *su;
+    const int32_t *seg_off, *tile_off;
+    const float *row_w;
+    float *out;
+    int M, K, N, Ne, lda;
+    PlaceTab tab;
+    int m_tiles;
+};
+// out[r, c] = bf16( (hs_r sd[e][c]) (hq_r . Wd[e][c]) ).
+struct Down8Args {
+    const int8_t *A;
+    const float *a_scale;
+    const int8_t *W;
+    const float *sd;
+    const int32_t *seg_off, *tile_off;
+    uint16_t *out;
+    int M, K, N, Ne, lda;
+    PlaceTab tab;
+    int m_tiles;
+};
+hipError_t launch_gemm_up8(const Up8Args &a, size_t max_m_tiles, hipStream_t s);
+hipError_t launch_gemm_down8(const Down8Args &a, size_t max_m_tiles, hipStream_t s);
+hipError_t launch_gemm_up8_m128(const Up8Args &a, size_t max_m_tiles, hipStream_t s);
+hipError_t launch_gemm_down8_m128(const Down8Args &a, size_t max_m_tiles, hipStream_t s);
+
+// --- routing by scores (score.hip) ---
+struct ScoreArgs {
+    const float *logits, *bias;  // bias may be NULL
+    int T, Ne, k, sigmoid, top_groups, group_best, renormalise;
+    float scale;
+    PlaceTab tab;
+    int32_t *ids;
+    float *w;
+};
+hipError_t launch_route_scored(const ScoreArgs &a, hipStream_t s);
+hipError_t launch_route_scored_back(const float *logits, const int32_t *ids, const float *dw,
+                                    const float *dlogits_in, int T, int Ne, int k, int sigmoid,
+                                    int renormalise, float scale, float *dlogits, hipStream_t s);
+size_t bias_part_bytes(int T, int Ne, int k);
+hipError_t launch_bias_step(const int32_t *ids, const uint8_t *valid, int T, int k, int Ne,
+                            const float *bias_in, float rate, int32_t *counts, float *bias,
+                            int32_t *part, hipStream_t s);
+
 // --- backward grouped GEMMs, bf16 MFMA (gemm_bwd.hip) ---
 // Input-gradient GEMM over row tiles of up to kBwdRowTile rows (tile_off over the segments
 // seg_off of placement positions; first_cnt and phase select rows as in

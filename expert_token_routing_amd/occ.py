@@ -28,6 +28,7 @@ OCC_FLAG_DETERMINISTIC = 2
 OCC_NOALLOC_SCRATCH_BYTES = 128 << 20
 OCC_GATE_NONE, OCC_GATE_CHANNEL, OCC_GATE_TOKEN = 0, 1, 2
 OCC_ADAMW_32BIT, OCC_ADAMW_8BIT = 0, 1
+OCC_SCORE_SOFTMAX, OCC_SCORE_SIGMOID = 0, 1
 OCC_ADAMW_BLOCK = 256
 BSTAGES = ["dispatch", "dgrad_down", "dgrad_up", "shared", "combine", "wgrad_down", "wgrad_up",
            "route"]
@@ -43,7 +44,9 @@ EXPORTED = ["occ_status_string", "occ_workspace_size", "occ_route",
             "occ_coactivation_stats", "occ_place_experts", "occ_events_create",
             "occ_events_destroy", "occ_event_elapsed_ms", "occ_moe_forward_noalloc",
             "occ_block_workspace_size", "occ_block_norm", "occ_block_norm_backward",
-            "occ_balance_loss", "occ_balance_backward", "occ_gate_backward", "occ_adamw_step"]
+            "occ_balance_loss", "occ_balance_backward", "occ_gate_backward", "occ_adamw_step",
+            "occ_route_scored", "occ_route_scored_backward", "occ_route_bias_step",
+            "occ_quantize_int8", "occ_int8_workspace_size", "occ_moe_forward_int8"]
 
 
 class OccError(RuntimeError):
@@ -87,6 +90,16 @@ class AdamwDesc(ctypes.Structure):
                 [(n, ctypes.c_double) for n in
                  ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] +
                 [("step", ctypes.c_int64)])
+
+
+class ScoreDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("score", "top_groups", "group_best",
+                                               "renormalise")] + [("scale", ctypes.c_float)])
+
+
+class Int8Pointers(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "up", "down", "gate_scale", "up_scale",
+                                               "down_scale")]
 
 
 class AdamwTensor(ctypes.Structure):
@@ -140,6 +153,14 @@ def lib() -> ctypes.CDLL:
                                      [ctypes.c_float, vp, vp, vp], ctypes.c_int),
             "occ_gate_backward": ([dp] + [vp] * 7 + [sz, vp], ctypes.c_int),
             "occ_adamw_step": ([ctypes.POINTER(AdamwDesc), vp, i32, vp, vp], ctypes.c_int),
+            "occ_route_scored": ([dp, ctypes.POINTER(ScoreDesc)] + [vp] * 6, ctypes.c_int),
+            "occ_route_scored_backward": ([dp, ctypes.POINTER(ScoreDesc)] + [vp] * 6,
+                                          ctypes.c_int),
+            "occ_route_bias_step": ([dp, ctypes.c_float] + [vp] * 6 + [sz, vp], ctypes.c_int),
+            "occ_quantize_int8": ([ctypes.c_int64, i32, i32] + [vp] * 4, ctypes.c_int),
+            "occ_int8_workspace_size": ([dp, ctypes.POINTER(sz)], ctypes.c_int),
+            "occ_moe_forward_int8": ([dp] + [vp] * 4 + [ctypes.POINTER(Int8Pointers)] * 2 +
+                                     [vp, vp, sz, vp], ctypes.c_int),
             "occ_events_create": ([i32, vp], ctypes.c_int),
             "occ_events_destroy": ([i32, vp], ctypes.c_int),
             "occ_event_elapsed_ms": ([vp, vp, ctypes.POINTER(ctypes.c_float)], ctypes.c_int),
@@ -605,6 +626,114 @@ def occ_adamw_step(opt: AdamwDesc, tensors: AdamwTensors, dynamic=None, stream=N
         return
     _queue("occ_adamw_step", lib().occ_adamw_step, tensors.index, stream, opt, tensors.table,
            len(tensors.tensors), _addr(dynamic, "dynamic", torch.float32, (3,), tensors.index))
+
+
+# ---- routing by scores ----
+
+def occ_route_scored(desc: LayerDesc, opt: ScoreDesc, logits, bias, placement, ids, w,
+                     stream=None):
+    """The k experts of the best scores (softmax or sigmoid, plus a bias for the choice) in the
+    best groups, and their weights; bias may be None, placement too when all groups are used."""
+    T, Ne, f32, i = desc.T, desc.Ne, torch.float32, _device(logits)
+    place = _place(desc, placement)
+    _queue("occ_route_scored", lib().occ_route_scored, i, stream, desc, opt,
+           _addr(logits, "logits", f32, (T, Ne), i), _addr(bias, "bias", f32, (Ne,), i), place,
+           _addr(ids, "ids", torch.int32, (T, desc.k), i), _addr(w, "w", f32, (T, desc.k), i))
+
+
+def occ_route_scored_backward(desc: LayerDesc, opt: ScoreDesc, logits, ids, dw, dlogits_in,
+                              dlogits, stream=None):
+    """dlogits = dlogits_in + the gradient of occ_route_scored's weights in the logits."""
+    T, Ne, f32, i = desc.T, desc.Ne, torch.float32, _device(logits)
+    _queue("occ_route_scored_backward", lib().occ_route_scored_backward, i, stream, desc, opt,
+           _addr(logits, "logits", f32, (T, Ne), i),
+           _addr(ids, "ids", torch.int32, (T, desc.k), i), _addr(dw, "dw", f32, (T, desc.k), i),
+           _addr(dlogits_in, "dlogits_in", f32, (T, Ne), i),
+           _addr(dlogits, "dlogits", f32, (T, Ne), i))
+
+
+def occ_route_bias_step(desc: LayerDesc, rate: float, ids, valid, bias_in, counts, bias,
+                        workspace, stream=None):
+    """bias = bias_in + rate sign(mean load - load), with the counts (Ne, then the valid
+    tokens); bias may be bias_in."""
+    Ne, f32, i32, i = desc.Ne, torch.float32, torch.int32, _device(ids)
+    _queue("occ_route_bias_step", lib().occ_route_bias_step, i, stream, desc, rate,
+           _addr(ids, "ids", i32, (desc.T, desc.k), i), _mask(valid, desc.T, i),
+           _addr(bias_in, "bias_in", f32, (Ne,), i), _addr(counts, "counts", i32, (Ne + 1,), i),
+           _addr(bias, "bias", f32, (Ne,), i), *_ws(workspace, i))
+
+
+# ---- experts in 8-bit integers ----
+
+_OCC = {torch.float32: OCC_F32, torch.bfloat16: OCC_BF16}
+
+
+def occ_quantize_int8(x, q, scale, stream=None):
+    """Rows of x (its last dimension; bf16 or fp32) as int8 codes q and a scale each."""
+    i = _device(x)
+    if x.dim() < 1 or x.dtype not in _OCC:
+        raise ValueError("x must be rows of torch.float32 or torch.bfloat16")
+    cols = x.shape[-1]
+    _queue("occ_quantize_int8", lib().occ_quantize_int8, i, stream,
+           x.numel() // cols if cols else 0, cols, _OCC[x.dtype],
+           _addr(x, "x", x.dtype, x.shape, i), _addr(q, "q", torch.int8, x.shape, i),
+           _addr(scale, "scale", torch.float32, x.shape[:-1], i))
+
+
+class Int8Experts:
+    """The weights of experts in 8 bits, laid out once: device tensors gate and up (N x F x d
+    int8), down (N x d x F int8), gate_scale and up_scale (N x F fp32), down_scale (N x d fp32),
+    as occ_quantize_int8 makes them of bf16 weights.  Keeps the tensors alive."""
+
+    def __init__(self, gate, up, down, gate_scale, up_scale, down_scale):
+        self.index, self.shape = _device(gate), tuple(gate.shape)
+        if len(self.shape) != 3:
+            raise ValueError(f"gate must be N x F x d, got {self.shape}")
+        N, F, d = self.shape
+        self.tensors = (gate, up, down, gate_scale, up_scale, down_scale)
+        i8, f32 = torch.int8, torch.float32
+        wants = (("gate", i8, (N, F, d)), ("up", i8, (N, F, d)), ("down", i8, (N, d, F)),
+                 ("gate_scale", f32, (N, F)), ("up_scale", f32, (N, F)),
+                 ("down_scale", f32, (N, d)))
+        for t, (name, _, _) in zip(self.tensors, wants):
+            if t is None:
+                raise ValueError(f"{name} must be given")
+        self.table = Int8Pointers(*[_addr(t, name, dtype, shape, self.index)
+                                    for t, (name, dtype, shape) in zip(self.tensors, wants)])
+
+
+def _int8_table(group, name: str, shape: tuple, index: int):
+    if group is None:
+        return None
+    if group.shape != shape or group.index != index:
+        raise ValueError(f"{name} are {group.shape} on cuda:{group.index}, expected {shape} on "
+                         f"cuda:{index}")
+    return group.table
+
+
+def occ_int8_workspace_size(desc: LayerDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().occ_int8_workspace_size(ctypes.byref(desc), ctypes.byref(n)),
+           "occ_int8_workspace_size")
+    return n.value
+
+
+def alloc_int8_workspace(desc: LayerDesc, device="cuda") -> torch.Tensor:
+    """A device byte tensor of occ_int8_workspace_size bytes."""
+    return torch.empty(occ_int8_workspace_size(desc), dtype=torch.uint8, device=device)
+
+
+def occ_moe_forward_int8(desc: LayerDesc, x, ids, w, placement, experts: Int8Experts,
+                         shared: Int8Experts | None, y, workspace, stream=None):
+    """The layer on a given routing with experts in 8 bits (x and y bf16)."""
+    T, d, k, i = desc.T, desc.d, desc.k, _device(x)
+    bf16, place = torch.bfloat16, _place(desc, placement)
+    _queue("occ_moe_forward_int8", lib().occ_moe_forward_int8, i, stream, desc,
+           _addr(x, "x", bf16, (T, d), i), _addr(ids, "ids", torch.int32, (T, k), i),
+           _addr(w, "w", torch.float32, (T, k), i), place,
+           _int8_table(experts, "experts", (desc.Ne, desc.F, d), i),
+           _int8_table(shared, "shared experts", (desc.n_shared, desc.F_shared, d), i),
+           _addr(y, "y", bf16, (T, d), i), *_ws(workspace, i))
 
 
 def occ_forward_views(desc: LayerDesc, workspace) -> ForwardView:

@@ -620,6 +620,132 @@ typedef struct occ_adamw_tensor {
 occ_status occ_adamw_step(const occ_adamw_desc *opt, const occ_adamw_tensor *tensors_host,
                           int32_t count, const float *dynamic, void *stream);
 
+/* ---- routing by scores ----
+ *
+ * A router whose choice and weights come from scores, in place of occ_route's:
+ * its ids and weights go to occ_moe_forward_routed or occ_moe_forward_int8,
+ * and the dw of occ_moe_backward comes back through
+ * occ_route_scored_backward.  Arrays are aligned to their elements, outputs
+ * overlap nothing but where said (INVALID_ARG otherwise, as far as arrays that
+ * start alike); prune_rule must be OFF.  Results repeat bitwise. */
+
+typedef enum occ_score { OCC_SCORE_SOFTMAX = 0, OCC_SCORE_SIGMOID = 1 } occ_score;
+
+typedef struct occ_score_desc {
+    int32_t score;       /* occ_score: softmax over the Ne logits, or 1 / (1 + exp(-logit)) */
+    int32_t top_groups;  /* groups of the placement that a token may use, Nd for all;
+                            top_groups * Ne / Nd >= k */
+    int32_t group_best;  /* a group's score is that of its best expert (1) or the sum of its
+                            best two's (2, with at least two experts in a group) */
+    int32_t renormalise; /* 1: the token's k weights sum to `scale`; 0: they are scores times
+                            `scale` */
+    float scale;         /* finite */
+} occ_score_desc;
+
+/* With s the token's scores and c = s + bias:
+ *   the top_groups groups of the best score are kept (ties to the lower group),
+ *   ids = the k experts of the largest c in them, largest first, ties to the
+ *         lower index (without a bias, of the largest logit),
+ *   w   = scale * s / (renormalise ? sum of the k scores : 1).
+ * The bias moves the choice alone.  Scores, choice and weights are formed in
+ * 64 bits and the weights rounded once.
+ * Uses T, Ne, k and Nd.
+ *   logits     T x Ne fp32.  -inf or NaN leaves an expert out: its score is 0
+ *              and it comes behind every other one (the ids stay distinct); a
+ *              group is scored by the experts that are not left out.  A token
+ *              whose chosen scores sum to 0 has weights of 0.
+ *   bias       Ne fp32, or NULL.
+ *   placement_host  as for occ_route; may be NULL when top_groups is Nd.
+ *   ids (out)  T x k int32.   w (out)  T x k fp32. */
+occ_status occ_route_scored(const occ_layer_desc *desc, const occ_score_desc *opt,
+                            const float *logits, const float *bias, const int32_t *placement_host,
+                            int32_t *ids, float *w, void *stream);
+
+/* Its gradient in the logits, the choice held fixed, added to what is there:
+ * from dw (T x k fp32, the gradient of w), with r_j = s_j / sum of the k scores,
+ *   sigmoid, renormalised:  dl_j = scale r_j (1 - s_j) (dw_j - sum_i dw_i r_i)
+ *   sigmoid, not:           dl_j = scale s_j (1 - s_j) dw_j
+ *   softmax, renormalised:  dl_j = scale r_j (dw_j - sum_i dw_i r_i)
+ *   softmax, not:           dl_e = scale s_e ([e chosen] dw_e - sum_i dw_i s_i)
+ * and 0 for every other expert, in fp32.  An expert that was left out gets 0,
+ * and its dw is not used.
+ *   ids         as written by occ_route_scored (one outside 0..Ne-1 counts
+ *               nothing, one that repeats counts again).
+ *   dlogits_in  T x Ne fp32, or NULL for zero.
+ *   dlogits (out)  T x Ne fp32; may be dlogits_in or logits. */
+occ_status occ_route_scored_backward(const occ_layer_desc *desc, const occ_score_desc *opt,
+                                     const float *logits, const int32_t *ids, const float *dw,
+                                     const float *dlogits_in, float *dlogits, void *stream);
+
+/* The step that evens the experts' load by the bias, with the counts:
+ *   counts[e] = slots routed to e,  counts[Ne] = n, the valid tokens
+ *   bias[e] = bias_in[e] + rate * sign(mean of the Ne counts - counts[e])
+ * (no step where they are equal).  Uses T, Ne and k.
+ *   rate     finite.
+ *   ids      T x k int32 (an id outside 0..Ne-1 is not counted).
+ *   valid    T bytes, 0 for padding, or NULL: every token counts.
+ *   bias_in  Ne fp32.   counts (out)  Ne + 1 int32.
+ *   bias (out)  Ne fp32; may be bias_in.
+ *   workspace   256-byte aligned, ws_bytes >= occ_block_workspace_size. */
+occ_status occ_route_bias_step(const occ_layer_desc *desc, float rate, const int32_t *ids,
+                               const uint8_t *valid, const float *bias_in, int32_t *counts,
+                               float *bias, void *workspace, size_t ws_bytes, void *stream);
+
+/* ---- experts in 8-bit integers ----
+ *
+ * The layer for serving with weights of one byte: products of 8-bit integers,
+ * summed exactly in 32 bits, with an fp32 scale for each token and each output
+ * channel.  Weights are quantised once, rows of activations in each call. */
+
+/* Rows as 8-bit integers with a scale each: with a the row's largest magnitude,
+ *   scale = a / 127,  q = round(x * (127 / a))   (fp32, ties to even)
+ * so that an element stands for q * scale.  A row with a < 2^-100 is held as
+ * zeros with a scale of 0; one with a value that is not finite as zeros with a
+ * scale of NaN, which makes what is computed from it NaN.
+ *   x       rows x cols (dtype), 16-byte aligned; cols a multiple of 16
+ *           (UNSUPPORTED otherwise).  For the layer's weights a row is an
+ *           output channel (Ne * F rows of d, Ne * d rows of F).
+ *   q (out) rows x cols int8, 16-byte aligned.   scale (out)  rows fp32. */
+occ_status occ_quantize_int8(int64_t rows, int32_t cols, int32_t dtype, const void *x, int8_t *q,
+                             float *scale, void *stream);
+
+/* Experts in 8 bits: N experts (Ne routed ones, or n_shared shared ones) of
+ * width F (or F_shared).  Device pointers, the weights 16-byte aligned. */
+typedef struct occ_int8_experts {
+    const int8_t *gate, *up;              /* N x F x d */
+    const int8_t *down;                   /* N x d x F */
+    const float *gate_scale, *up_scale;   /* N x F */
+    const float *down_scale;              /* N x d */
+} occ_int8_experts;
+
+/* Bytes of device workspace occ_moe_forward_int8 needs for this shape. */
+occ_status occ_int8_workspace_size(const occ_layer_desc *desc, size_t *bytes_host);
+
+/* The layer from a routing computed elsewhere (occ_route_scored, occ_route),
+ * with Q the quantiser of rows above and D what its codes stand for:
+ *   x' = D(Q(x_t)) per token,   h = w silu(W_gate x') (W_up x') per slot (t, e, w),
+ *   y_t = sum over the token's slots of W_down D(Q(h))  (+ shared experts, w = 1)
+ * with the weights' own codes and scales.  h is fp32 until it is quantised; the
+ * token's terms are each rounded to bf16 and summed in fp32, in the order of
+ * its ids and then the shared experts', and y is rounded once.  Results repeat
+ * bitwise whatever the flags say.  The placement orders the experts' rows
+ * (Algorithm 5) and changes no result.
+ * Needs the dtype bf16, no OCC_FLAG_TRAIN, F and F_shared <= 131072
+ * (UNSUPPORTED otherwise); desc->prune_rule is not used.
+ *   x        T x d bf16, 16-byte aligned.
+ *   ids, w   as for occ_moe_forward_routed.
+ *   experts_host, shared_host   read by the time the call returns; shared_host
+ *            is NULL when n_shared = 0.
+ *   y (out)  T x d bf16, 16-byte aligned, none of the other arrays.
+ *   workspace  256-byte aligned, ws_bytes >= occ_int8_workspace_size; scratch:
+ *            nothing is kept in it between calls, but calls that may overlap
+ *            need one each. */
+occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const int32_t *ids,
+                                const float *w, const int32_t *placement_host,
+                                const occ_int8_experts *experts_host,
+                                const occ_int8_experts *shared_host, void *y, void *workspace,
+                                size_t ws_bytes, void *stream);
+
 /* Device addresses of the intermediates occ_moe_forward leaves in a
  * workspace (pure host arithmetic, nothing queued). */
 occ_status occ_forward_views(const occ_layer_desc *desc, void *workspace,
