@@ -653,7 +653,7 @@ typedef struct occ_score_desc {
  *   logits     T x Ne fp32.  -inf or NaN leaves an expert out: its score is 0
  *              and it comes behind every other one (the ids stay distinct); a
  *              group is scored by the experts that are not left out.  A token
- *              whose chosen scores sum to 0 has weights of 0.
+ *              whose chosen experts are all left out has weights of 0.
  *   bias       Ne fp32, or NULL.
  *   placement_host  as for occ_route; may be NULL when top_groups is Nd.
  *   ids (out)  T x k int32.   w (out)  T x k fp32. */

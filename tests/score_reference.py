@@ -33,6 +33,21 @@ def scores(logits, kind):
     return torch.where(total > 0, e / torch.where(total > 0, total, torch.ones_like(total)), e)
 
 
+def shares(logits, ids, kind):
+    """s / (sum of the chosen s) of the chosen, from the scores' logarithms (a softmax's but for a
+    term that cancels), which do not vanish; 0 where all of them are left out."""
+    v = logits.gather(1, ids.long())
+    dead = left_out(v)
+    v = torch.where(dead, torch.zeros_like(v), v).double()
+    if kind == SIGMOID:
+        v = v.clamp(max=0) - torch.log1p(torch.exp(-v.abs()))
+    v = torch.where(dead, torch.full_like(v, -math.inf), v)
+    top = v.amax(1, keepdim=True)
+    e = torch.exp(v - torch.where(top == -math.inf, torch.zeros_like(top), top))
+    total = e.sum(1, keepdim=True)
+    return torch.where(total > 0, e / torch.where(total > 0, total, torch.ones_like(total)), e)
+
+
 def route(logits, bias, placement, k, kind, top_groups, group_best, renormalise, scale):
     """ids (T x k) and w in 64 bits."""
     T, Ne = logits.shape
@@ -55,8 +70,7 @@ def route(logits, bias, placement, k, kind, top_groups, group_best, renormalise,
         for j, (_, e) in enumerate(pick):
             ids[t, j], w[t, j] = e, s[t, e]
     if renormalise:
-        total = w.sum(1, keepdim=True)
-        w = torch.where(total > 0, w / torch.where(total > 0, total, torch.ones_like(total)), w)
+        w = shares(logits, ids, kind)
     return ids, scale * w
 
 
@@ -75,10 +89,10 @@ def route_back(logits, ids, dw, kind, renormalise, scale):
         size = torch.zeros_like(grad).scatter_add_(1, at, g.abs())
         sub, subm = (g * sj).sum(1, keepdim=True), (g * sj).abs().sum(1, keepdim=True)
         return scale * s * (chosen - sub), abs(scale) * s * (size + subm)
-    total = sj.sum(1, keepdim=True)
     r = sj
-    if renormalise:
-        r = torch.where(total > 0, sj / torch.where(total > 0, total, torch.ones_like(total)), sj)
+    if renormalise:  # of those that count: others read as left out
+        r = shares(torch.where(good, logits.gather(1, at), torch.full_like(logits[:1, :1], -math.inf)),
+                   torch.arange(ids.shape[1]).expand_as(ids), kind)
     rest = 1.0
     if kind == SIGMOID:  # 1 - s without its cancellation
         x = torch.where(good, logits.gather(1, at), torch.zeros_like(sj, dtype=logits.dtype)).double()
