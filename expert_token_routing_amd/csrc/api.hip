@@ -386,12 +386,23 @@ occ_status check_score(const occ_layer_desc *desc, const occ_score_desc *opt) {
     return OCC_OK;
 }
 
+#ifndef OCC_FEW_SLOTS
+#define OCC_FEW_SLOTS 32
+#endif
+constexpr int kFewTokenSlots = OCC_FEW_SLOTS;
+
 // The 8-bit layer's buffers: the BRIM at the places that the layer's own
 // layout gives it, then the codes, scales and terms.
 struct Int8Layout {
     Layout brim;
     size_t epd_tok, xq, xs, h, hq, hs, y_epd, y_sh, total;
 };
+
+// Whether the layer runs without sorting its slots (int8_few.hip).
+bool few_tokens(const occ_layer_desc &D) {
+    return static_cast<int64_t>(D.T) * D.k <= kFewTokenSlots &&
+           few_fits(D.d, D.k, D.F, D.n_shared, D.F_shared);
+}
 
 Int8Layout int8_layout(const occ_layer_desc &D) {
     const size_t T = D.T, d = D.d, F = D.F, nepd = T * D.k, Fs = D.n_shared > 0 ? D.F_shared : 0;
@@ -407,7 +418,8 @@ Int8Layout int8_layout(const occ_layer_desc &D) {
     L.xq = take(T * round_line(d));
     L.xs = take(T * 4);
     // the shared experts' hidden states go through the routed ones' buffers first
-    L.h = take(std::max(nepd * F, T * Fs) * 4);
+    // (few tokens keep both)
+    L.h = take(few_tokens(D) ? (nepd * F + T * D.n_shared * Fs) * 4 : std::max(nepd * F, T * Fs) * 4);
     L.hq = take(std::max(nepd * round_line(F), T * round_line(Fs)));
     L.hs = take(nepd * 4);
     L.y_epd = take(nepd * d * 2);
@@ -1375,6 +1387,30 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
     float *h = at<float>(workspace, L.h);
     uint16_t *y_epd = at<uint16_t>(workspace, L.y_epd), *y_sh = at<uint16_t>(workspace, L.y_sh);
     const size_t T = D.T, d = D.d, nepd = T * D.k;
+    if (few_tokens(D)) {
+        const auto weights = [](const occ_int8_experts *e) {
+            return e ? Int8Weights{e->gate, e->up, e->down, e->gate_scale, e->up_scale, e->down_scale}
+                     : Int8Weights{};
+        };
+        FewArgs f{};
+        f.x = static_cast<const uint16_t *>(x);
+        f.ids = ids_in;
+        f.w = w_in;
+        f.routed = weights(experts_host);
+        f.shared = weights(shared_host);
+        f.h = h;
+        f.h_sh = h + nepd * D.F;
+        f.y = static_cast<uint16_t *>(y);
+        f.T = D.T;
+        f.d = D.d;
+        f.Ne = D.Ne;
+        f.k = D.k;
+        f.F = D.F;
+        f.n_shared = D.n_shared;
+        f.F_shared = D.n_shared > 0 ? D.F_shared : 0;
+        OCC_HIP(launch_few(f, s));
+        return OCC_OK;
+    }
     // the tile heights and their rule are the bf16 products'
     const bool small = tile_rows(D) == kGemmBmBf16Small;
     const auto gemm_up = small ? launch_gemm_up8_m128 : launch_gemm_up8;

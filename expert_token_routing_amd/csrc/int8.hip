@@ -3,65 +3,20 @@
 // bound by memory.
 #include <algorithm>
 
-#include "launch.h"
+#include "int8_rows.h"
 
 namespace occ {
 namespace {
 
 constexpr int kQuantThreads = 256;
 constexpr size_t kMaxGrid = 1 << 22;  // workgroups; larger problems loop
-typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
-
-// A 16-byte chunk of a row as floats: 8 bf16 or 4 fp32.
 template <bool BF16>
-struct Chunk {
-    static constexpr int N = BF16 ? 8 : 4;
-    float v[N];
-    __device__ __forceinline__ void from(u32x4 raw) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            if constexpr (BF16) {
-                v[2 * i] = __uint_as_float(raw[i] << 16);
-                v[2 * i + 1] = __uint_as_float(raw[i] & 0xffff0000u);
-            } else {
-                v[i] = __uint_as_float(raw[i]);
-            }
-        }
-    }
-    // The largest magnitude's bits: as whole numbers in the order of the
-    // magnitudes, infinity and NaN above all others.
-    __device__ __forceinline__ uint32_t top() const {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < N; i++) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-        return m;
-    }
-};
-
-__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, float inv) {
-    const auto code = [inv](float x) {
-        return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(x * inv), -127.f), 127.f))) & 0xffu;
-    };
-    return code(a) | code(b) << 8 | code(c) << 16 | code(d) << 24;
-}
-
-// The row's factor of its values and what a code stands for, from its largest
-// magnitude's bits.  Not finite: codes of zero and a scale of NaN.
-__device__ __forceinline__ void row_scale(uint32_t bits, float &inv, float &scale) {
-    const float a = __uint_as_float(bits);
-    const bool bad = bits >= 0x7f800000u, held = !bad && a >= kInt8Tiny;
-    inv = held ? 127.f / a : 0.f;
-    scale = bad ? __uint_as_float(0x7fc00000u) : held ? a / 127.f : 0.f;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store_codes(const Chunk<BF16> &x, bool bad, float inv, int8_t *q) {
-    uint32_t c[Chunk<BF16>::N / 4];
-#pragma unroll
-    for (int i = 0; i < Chunk<BF16>::N / 4; i++)
-        c[i] = bad ? 0u : code4(x.v[4 * i], x.v[4 * i + 1], x.v[4 * i + 2], x.v[4 * i + 3], inv);
-    if constexpr (BF16) *reinterpret_cast<u32x2 *>(q) = u32x2{c[0], c[1]};
-    else *reinterpret_cast<uint32_t *>(q) = c[0];
+__device__ __forceinline__ void store_codes(const Chunk<BF16> &x, const RowScale &r, int8_t *q) {
+    if constexpr (BF16)
+        *reinterpret_cast<u32x2 *>(q) = u32x2{r.code4(x.v[0], x.v[1], x.v[2], x.v[3]),
+                                              r.code4(x.v[4], x.v[5], x.v[6], x.v[7])};
+    else
+        *reinterpret_cast<uint32_t *>(q) = r.code4(x.v[0], x.v[1], x.v[2], x.v[3]);
 }
 
 // One wave a row of at most 64 NV chunks, held in registers between the
@@ -92,8 +47,7 @@ __global__ __launch_bounds__(kQuantThreads) void k_quantize_rows(
                 m = max(m, v[0].top());
             }
         }
-        // (the bits of a magnitude have no sign: signed order is theirs)
-        m = static_cast<uint32_t>(group_reduce<kWave>(static_cast<int>(m), [](int a, int b) { return max(a, b); }));
+        m = wave_top(m);
         if constexpr (NV == 0) {
             __shared__ uint32_t part[kQuantThreads / kWave];
             __syncthreads();  // the last row's maxima have been read
@@ -102,25 +56,23 @@ __global__ __launch_bounds__(kQuantThreads) void k_quantize_rows(
 #pragma unroll
             for (int j = 0; j < kQuantThreads / kWave; j++) m = max(m, part[j]);
         }
-        float inv, sc;
-        row_scale(m, inv, sc);
-        const bool bad = m >= 0x7f800000u;
-        if (i == 0) scale[row] = sc;
+        const RowScale r(m);
+        if (i == 0) scale[row] = r.scale;
         int8_t *dst = q + row * ldq;
         if constexpr (NV != 0) {
 #pragma unroll
             for (int j = 0; j < NV; j++) {
                 const int c = i + kWave * j;
-                if (c < chunks) store_codes(v[j], bad, inv, dst + static_cast<size_t>(c) * per);
+                if (c < chunks) store_codes(v[j], r, dst + static_cast<size_t>(c) * per);
             }
         } else {
             for (int c = i; c < chunks; c += kTeam) {
                 v[0].from(src[c]);
-                store_codes(v[0], bad, inv, dst + static_cast<size_t>(c) * per);
+                store_codes(v[0], r, dst + static_cast<size_t>(c) * per);
             }
         }
-        for (int c = chunks + i; c < static_cast<int>(ldq / per); c += kTeam)
-            store_codes(v[0], true, 0.f, dst + static_cast<size_t>(c) * per);
+        for (size_t c = static_cast<size_t>(chunks) * per + 4 * i; c < ldq; c += 4 * kTeam)
+            *reinterpret_cast<uint32_t *>(dst + c) = 0u;
     }
 }
 

@@ -187,6 +187,26 @@ hipError_t launch_gemm_down8(const Down8Args &a, size_t max_m_tiles, hipStream_t
 hipError_t launch_gemm_up8_m128(const Up8Args &a, size_t max_m_tiles, hipStream_t s);
 hipError_t launch_gemm_down8_m128(const Down8Args &a, size_t max_m_tiles, hipStream_t s);
 
+// (int8_few.hip) The whole layer for few tokens: x, y T x d bf16, ids and w as
+// the caller gave them; h (T k x F) and h_sh (T n_shared x F_shared) are
+// scratch.  Shapes that few_fits refuses take the general path.
+constexpr int kFewMaxD = 8192, kFewMaxShared = 16;
+struct Int8Weights {
+    const int8_t *gate, *up, *down;
+    const float *gate_scale, *up_scale, *down_scale;
+};
+struct FewArgs {
+    const uint16_t *x;
+    const int32_t *ids;
+    const float *w;
+    Int8Weights routed, shared;
+    float *h, *h_sh;
+    uint16_t *y;
+    int T, d, Ne, k, F, n_shared, F_shared;
+};
+bool few_fits(int d, int k, int F, int n_shared, int F_shared);
+hipError_t launch_few(const FewArgs &a, hipStream_t s);
+
 // --- routing by scores (score.hip) ---
 struct ScoreArgs {
     const float *logits, *bias;  // bias may be NULL

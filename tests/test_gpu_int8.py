@@ -154,7 +154,12 @@ LAYERS = [(1, 64, 1, 1, 64, 1, 0, 0), (1, 256, 8, 8, 128, 8, 0, 0), (1, 192, 16,
           (300, 192, 8, 2, 192, 4, 1, 320), (700, 128, 4, 2, 256, 2, 0, 0),
           (401, 320, 3, 3, 448, 3, 2, 64), (1000, 64, 4, 4, 64, 2, 0, 0), (33, 64, 2, 1, 2112, 1, 0, 0),
           (450, 64, 2, 2, 2112, 2, 1, 2176), (9, 4160, 3, 1, 64, 3, 0, 0), (70, 8192, 2, 1, 64, 1, 0, 0),
-          (650, 512, 60, 4, 192, 4, 1, 256), (257, 128, 256, 2, 64, 64, 0, 0)]
+          (650, 512, 60, 4, 192, 4, 1, 256), (257, 128, 256, 2, 64, 64, 0, 0),
+          # few tokens: many slots, the widest rows, hidden rows longer than what a wave asks for
+          # at once, shared experts alone long, widths that no workgroup's share divides
+          (1, 64, 40, 32, 64, 2, 0, 0), (1, 8192, 3, 2, 64, 1, 1, 64), (4, 1088, 4, 2, 1088, 2, 0, 0),
+          (2, 128, 3, 3, 4160, 1, 0, 0), (3, 2048, 2, 1, 64, 1, 2, 5632), (2, 1024, 8, 8, 1024, 8, 1, 2112),
+          (1, 2112, 2, 1, 20480, 1, 0, 0), (1, 64, 2, 2, 40960, 1, 0, 0)]
 
 
 @pytest.mark.parametrize("T,d,Ne,k,F,Nd,n_shared,F_shared", LAYERS)
@@ -188,6 +193,28 @@ def test_layer_routing_of_any_values(T, Ne):
     case.w[3] = torch.tensor([0.0, -1.5, 0.0])
     y = case.check()
     assert not y[0].any()
+
+
+@pytest.mark.parametrize("T,Ne,k", [(1, 70, 20), (1, 256, 32), (40, 70, 20), (64, 256, 32)])
+def test_layer_routing_of_many_slots_with_bad_ids(T, Ne, k):
+    g = torch.Generator().manual_seed(k)
+    ids = torch.randint(-3, Ne + 3, (T, k), generator=g)
+    ids[0] = torch.arange(k) + Ne - k // 2  # the second half out of range
+    Case(T, 64, Ne, k, 64, seed=11, ids=ids).check()
+
+
+@pytest.mark.parametrize("d,F,F_shared", [(192, 320, 64), (2048, 1024, 1408)])
+def test_layer_of_a_token_does_not_depend_on_its_batch(d, F, F_shared):
+    """A token alone, with a few others and in batches of either tile height: the same bits."""
+    case = Case(520, d, 8, 3, F, Nd=2, n_shared=1, F_shared=F_shared, seed=12)
+    whole = case.run()
+    ex, sh = on_gpu(case.experts), on_gpu(case.shared)
+    for first, T in ((0, 1), (7, 1), (20, 3), (40, 10), (50, 11), (100, 100), (519, 1)):
+        desc = layer(T, d, 8, 3, F, 2, 1, F_shared)
+        x, ids, w = (a[first:first + T].contiguous().cuda() for a in (case.x, case.ids, case.w))
+        y = torch.empty(T, d, dtype=BF16, device="cuda")
+        occ.occ_moe_forward_int8(desc, x, ids, w, case.place, ex, sh, y, occ.alloc_int8_workspace(desc))
+        assert torch.equal(y.cpu(), whole[first:first + T]), (first, T)
 
 
 @pytest.mark.parametrize("T,Ne", [(7, 8), (300, 4)])
