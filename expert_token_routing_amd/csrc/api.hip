@@ -391,11 +391,9 @@ occ_status check_score(const occ_layer_desc *desc, const occ_score_desc *opt) {
 #endif
 constexpr int kFewTokenSlots = OCC_FEW_SLOTS;
 
-// The 8-bit layer's buffers: the BRIM at the places that the layer's own
-// layout gives it, then the codes, scales and terms.
+// The 8-bit layer's buffers: the sorted slots, then codes, scales and terms.
 struct Int8Layout {
-    Layout brim;
-    size_t epd_tok, xq, xs, h, hq, hs, y_epd, y_sh, total;
+    size_t tok_epd, epd_tok, epd_w, epd_off, tile_off, counts, xq, xs, h, hq, hs, y_epd, y_sh, total;
 };
 
 // Whether the layer runs without sorting its slots (int8_few.hip).
@@ -407,14 +405,18 @@ bool few_tokens(const occ_layer_desc &D) {
 Int8Layout int8_layout(const occ_layer_desc &D) {
     const size_t T = D.T, d = D.d, F = D.F, nepd = T * D.k, Fs = D.n_shared > 0 ? D.F_shared : 0;
     Int8Layout L{};
-    L.brim = layout(D);
-    size_t o = L.brim.brim_end;
+    size_t o = 0;
     auto take = [&o](size_t bytes) {
         const size_t r = o;
         o = align_up(o + std::max<size_t>(bytes, 1));
         return r;
     };
+    L.tok_epd = take(nepd * 4);
     L.epd_tok = take(nepd * 4);
+    L.epd_w = take(nepd * 4);
+    L.epd_off = take((D.Ne + 1) * 4);
+    L.tile_off = take((D.Ne + 1) * 4);
+    L.counts = take(static_cast<size_t>(kSlotsMaxShares) * D.Ne * 4);
     L.xq = take(T * round_line(d));
     L.xs = take(T * 4);
     // the shared experts' hidden states go through the routed ones' buffers first
@@ -1346,8 +1348,7 @@ occ_status occ_quantize_int8(int64_t rows, int32_t cols, int32_t dtype, const vo
         return OCC_ERR_INVALID_ARG;
     if (cols % 16 || rows >= (1ll << 31)) return OCC_ERR_UNSUPPORTED;
     OCC_HIP(launch_quantize_rows(x, dtype == OCC_BF16, static_cast<size_t>(rows), cols, q,
-                                 static_cast<size_t>(cols), scale, nullptr, 0, nullptr,
-                                 static_cast<hipStream_t>(stream)));
+                                 static_cast<size_t>(cols), scale, static_cast<hipStream_t>(stream)));
     return OCC_OK;
 }
 
@@ -1378,10 +1379,6 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
     OCC_TRY(check_ws(D, workspace, ws_bytes, L.total));
 
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const BrimBufs bb = brim_bufs(workspace, L.brim);
-    int32_t *ids = at<int32_t>(workspace, L.brim.ids);
-    float *w = at<float>(workspace, L.brim.w);
-    int32_t *epd_tok = at<int32_t>(workspace, L.epd_tok);
     int8_t *xq = at<int8_t>(workspace, L.xq), *hq = at<int8_t>(workspace, L.hq);
     float *xs = at<float>(workspace, L.xs), *hs = at<float>(workspace, L.hs);
     float *h = at<float>(workspace, L.h);
@@ -1417,11 +1414,27 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
     const auto gemm_down = small ? launch_gemm_down8_m128 : launch_gemm_down8;
     const size_t routed_tiles = (nepd + tile_rows(D) - 1) / tile_rows(D) + D.Ne + kBrimMaxFill;
 
-    OCC_HIP(launch_sanitize_ids(ids_in, w_in, D.T, D.k, D.Ne, ids, w, s));
-    OCC_HIP(launch_brim(ids, w, D.T, D.k, tab, tile_rows(D), fill_cols(D), 0, bb, s));
-    // the tokens' codes, and the token of each EPD row, so that a token's row
-    // is kept once and gathered by each of its experts
-    OCC_HIP(launch_quantize_rows(x, 1, T, D.d, xq, round_line(d), xs, bb.tok_epd, D.k, epd_tok, s));
+    // a token's row of codes is kept once and gathered by each of its experts
+    SlotArgs sl{};
+    sl.ids = ids_in;
+    sl.w = w_in;
+    sl.x = static_cast<const u32x4 *>(x);
+    sl.xq = xq;
+    sl.xs = xs;
+    sl.tok_epd = at<int32_t>(workspace, L.tok_epd);
+    sl.epd_tok = at<int32_t>(workspace, L.epd_tok);
+    sl.epd_off = at<int32_t>(workspace, L.epd_off);
+    sl.tile_off = at<int32_t>(workspace, L.tile_off);
+    sl.epd_w = at<float>(workspace, L.epd_w);
+    sl.counts = at<int32_t>(workspace, L.counts);
+    sl.ldx = round_line(d);
+    sl.T = D.T;
+    sl.d = D.d;
+    sl.k = D.k;
+    sl.tile_rows = tile_rows(D);
+    sl.fill_cols = fill_cols(D);
+    sl.tab = tab;
+    OCC_HIP(launch_slots(sl, s));
     for (int sx = 0; sx < D.n_shared; sx++) {
         const size_t Fs = D.F_shared, wo = sx * Fs * d;
         Up8Args up{};
@@ -1439,7 +1452,7 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
         up.lda = static_cast<int>(round_line(d));
         up.tab = tab;
         OCC_HIP(gemm_up(up, 0, s));
-        OCC_HIP(launch_quantize_rows(h, 0, T, D.F_shared, hq, round_line(Fs), hs, nullptr, 0, nullptr, s));
+        OCC_HIP(launch_quantize_rows(h, 0, T, D.F_shared, hq, round_line(Fs), hs, s));
         Down8Args dn{};
         dn.A = hq;
         dn.a_scale = hs;
@@ -1456,15 +1469,15 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
     }
     Up8Args up{};
     up.A = xq;
-    up.a_rows = epd_tok;
+    up.a_rows = sl.epd_tok;
     up.a_scale = xs;
     up.Wg = experts_host->gate;
     up.Wu = experts_host->up;
     up.sg = experts_host->gate_scale;
     up.su = experts_host->up_scale;
-    up.seg_off = bb.epd_off;
-    up.tile_off = bb.tile_off;
-    up.row_w = bb.epd_w;
+    up.seg_off = sl.epd_off;
+    up.tile_off = sl.tile_off;
+    up.row_w = sl.epd_w;
     up.out = h;
     up.M = D.T * D.k;
     up.K = D.d;
@@ -1473,14 +1486,14 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
     up.lda = static_cast<int>(round_line(d));
     up.tab = tab;
     OCC_HIP(gemm_up(up, routed_tiles, s));
-    OCC_HIP(launch_quantize_rows(h, 0, nepd, D.F, hq, round_line(D.F), hs, nullptr, 0, nullptr, s));
+    OCC_HIP(launch_quantize_rows(h, 0, nepd, D.F, hq, round_line(D.F), hs, s));
     Down8Args dn{};
     dn.A = hq;
     dn.a_scale = hs;
     dn.W = experts_host->down;
     dn.sd = experts_host->down_scale;
-    dn.seg_off = bb.epd_off;
-    dn.tile_off = bb.tile_off;
+    dn.seg_off = sl.epd_off;
+    dn.tile_off = sl.tile_off;
     dn.out = y_epd;
     dn.M = D.T * D.k;
     dn.K = D.F;
@@ -1489,7 +1502,7 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
     dn.lda = static_cast<int>(round_line(D.F));
     dn.tab = tab;
     OCC_HIP(gemm_down(dn, routed_tiles, s));
-    OCC_HIP(launch_combine_rows(y_epd, bb.tok_epd, y_sh, D.n_shared, D.T, D.k, D.d,
+    OCC_HIP(launch_combine_rows(y_epd, sl.tok_epd, y_sh, D.n_shared, D.T, D.k, D.d,
                                 static_cast<uint16_t *>(y), s));
     return OCC_OK;
 }

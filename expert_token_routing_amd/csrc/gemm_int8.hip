@@ -126,7 +126,7 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
                 const float u = static_cast<float>(acc[mi][ni + NI / 2][v]) * (xs * cu[v]);
                 o[v] = swiglu(g, u) * wr;
             }
-            __builtin_nontemporal_store(o, reinterpret_cast<f32x4 *>(dst + t.n0 + c));
+            *reinterpret_cast<f32x4 *>(dst + t.n0 + c) = o;
         }
     }
 }
@@ -204,8 +204,7 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
             const int col = t.n0 + (c >> 6) * WN + half * 64 + (c & 63);
             if (r >= t.rows || col >= N) continue;
             const u32x4 v = *reinterpret_cast<const u32x4 *>(smem + r * OUT_PITCH + c);
-            __builtin_nontemporal_store(
-                v, reinterpret_cast<u32x4 *>(out + (static_cast<size_t>(t.seg) + t.m0 + r) * N + col));
+            *reinterpret_cast<u32x4 *>(out + (static_cast<size_t>(t.seg) + t.m0 + r) * N + col) = v;
         }
         if (half == 0) __syncthreads();
     }

@@ -10,69 +10,45 @@ namespace {
 
 constexpr int kQuantThreads = 256;
 constexpr size_t kMaxGrid = 1 << 22;  // workgroups; larger problems loop
-template <bool BF16>
-__device__ __forceinline__ void store_codes(const Chunk<BF16> &x, const RowScale &r, int8_t *q) {
-    if constexpr (BF16)
-        *reinterpret_cast<u32x2 *>(q) = u32x2{r.code4(x.v[0], x.v[1], x.v[2], x.v[3]),
-                                              r.code4(x.v[4], x.v[5], x.v[6], x.v[7])};
-    else
-        *reinterpret_cast<uint32_t *>(q) = r.code4(x.v[0], x.v[1], x.v[2], x.v[3]);
-}
-
-// One wave a row of at most 64 NV chunks, held in registers between the
-// maximum and the codes; longer rows (NV = 0) take a workgroup and are read
-// twice, the second time from the caches.
+// One wave a row of at most 64 NV chunks; longer rows (NV = 0) take a workgroup
+// and are read twice, the second time from the caches.
 template <bool BF16, int NV>
-__global__ __launch_bounds__(kQuantThreads) void k_quantize_rows(
-    const u32x4 *__restrict__ x, size_t rows, int chunks, int8_t *__restrict__ q, size_t ldq,
-    float *__restrict__ scale, const int32_t *__restrict__ tok_epd, int k,
-    int32_t *__restrict__ epd_tok) {
-    constexpr int kTeam = NV ? kWave : kQuantThreads, kTeams = kQuantThreads / kTeam, per = Chunk<BF16>::N;
-    const int i = threadIdx.x % kTeam;
-    for (size_t row = static_cast<size_t>(blockIdx.x) * kTeams + threadIdx.x / kTeam; row < rows;
-         row += static_cast<size_t>(gridDim.x) * kTeams) {
-        const u32x4 *src = x + row * chunks;
-        if (tok_epd)
-            for (int j = i; j < k; j += kTeam) epd_tok[tok_epd[row * k + j]] = static_cast<int32_t>(row);
-        Chunk<BF16> v[NV ? NV : 1];
-        uint32_t m = 0;
-        if constexpr (NV != 0) {
-#pragma unroll
-            for (int j = 0; j < NV; j++) v[j].from(src[min(i + kWave * j, chunks - 1)]);
-#pragma unroll
-            for (int j = 0; j < NV; j++) m = max(m, v[j].top());
-        } else {
-            for (int c = i; c < chunks; c += kTeam) {
-                v[0].from(src[c]);
-                m = max(m, v[0].top());
+__global__ __launch_bounds__(kQuantThreads) void k_quantize_rows(const u32x4 *__restrict__ x, size_t rows,
+                                                                 int chunks, int8_t *__restrict__ q,
+                                                                 size_t ldq, float *__restrict__ scale) {
+    if constexpr (NV != 0) {
+        constexpr int kTeams = kQuantThreads / kWave;
+        for (size_t row = static_cast<size_t>(blockIdx.x) * kTeams + threadIdx.x / kWave; row < rows;
+             row += static_cast<size_t>(gridDim.x) * kTeams)
+            quantise_row<BF16, NV>(x + row * chunks, chunks, q + row * ldq, ldq, scale + row);
+    } else {
+        constexpr int per = Chunk<BF16>::N;
+        __shared__ uint32_t part[kQuantThreads / kWave];
+        const int i = threadIdx.x;
+        for (size_t row = blockIdx.x; row < rows; row += gridDim.x) {
+            const u32x4 *src = x + row * chunks;
+            Chunk<BF16> v;
+            uint32_t m = 0;
+            for (int c = i; c < chunks; c += kQuantThreads) {
+                v.from(src[c]);
+                m = max(m, v.top());
             }
-        }
-        m = wave_top(m);
-        if constexpr (NV == 0) {
-            __shared__ uint32_t part[kQuantThreads / kWave];
+            m = wave_top(m);
             __syncthreads();  // the last row's maxima have been read
             if (lane_id() == 0) part[threadIdx.x / kWave] = m;
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < kQuantThreads / kWave; j++) m = max(m, part[j]);
-        }
-        const RowScale r(m);
-        if (i == 0) scale[row] = r.scale;
-        int8_t *dst = q + row * ldq;
-        if constexpr (NV != 0) {
-#pragma unroll
-            for (int j = 0; j < NV; j++) {
-                const int c = i + kWave * j;
-                if (c < chunks) store_codes(v[j], r, dst + static_cast<size_t>(c) * per);
+            const RowScale r(m);
+            if (i == 0) scale[row] = r.scale;
+            int8_t *dst = q + row * ldq;
+            for (int c = i; c < chunks; c += kQuantThreads) {
+                v.from(src[c]);
+                store_codes(v, r, dst + static_cast<size_t>(c) * per);
             }
-        } else {
-            for (int c = i; c < chunks; c += kTeam) {
-                v[0].from(src[c]);
-                store_codes(v[0], r, dst + static_cast<size_t>(c) * per);
-            }
+            for (size_t c = static_cast<size_t>(chunks) * per + 4 * i; c < ldq; c += 4 * kQuantThreads)
+                *reinterpret_cast<uint32_t *>(dst + c) = 0u;
         }
-        for (size_t c = static_cast<size_t>(chunks) * per + 4 * i; c < ldq; c += 4 * kTeam)
-            *reinterpret_cast<uint32_t *>(dst + c) = 0u;
     }
 }
 
@@ -124,17 +100,16 @@ __global__ __launch_bounds__(kCombThreads) void k_combine_rows(
 }  // namespace
 
 hipError_t launch_quantize_rows(const void *x, int bf16, size_t rows, int cols, int8_t *q,
-                                size_t ldq, float *scale, const int32_t *tok_epd, int k,
-                                int32_t *epd_tok, hipStream_t s) {
+                                size_t ldq, float *scale, hipStream_t s) {
     const int chunks = cols / (bf16 ? 8 : 4);
     const u32x4 *xs = static_cast<const u32x4 *>(x);
     const int nv = (chunks + kWave - 1) / kWave;
     const size_t rows_per = nv <= 8 ? kQuantThreads / kWave : 1;
     const unsigned grid = static_cast<unsigned>(std::min<size_t>(ceil_div(rows, rows_per), kMaxGrid));
-#define OCC_QUANT(NV)                                                                          \
-    do {                                                                                       \
-        if (bf16) k_quantize_rows<true, NV><<<grid, kQuantThreads, 0, s>>>(xs, rows, chunks, q, ldq, scale, tok_epd, k, epd_tok);  \
-        else k_quantize_rows<false, NV><<<grid, kQuantThreads, 0, s>>>(xs, rows, chunks, q, ldq, scale, tok_epd, k, epd_tok);      \
+#define OCC_QUANT(NV)                                                                                       \
+    do {                                                                                                    \
+        if (bf16) k_quantize_rows<true, NV><<<grid, kQuantThreads, 0, s>>>(xs, rows, chunks, q, ldq, scale); \
+        else k_quantize_rows<false, NV><<<grid, kQuantThreads, 0, s>>>(xs, rows, chunks, q, ldq, scale);     \
     } while (0)
     if (nv <= 1) OCC_QUANT(1);
     else if (nv <= 2) OCC_QUANT(2);

@@ -61,4 +61,54 @@ __device__ __forceinline__ uint32_t wave_top(uint32_t m) {
 
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 
+// The codes of a chunk at dst (aligned to their number).
+template <bool BF16>
+__device__ __forceinline__ void store_codes(const Chunk<BF16> &x, const RowScale &r, int8_t *dst) {
+    if constexpr (BF16)
+        *reinterpret_cast<u32x2 *>(dst) = u32x2{r.code4(x.v[0], x.v[1], x.v[2], x.v[3]),
+                                                r.code4(x.v[4], x.v[5], x.v[6], x.v[7])};
+    else
+        *reinterpret_cast<uint32_t *>(dst) = r.code4(x.v[0], x.v[1], x.v[2], x.v[3]);
+}
+
+// A row of at most 64 NV chunks by one wave, held in registers between the
+// maximum and the codes where it is at most 8 chunks a lane and read twice
+// otherwise; zeros behind it up to ldq bytes.
+template <bool BF16, int NV>
+__device__ __forceinline__ void quantise_row(const u32x4 *src, int chunks, int8_t *dst, size_t ldq,
+                                             float *scale) {
+    constexpr int per = Chunk<BF16>::N, B = NV < 8 ? NV : 8;
+    const int lane = lane_id();
+    u32x4 raw[B];
+    uint32_t m = 0;
+    Chunk<BF16> x;
+#pragma unroll
+    for (int j0 = 0; j0 < NV; j0 += B) {
+#pragma unroll
+        for (int j = 0; j < B; j++) raw[j] = src[min(lane + kWave * (j0 + j), chunks - 1)];
+#pragma unroll
+        for (int j = 0; j < B; j++) {
+            x.from(raw[j]);
+            m = max(m, x.top());
+        }
+    }
+    const RowScale r(wave_top(m));
+    if (lane == 0) *scale = r.scale;
+#pragma unroll
+    for (int j0 = 0; j0 < NV; j0 += B) {
+        if constexpr (NV > B) {
+#pragma unroll
+            for (int j = 0; j < B; j++) raw[j] = src[min(lane + kWave * (j0 + j), chunks - 1)];
+        }
+#pragma unroll
+        for (int j = 0; j < B; j++) {
+            const int c = lane + kWave * (j0 + j);
+            x.from(raw[j]);
+            if (c < chunks) store_codes(x, r, dst + static_cast<size_t>(c) * per);
+        }
+    }
+    for (size_t c = static_cast<size_t>(chunks) * per + 4 * lane; c < ldq; c += 4 * kWave)
+        *reinterpret_cast<uint32_t *>(dst + c) = 0u;
+}
+
 }  // namespace occ

@@ -145,12 +145,37 @@ inline size_t round_line(size_t k) { return (k + 127) / 128 * 128; }
 // (int8.hip) Rows of x (bf16 or fp32) as codes and a scale each: scale = a / 127,
 // code = rint(v * (127 / a)), a the row's largest magnitude; a row with a below
 // kInt8Tiny is held as zeros, one that is not finite gets a scale of NaN.  Rows
-// of q lie ldq bytes apart, with zeros in cols .. ldq (multiples of 16).  With
-// tok_epd also epd_tok[tok_epd[t k + j]] = t for every row t.
+// of q lie ldq bytes apart, with zeros in cols .. ldq (multiples of 16).
 constexpr float kInt8Tiny = 0x1p-100f;
 hipError_t launch_quantize_rows(const void *x, int bf16, size_t rows, int cols, int8_t *q,
-                                size_t ldq, float *scale, const int32_t *tok_epd, int k,
-                                int32_t *epd_tok, hipStream_t s);
+                                size_t ldq, float *scale, hipStream_t s);
+// (slots.hip) The slots sorted by expert: EPD row of each slot (tok_epd, T x k), token and
+// weight of each EPD row (epd_tok, epd_w), segments of the placement's positions (epd_off) and
+// their row tiles (tile_off) as launch_brim's; ids and w are the caller's, made safe as by
+// launch_sanitize_ids.  Beside that the rows of x as codes (xq, ldx bytes apart) with scales xs.
+constexpr int kSlotsSmall = 1024, kSlotsSmallEntries = 8192;  // tokens and entries of one workgroup
+constexpr int kSlotsMaxShares = 256;
+struct SlotArgs {
+    const int32_t *ids;
+    const float *w;
+    const u32x4 *x;
+    int8_t *xq;
+    float *xs;
+    int32_t *tok_epd, *epd_tok, *epd_off, *tile_off;
+    float *epd_w;
+    int32_t *counts;  // kSlotsMaxShares x Ne
+    size_t ldx;
+    int T, d, k, tile_rows, fill_cols;
+    PlaceTab tab;
+    int share, shares, cus;  // set by the launcher
+};
+// Tokens a workgroup sorts; 0: one workgroup sorts all.
+inline int slot_shares(int T, int k) {
+    if (T <= kSlotsSmall && static_cast<size_t>(T) * k <= kSlotsSmallEntries) return 0;
+    const int per = static_cast<int>(ceil_div(T, kSlotsMaxShares));
+    return per > 256 ? per : 256;
+}
+hipError_t launch_slots(const SlotArgs &a, hipStream_t s);
 // y[t] = bf16( sum over j of y_epd[tok_epd[t k + j]] + sum over s of y_sh[s T + t] ), bf16
 // rows of d, fp32 sums in that order.
 hipError_t launch_combine_rows(const uint16_t *y_epd, const int32_t *tok_epd, const uint16_t *y_sh,
