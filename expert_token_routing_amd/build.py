@@ -23,7 +23,7 @@ ARCH = os.environ.get("OCC_OFFLOAD_ARCH", "gfx950")
 SOURCES = ["api.hip", "route.hip", "brim.hip", "rows.hip", "gemm_bf16.hip", "gemm_f32.hip",
            "coact.hip", "similarity.hip", "gate.hip", "gemm_bf16_m128.hip", "gemm_bf16_dense.hip",
            "gemm_bwd.hip", "backward.hip", "norm.hip", "balance.hip", "gate_bwd.hip", "adamw.hip",
-           "gemm_int8.hip", "gemm_int8_m128.hip", "int8.hip", "int8_few.hip", "slots.hip", "score.hip"]
+           "gemm_int8.hip", "gemm_int8_m80.hip", "int8.hip", "int8_few.hip", "slots.hip", "score.hip"]
 
 CXXFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",

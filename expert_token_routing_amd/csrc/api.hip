@@ -386,19 +386,42 @@ occ_status check_score(const occ_layer_desc *desc, const occ_score_desc *opt) {
     return OCC_OK;
 }
 
-#ifndef OCC_FEW_SLOTS
-#define OCC_FEW_SLOTS 32
-#endif
-constexpr int kFewTokenSlots = OCC_FEW_SLOTS;
-
 // The 8-bit layer's buffers: the sorted slots, then codes, scales and terms.
 struct Int8Layout {
     size_t tok_epd, epd_tok, epd_w, epd_off, tile_off, counts, xq, xs, h, hq, hs, y_epd, y_sh, total;
 };
 
-// Whether the layer runs without sorting its slots (int8_few.hip).
+// The row tiles of its products: the capacity, and the columns by which the
+// schedule fills the last round (0: not).
+bool small_tiles8(const occ_layer_desc &D) {
+    return static_cast<int64_t>(D.T) * D.k < static_cast<int64_t>(kSmallTileRows8) * D.Ne;
+}
+int tile_rows8(const occ_layer_desc &D) { return small_tiles8(D) ? kGemmBmInt8Small : kGemmBmBf16; }
+int fill_cols8(const occ_layer_desc &D) { return small_tiles8(D) ? 0 : static_cast<int>(ceil_div(D.F, 128)); }
+
+// The most row tiles that a routing can make: E experts with rows have at most
+// (slots - E) / capacity + E, and filling the last round of the CUs adds no
+// more than that round holds.
+size_t most_row_tiles8(const occ_layer_desc &D) {
+    const int64_t slots = static_cast<int64_t>(D.T) * D.k, E = std::min<int64_t>(D.Ne, slots);
+    const int64_t most = (slots - E) / tile_rows8(D) + E, cols = fill_cols8(D);
+    if (cols == 0) return static_cast<size_t>(most);
+    const int64_t cus = compute_units(), rounds = (most * cols + cus - 1) / cus;
+    return static_cast<size_t>(std::min(std::max(most, rounds * cus / cols), most + kBrimMaxFill));
+}
+
+// Whether the layer runs without sorting its slots (int8_few.hip): each slot
+// then reads its expert's weights for itself, so what decides is the bytes that
+// all slots read.  Measured against the general path (us): 64 experts of F =
+// 1024, top 8 (50 MB a token): 1 token 18 / 33, 4 tokens 42 / 48, 5 50 / 52, 6
+// 58 / 53; 60 of F = 1408, top 4, with a shared expert of 5632 (69 MB, shared
+// bytes from the caches): 3 tokens 51 / 75, 6 84 / 90, 7 100 / 89; 128 of F =
+// 768, d = 1024, top 2 (5 MB): 16 tokens 21 / 29.
+constexpr int64_t kFewBytes = 256 << 20;
+constexpr int kFewTokenSlots = 64;
 bool few_tokens(const occ_layer_desc &D) {
-    return static_cast<int64_t>(D.T) * D.k <= kFewTokenSlots &&
+    const int64_t token = 3ll * D.d * (static_cast<int64_t>(D.k) * D.F + static_cast<int64_t>(D.n_shared) * (D.n_shared > 0 ? D.F_shared : 0));
+    return static_cast<int64_t>(D.T) * D.k <= kFewTokenSlots && D.T * token <= kFewBytes &&
            few_fits(D.d, D.k, D.F, D.n_shared, D.F_shared);
 }
 
@@ -1408,11 +1431,10 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
         OCC_HIP(launch_few(f, s));
         return OCC_OK;
     }
-    // the tile heights and their rule are the bf16 products'
-    const bool small = tile_rows(D) == kGemmBmBf16Small;
-    const auto gemm_up = small ? launch_gemm_up8_m128 : launch_gemm_up8;
-    const auto gemm_down = small ? launch_gemm_down8_m128 : launch_gemm_down8;
-    const size_t routed_tiles = (nepd + tile_rows(D) - 1) / tile_rows(D) + D.Ne + kBrimMaxFill;
+    const bool small = small_tiles8(D);
+    const auto gemm_up = small ? launch_gemm_up8_m80 : launch_gemm_up8;
+    const auto gemm_down = small ? launch_gemm_down8_m80 : launch_gemm_down8;
+    const size_t routed_tiles = most_row_tiles8(D);
 
     // a token's row of codes is kept once and gathered by each of its experts
     SlotArgs sl{};
@@ -1431,8 +1453,8 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
     sl.T = D.T;
     sl.d = D.d;
     sl.k = D.k;
-    sl.tile_rows = tile_rows(D);
-    sl.fill_cols = fill_cols(D);
+    sl.tile_rows = tile_rows8(D);
+    sl.fill_cols = fill_cols8(D);
     sl.tab = tab;
     OCC_HIP(launch_slots(sl, s));
     for (int sx = 0; sx < D.n_shared; sx++) {

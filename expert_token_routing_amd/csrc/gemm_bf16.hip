@@ -57,7 +57,7 @@ namespace {
 
 // Second bound: waves per SIMD = workgroups per CU x NT / 256.
 __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k_gemm_up)(UpArgs a) {
-    __shared__ __attribute__((aligned(16))) uint16_t smem[NSTAGE * STAGE];
+    __shared__ __attribute__((aligned(16))) uint16_t smem[RING];
     __shared__ float s_w[BM];
     Tile t;
     if (!tile_of(a.seg_off, a.tile_off, a.M, a.m_tiles, a.Ne, a.tab, (a.N + 127) / 128, 128, t))
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
 }
 
 __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k_gemm_down)(DownArgs a) {
-    __shared__ __attribute__((aligned(16))) uint16_t smem[NSTAGE * STAGE];
+    __shared__ __attribute__((aligned(16))) uint16_t smem[RING];
     __shared__ int s_dst[BM];
     Tile t;
     if (!tile_of(a.seg_off, a.tile_off, a.M, a.m_tiles, a.Ne, a.tab, (a.N + BN - 1) / BN, BN, t,

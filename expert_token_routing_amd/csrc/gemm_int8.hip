@@ -14,7 +14,7 @@
 // cycles that the bf16 one does.  Half the bytes and half the instructions a
 // product.  K need only be a multiple of 64: rows of codes are padded with
 // zeros to whole lines (lda), and in the last line the loads of weights that
-// would pass the row's end read its first half again, which meets zeros.
+// would pass the row's end read what lies before it again, which meets zeros.
 #ifndef OCC_GEMM_INT8
 #define OCC_GEMM_INT8 1
 #endif
@@ -23,20 +23,21 @@
 namespace occ {
 namespace {
 
-// The direct loads' addresses; the last K slice of a product whose K is an
-// odd number of half lines starts at `last`, where the threads that hold the
-// missing half step back to the present one.
-struct HalfLineSrc {
+constexpr int FT = BN / 2;  // features of an up-projection tile: as many gate and up columns
+
+// The direct loads' addresses; where the last K slice is not a whole line it
+// starts at `last`, and the threads behind the row's end step back into it.
+struct LineEndSrc {
     const uint16_t *a[A_LD], *b[B_LD];
     size_t last;
     int back;
     __device__ const uint16_t *a_at(int i, int k0) const { return a[i] + k0; }
     __device__ const uint16_t *b_at(int i, size_t bo) const { return b[i] + bo - (bo == last ? back : 0); }
 };
-__device__ __forceinline__ void half_line(HalfLineSrc &src, int K, int chunk) {
-    const bool half = K % BK != 0;
-    src.last = half ? static_cast<size_t>(K - K % BK) : ~static_cast<size_t>(0);
-    src.back = half && chunk >= CHUNKS / 2 ? BK / 2 : 0;
+__device__ __forceinline__ void line_end(LineEndSrc &src, int K, int chunk) {
+    const int rest = K % BK, chunks = rest / 8;
+    src.last = rest ? static_cast<size_t>(K - rest) : ~static_cast<size_t>(0);
+    src.back = rest && chunk >= chunks ? (chunk - chunk % chunks) * 8 : 0;
 }
 
 __device__ __forceinline__ void clear(acc_t (&acc)[MI][NI]) {
@@ -47,11 +48,11 @@ __device__ __forceinline__ void clear(acc_t (&acc)[MI][NI]) {
 }
 
 __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k_gemm_up8)(Up8Args a) {
-    __shared__ __attribute__((aligned(16))) uint16_t smem[NSTAGE * STAGE];
+    __shared__ __attribute__((aligned(16))) uint16_t smem[RING];
     __shared__ float s_x[BM], s_w[BM];
-    __shared__ f32x4 s_g[128 / 4], s_u[128 / 4];
+    __shared__ f32x4 s_g[FT / 4], s_u[FT / 4];
     Tile t;
-    if (!tile_of(a.seg_off, a.tile_off, a.M, a.m_tiles, a.Ne, a.tab, (a.N + 127) / 128, 128, t))
+    if (!tile_of(a.seg_off, a.tile_off, a.M, a.m_tiles, a.Ne, a.tab, (a.N + FT - 1) / FT, FT, t))
         return;
 
     const int tid = threadIdx.x, r0 = tid / CHUNKS;
@@ -60,7 +61,7 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
     const size_t w0 = static_cast<size_t>(t.e) * N;
     const uint16_t *Wg = reinterpret_cast<const uint16_t *>(a.Wg) + w0 * K;
     const uint16_t *Wu = reinterpret_cast<const uint16_t *>(a.Wu) + w0 * K;
-    HalfLineSrc src;
+    LineEndSrc src;
 #pragma unroll
     for (int i = 0; i < A_LD; i++) {
         const int r = min(r0 + i * ROWS_PER_PASS, t.rows - 1);
@@ -71,19 +72,19 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
 #pragma unroll
     for (int i = 0; i < B_LD; i++) {
         const int rb = r0 + i * ROWS_PER_PASS;
-        const int f = min(t.n0 + (rb & 127), N - 1);
-        src.b[i] = (rb < 128 ? Wg : Wu) + static_cast<size_t>(f) * K + fetch_chunk(rb) * 8;
+        const int f = min(t.n0 + rb % FT, N - 1);
+        src.b[i] = (rb < FT ? Wg : Wu) + static_cast<size_t>(f) * K + fetch_chunk(rb) * 8;
     }
     // rows a whole number of passes apart share their swizzle key, and so a
     // thread's chunk
-    static_assert(ROWS_PER_PASS % (2 * CHUNKS) == 0, "one fetch chunk a thread");
-    half_line(src, K, fetch_chunk(r0));
+    static_assert(ROWS_PER_PASS % 16 == 0, "one fetch chunk a thread");
+    line_end(src, K, fetch_chunk(r0));
 
     const int l = lane_id(), wv = tid / kWave, wm = wv >> 1, wn = wv & 1;
     int brow[NI];
 #pragma unroll
     for (int ni = 0; ni < NI; ni++)
-        brow[ni] = (ni < NI / 2 ? 0 : 128) + wn * 64 + (ni % (NI / 2)) * 16 + (l & 15);
+        brow[ni] = (ni < NI / 2 ? 0 : FT) + wn * (FT / 2) + (ni % (NI / 2)) * 16 + (l & 15);
     acc_t acc[MI][NI];
     clear(acc);
 
@@ -95,7 +96,7 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
             s_x[tid] = a.a_scale[a.a_rows ? a.a_rows[row] : row];
             s_w[tid] = a.row_w ? a.row_w[row] : 1.f;
         }
-        if (tid < 128) {
+        if (tid < FT) {
             const int f = min(t.n0 + tid, N - 1);
             reinterpret_cast<float *>(s_g)[tid] = a.sg[w0 + f];
             reinterpret_cast<float *>(s_u)[tid] = a.su[w0 + f];
@@ -116,7 +117,7 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
         float *dst = a.out + (static_cast<size_t>(t.seg) + t.m0 + r) * N;
 #pragma unroll
         for (int ni = 0; ni < NI / 2; ni++) {
-            const int c = wn * 64 + ni * 16 + 4 * (l >> 4);
+            const int c = wn * (FT / 2) + ni * 16 + 4 * (l >> 4);
             if (t.n0 + c >= N) continue;
             const f32x4 cg = s_g[c / 4], cu = s_u[c / 4];
             f32x4 o;
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
 }
 
 __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k_gemm_down8)(Down8Args a) {
-    __shared__ __attribute__((aligned(16))) uint16_t smem[NSTAGE * STAGE];
+    __shared__ __attribute__((aligned(16))) uint16_t smem[RING];
     __shared__ float s_h[BM];
     __shared__ f32x4 s_d[BN / 4];
     Tile t;
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
     const uint16_t *A = reinterpret_cast<const uint16_t *>(a.A);
     const size_t w0 = static_cast<size_t>(t.e) * N;
     const uint16_t *W = reinterpret_cast<const uint16_t *>(a.W) + w0 * K;
-    HalfLineSrc src;
+    LineEndSrc src;
 #pragma unroll
     for (int i = 0; i < A_LD; i++) {
         const int r = min(r0 + i * ROWS_PER_PASS, t.rows - 1);
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
         const int n = min(t.n0 + r0 + i * ROWS_PER_PASS, N - 1);
         src.b[i] = W + static_cast<size_t>(n) * K + fetch_chunk(r0 + i * ROWS_PER_PASS) * 8;
     }
-    half_line(src, K, fetch_chunk(r0));
+    line_end(src, K, fetch_chunk(r0));
 
     const int l = lane_id(), wv = tid / kWave, wm = wv >> 1, wn = wv & 1;
     int brow[NI];
@@ -171,9 +172,9 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
         if (tid < t.rows) s_h[tid] = a.a_scale[static_cast<size_t>(t.seg) + t.m0 + tid];
         if (tid < BN) reinterpret_cast<float *>(s_d)[tid] = a.sd[w0 + min(t.n0 + tid, N - 1)];
     };
-    run_k_loop<true>(nv, src, K, K, 0, smem, wm, brow, acc, na, pre);
+    run_k_loop<true, false>(nv, src, K, K, 0, smem, wm, brow, acc, na, pre);
 
-    // bf16 rows staged in LDS, 2 x 64 columns at a time (the K buffers are
+    // bf16 rows staged in LDS, 64 columns of each wave column at a time (the K buffers are
     // free after the loop), and written as 16-byte chunks.  The terms of a
     // token's sum are rounded to bf16 here (2^-9, a fifth of the codes' own
     // error) since in fp32 they would be most of what the layer moves: the
@@ -181,14 +182,14 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
     constexpr int CH = 128 / 8;
     uint16_t *out = a.out;
 #pragma unroll
-    for (int half = 0; half < 2; half++) {
+    for (int part = 0; part < WN / 64; part++) {
 #pragma unroll
         for (int mi = 0; mi < MI; mi++) {
             const int r = block_row(wm, mi) + (l & 15);
             const float hs = s_h[min(r, t.rows - 1)];
 #pragma unroll
-            for (int q = 0; q < NI / 2; q++) {
-                const int ni = half * (NI / 2) + q;
+            for (int q = 0; q < 4; q++) {
+                const int ni = part * 4 + q;
                 const f32x4 cd = s_d[(wn * WN + ni * 16) / 4 + (l >> 4)];
                 u16x4 o;
 #pragma unroll
@@ -201,12 +202,12 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
 #pragma unroll 4
         for (int i = tid; i < BM * CH; i += NT) {
             const int r = i / CH, c = (i % CH) * 8;
-            const int col = t.n0 + (c >> 6) * WN + half * 64 + (c & 63);
+            const int col = t.n0 + (c >> 6) * WN + part * 64 + (c & 63);
             if (r >= t.rows || col >= N) continue;
             const u32x4 v = *reinterpret_cast<const u32x4 *>(smem + r * OUT_PITCH + c);
             *reinterpret_cast<u32x4 *>(out + (static_cast<size_t>(t.seg) + t.m0 + r) * N + col) = v;
         }
-        if (half == 0) __syncthreads();
+        if (part + 1 < WN / 64) __syncthreads();
     }
 }
 
@@ -214,7 +215,7 @@ __global__ __launch_bounds__(NT, OCC_GEMM_WG_PER_CU * NT / 256) void OCC_NAMED(k
 
 hipError_t OCC_NAMED(launch_gemm_up8)(const Up8Args &a, size_t max_m_tiles, hipStream_t s) {
     Up8Args b = a;
-    const int n_tiles = static_cast<int>(ceil_div(a.N, 128));
+    const int n_tiles = static_cast<int>(ceil_div(a.N, FT));
     if (!a.seg_off) {
         b.m_tiles = dense_row_tiles(a.M, n_tiles);
         max_m_tiles = static_cast<size_t>(b.m_tiles);

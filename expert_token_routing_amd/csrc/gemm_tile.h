@@ -56,18 +56,21 @@ typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 #define OCC_CAT(a, b) OCC_CAT2(a, b)
 #define OCC_NAMED(name) OCC_CAT(name, OCC_GEMM_SUFFIX)
 constexpr int BM = OCC_GEMM_TILE_M;  // rows (tokens) per tile
-constexpr int BN = 256;           // MFMA columns per tile
+#ifndef OCC_GEMM_TILE_N
+#define OCC_GEMM_TILE_N 256
+#endif
+constexpr int BN = OCC_GEMM_TILE_N;  // MFMA columns per tile
 constexpr int BK = OCC_GEMM_BK;   // K slice
 #ifndef OCC_GEMM_NT
 #define OCC_GEMM_NT 512
 #endif
 constexpr int NT = OCC_GEMM_NT;          // threads: (NT/128) x 2 waves
 constexpr int WAVES_M = NT / kWave / 2;
-constexpr int WM = BM / WAVES_M, WN = BN / 2;  // wave sub-tile
-constexpr int MI = WM / 16, NI = WN / 16;
+constexpr int WN = BN / 2;               // columns of a wave
+constexpr int MI = (BM / 16 + WAVES_M - 1) / WAVES_M, NI = WN / 16;  // its 16 x 16 blocks
 constexpr int CHUNKS = BK / 8;           // 16-byte chunks per LDS row
 constexpr int ROWS_PER_PASS = NT / CHUNKS;  // rows one pass of the workgroup moves
-constexpr int A_LD = BM / ROWS_PER_PASS;
+constexpr int A_LD = (BM + ROWS_PER_PASS - 1) / ROWS_PER_PASS;
 constexpr int B_LD = BN / ROWS_PER_PASS;
 constexpr int STAGE = (BM + BN) * BK;    // bf16 elements per LDS buffer
 #ifndef OCC_GEMM_NSTAGE
@@ -77,8 +80,9 @@ constexpr int NSTAGE = OCC_GEMM_NSTAGE;  // LDS ring filled by direct global->LD
 static_assert(NSTAGE >= 2 && NSTAGE <= 5, "ring depth");
 static_assert(BK == 32 || BK == 64, "a wave load moves 1 KB: 16 rows of 64 bytes or 8 of 128");
 constexpr int OUT_PITCH = 128 + 8;       // up epilogue staging row (elements)
-static_assert(NSTAGE * STAGE * 2 * OCC_GEMM_WG_PER_CU <= 160 * 1024, "LDS");
-static_assert(BM * OUT_PITCH <= NSTAGE * STAGE, "epilogue staging fits in the K buffers");
+constexpr int RING = NSTAGE * STAGE;     // its elements
+static_assert(RING * 2 * OCC_GEMM_WG_PER_CU <= 160 * 1024, "LDS");
+static_assert(MI * WAVES_M * 16 * OUT_PITCH <= RING, "epilogue staging fits in the K buffers");
 
 // Chunk c of row r sits at chunk slot c ^ ((r >> 1) mod chunks-per-row).  A
 // 16-byte fragment read covers 16 consecutive rows at one logical chunk;
@@ -311,7 +315,7 @@ struct PtrSrc {  // one 64-bit address per slot
 // needs are loaded there, their latency hidden under those slices' (the
 // loop's first barrier publishes what it writes to LDS).
 #if !OCC_GEMM_PIPE
-template <int NV, bool SWAP, class Src, class Pre>
+template <int NV, bool SWAP, bool UP, class Src, class Pre>
 __device__ __forceinline__ void k_loop(const Src &src, int K, int ksp, size_t blk, uint16_t *smem,
                                        int wm, const int (&brow)[NI], acc_t (&acc)[MI][NI], int na,
                                        Pre &pre) {
@@ -401,7 +405,7 @@ __device__ __forceinline__ void frag_read(Frags<NV> &f, int r, const uint16_t *a
 // scheduling barrier after each MFMA keeps that order.  (The loads issued
 // in the step's first quarter or half instead were measured 2-5% slower in
 // both products.)
-template <int NV, bool SWAP, bool READ, class Dma>
+template <int NV, bool SWAP, bool UP, bool READ, class Dma>
 __device__ __forceinline__ void pipe_step(const Frags<NV> &cur, Frags<NV> &nxt, const uint16_t *ab,
                                           const uint16_t *bb, acc_t (&acc)[MI][NI], int nd,
                                           Dma &dma) {
@@ -413,7 +417,7 @@ __device__ __forceinline__ void pipe_step(const Frags<NV> &cur, Frags<NV> &nxt, 
         const int mi = m / NI, ni = m % NI;
         acc[mi][ni] = SWAP ? mma(cur.b[ni], cur.a[mi], acc[mi][ni]) : mma(cur.a[mi], cur.b[ni], acc[mi][ni]);
         const int r = (m * NR + RSPAN - 1) / RSPAN;
-        if (READ && r < NR && r * RSPAN / NR == m) frag_read<NV, SWAP>(nxt, r, ab, bb);
+        if (READ && r < NR && r * RSPAN / NR == m) frag_read<NV, UP>(nxt, r, ab, bb);
         const int d = (m * ND + DSPAN - 1) / DSPAN;
         if (d < ND && d * DSPAN / ND == m && d < nd) dma(d);
         __builtin_amdgcn_sched_barrier(0);
@@ -421,14 +425,14 @@ __device__ __forceinline__ void pipe_step(const Frags<NV> &cur, Frags<NV> &nxt, 
     if constexpr (READ) {
 #pragma unroll
         for (int r = 0; r < NR; r++)
-            if (r * RSPAN / NR >= NM) frag_read<NV, SWAP>(nxt, r, ab, bb);
+            if (r * RSPAN / NR >= NM) frag_read<NV, UP>(nxt, r, ab, bb);
     }
 #pragma unroll
     for (int d = 0; d < ND; d++)
         if (d * DSPAN / ND >= NM && d < nd) dma(d);
 }
 
-template <int NV, bool SWAP, class Src, class Pre>
+template <int NV, bool SWAP, bool UP, class Src, class Pre>
 __device__ __forceinline__ void k_loop(const Src &src, int K, int ksp, size_t blk, uint16_t *smem,
                                        int wm, const int (&brow)[NI], acc_t (&acc)[MI][NI], int,
                                        Pre &pre) {
@@ -467,50 +471,51 @@ __device__ __forceinline__ void k_loop(const Src &src, int K, int ksp, size_t bl
     auto bb = [&](int slot, int h) { return smem + slot * STAGE + bo0 + h; };
     Frags<NV> f0, f1;
 #pragma unroll
-    for (int r = 0; r < NV + NI; r++) frag_read<NV, SWAP>(f0, r, ab(0, h0), bb(0, h0));
+    for (int r = 0; r < NV + NI; r++) frag_read<NV, UP>(f0, r, ab(0, h0), bb(0, h0));
     auto none = [](int) {};
     int kt = 0;
     for (; kt + 2 < nk; kt++) {  // slice kt; slice kt+2's loads go out during its second step
         const int slot = kt & 1;
-        pipe_step<NV, SWAP, true>(f0, f1, ab(slot, h1), bb(slot, h1), acc, 0, none);
+        pipe_step<NV, SWAP, UP, true>(f0, f1, ab(slot, h1), bb(slot, h1), acc, 0, none);
         wait_vmcnt<0>();
         __syncthreads();
         const size_t bo = b_off(kt + 2);
         auto dma = [&](int d) { load(kt + 2, bo, d); };
-        pipe_step<NV, SWAP, true>(f1, f0, ab(slot ^ 1, h0), bb(slot ^ 1, h0), acc, LOADS, dma);
+        pipe_step<NV, SWAP, UP, true>(f1, f0, ab(slot ^ 1, h0), bb(slot ^ 1, h0), acc, LOADS, dma);
     }
     if (kt + 1 < nk) {  // the last but one slice: nothing left to load
         const int slot = kt & 1;
-        pipe_step<NV, SWAP, true>(f0, f1, ab(slot, h1), bb(slot, h1), acc, 0, none);
+        pipe_step<NV, SWAP, UP, true>(f0, f1, ab(slot, h1), bb(slot, h1), acc, 0, none);
         wait_vmcnt<0>();
         __syncthreads();
-        pipe_step<NV, SWAP, true>(f1, f0, ab(slot ^ 1, h0), bb(slot ^ 1, h0), acc, 0, none);
+        pipe_step<NV, SWAP, UP, true>(f1, f0, ab(slot ^ 1, h0), bb(slot ^ 1, h0), acc, 0, none);
         kt++;
     }
     {  // the last slice
         const int slot = kt & 1;
-        pipe_step<NV, SWAP, true>(f0, f1, ab(slot, h1), bb(slot, h1), acc, 0, none);
-        pipe_step<NV, SWAP, false>(f1, f0, ab(slot, h0), bb(slot, h0), acc, 0, none);
+        pipe_step<NV, SWAP, UP, true>(f0, f1, ab(slot, h1), bb(slot, h1), acc, 0, none);
+        pipe_step<NV, SWAP, UP, false>(f1, f0, ab(slot, h0), bb(slot, h0), acc, 0, none);
     }
     __syncthreads();
 }
 #endif
 
 // Runs the K loop with the wave's block count as a constant.
-template <bool SWAP, int NV = MI, class Src, class Pre>
+// UP: the B columns are pairs of gate and up blocks.
+template <bool SWAP, bool UP = SWAP, int NV = MI, class Src, class Pre>
 __device__ __forceinline__ void run_k_loop(int nv, const Src &src, int K, int ksp, size_t blk,
                                            uint16_t *smem, int wm, const int (&brow)[NI],
                                            acc_t (&acc)[MI][NI], int na, Pre &pre) {
     if constexpr (NV == 0) {
-        k_loop<0, SWAP>(src, K, ksp, blk, smem, wm, brow, acc, na, pre);
+        k_loop<0, SWAP, UP>(src, K, ksp, blk, smem, wm, brow, acc, na, pre);
     } else if constexpr (OCC_GEMM_PIPE) {
         // a wave with rows multiplies all of its blocks (those past the
         // tile's rows hold repeated rows whose results are not stored)
-        if (nv > 0) k_loop<MI, SWAP>(src, K, ksp, blk, smem, wm, brow, acc, na, pre);
-        else k_loop<0, SWAP>(src, K, ksp, blk, smem, wm, brow, acc, na, pre);
+        if (nv > 0) k_loop<MI, SWAP, UP>(src, K, ksp, blk, smem, wm, brow, acc, na, pre);
+        else k_loop<0, SWAP, UP>(src, K, ksp, blk, smem, wm, brow, acc, na, pre);
     } else {
-        if (nv >= NV) k_loop<NV, SWAP>(src, K, ksp, blk, smem, wm, brow, acc, na, pre);
-        else run_k_loop<SWAP, NV - 1>(nv, src, K, ksp, blk, smem, wm, brow, acc, na, pre);
+        if (nv >= NV) k_loop<NV, SWAP, UP>(src, K, ksp, blk, smem, wm, brow, acc, na, pre);
+        else run_k_loop<SWAP, UP, NV - 1>(nv, src, K, ksp, blk, smem, wm, brow, acc, na, pre);
     }
 }
 

@@ -209,8 +209,11 @@ struct Down8Args {
 };
 hipError_t launch_gemm_up8(const Up8Args &a, size_t max_m_tiles, hipStream_t s);
 hipError_t launch_gemm_down8(const Down8Args &a, size_t max_m_tiles, hipStream_t s);
-hipError_t launch_gemm_up8_m128(const Up8Args &a, size_t max_m_tiles, hipStream_t s);
-hipError_t launch_gemm_down8_m128(const Down8Args &a, size_t max_m_tiles, hipStream_t s);
+// The same with 80 x 128 tiles (gemm_int8_m80.hip), for batches whose experts average fewer
+// than kSmallTileRows8 rows.
+constexpr int kGemmBmInt8Small = 80, kSmallTileRows8 = 128;
+hipError_t launch_gemm_up8_m80(const Up8Args &a, size_t max_m_tiles, hipStream_t s);
+hipError_t launch_gemm_down8_m80(const Down8Args &a, size_t max_m_tiles, hipStream_t s);
 
 // (int8_few.hip) The whole layer for few tokens: x, y T x d bf16, ids and w as
 // the caller gave them; h (T k x F) and h_sh (T n_shared x F_shared) are
