@@ -21,6 +21,7 @@ namespace occ {
 namespace {
 
 constexpr int kScoreThreads = 256;
+constexpr int kScoreSerial = 8192;  // tokens from which a wave takes four one after another
 constexpr unsigned kScoreGrid = 1 << 20;  // workgroups; more tokens loop
 
 // A double's place in the order of the doubles, above 0; NaN reads as -inf.
@@ -88,12 +89,17 @@ struct GroupWalk {
     }
 };
 
-// A token's LDS: the choice by place (a group's places together, groups
-// n + 1 apart: other banks), the groups' scores, and what was chosen.
-template <int L, int NI>
-struct TokenLds {
-    double choice[L * NI + kMaxNd];
+// LDS of a wave in choose64: the choice by place (a group's places together,
+// groups n + 1 apart: other banks) and the groups' scores; of a team in
+// keep_groups the same in 32 bits.
+struct ChoiceLds {
+    double choice[kMaxNe + kMaxNd];
     double group[kMaxNd];
+};
+template <int L, int NI>
+struct GroupLds {
+    uint32_t key[L * NI + kMaxNd];
+    float group[kMaxNd];
 };
 
 // The best two of two pairs.
@@ -125,29 +131,138 @@ __device__ __forceinline__ void group_scores(const V *choice, int Nd, int n, int
     }
 }
 
-// What a lane knows of its experts: at places l + L j of the placement where
-// groups matter (which puts a group's experts together), of 0..Ne-1 otherwise.
-template <int NI>
-struct Experts {
-    int e[NI];
-    float v[NI], b[NI];  // logit (-inf for one that is left out), bias
-};
-
+// e^x for x <= 0, within 2^-50: x = n ln 2 + r, |r| <= ln 2 / 2, and the series
+// of e^r up to r^12 (the rest is below 2^-52); a third of the instructions of a
+// general exp.
+__device__ __forceinline__ double exp64(double x) {
+    x = fmax(x, -800.);  // 0 from -746 on
+    const double n = rint(x * 0x1.71547652b82fep+0);
+    double r = fma(n, -0x1.62e42fefa3800p-1, x);
+    r = fma(n, -0x1.ef35793c76730p-45, r);
+    double p = 1. / 479001600.;
+    p = fma(p, r, 1. / 39916800.);
+    p = fma(p, r, 1. / 3628800.);
+    p = fma(p, r, 1. / 362880.);
+    p = fma(p, r, 1. / 40320.);
+    p = fma(p, r, 1. / 5040.);
+    p = fma(p, r, 1. / 720.);
+    p = fma(p, r, 1. / 120.);
+    p = fma(p, r, 1. / 24.);
+    p = fma(p, r, 1. / 6.);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.);
+    p = fma(p, r, 1.);
+    return ldexp(p, static_cast<int>(n));
+}
+// 1 / x of a normal number, within 2^-51: the hardware's estimate and two
+// steps of Newton's method.
+__device__ __forceinline__ double over64(double x) {
+    double y = __builtin_amdgcn_rcp(x);
+    y = fma(y, fma(-x, y, 1.), y);
+    return fma(y, fma(-x, y, 1.), y);
+}
 // A softmax's terms over the largest logit m; a logit of -inf has none.
 __device__ __forceinline__ double exp_over(float v, float m) {
-    return v == -INFINITY ? 0. : v == m ? 1. : exp(static_cast<double>(v) - static_cast<double>(m));
+    return v == -INFINITY ? 0. : v == m ? 1. : exp64(static_cast<double>(v) - static_cast<double>(m));
 }
 __device__ __forceinline__ double sigmoid64(float v) {
-    const double e = exp(-fabs(static_cast<double>(v)));
-    return (v < 0.f ? e : 1.) / (1. + e);
+    const double e = exp64(-fabs(static_cast<double>(v)));
+    return (v < 0.f ? e : 1.) * over64(1. + e);
+}
+
+struct Chosen {
+    int e;
+    uint32_t key;
+};
+
+// The `need` best of a wave's experts in order: by key, then by `fine` (of
+// experts of one key; the same in all for none), then by the lower index (the
+// larger rev = 256 - e).  A key that between `need` and kMoreHeads more lanes'
+// largest ones reach, bit by bit by ballots; then every expert that reaches it,
+// one a lane through LDS, counts those ahead of it.  False where that is more
+// than a wave of experts or the lanes with any are fewer than `need`.
+constexpr int kMoreHeads = 3;
+struct Candidate {
+    uint32_t rev, key;
+};
+template <int NI, bool FINE>
+__device__ __forceinline__ bool few_best(const uint32_t (&key)[NI], const uint32_t (&rev)[NI], const uint64_t *fine,
+                                         int need, Candidate *best, uint64_t *best_fine, Chosen *chosen) {
+    uint32_t head = key[0];
+#pragma unroll
+    for (int j = 1; j < NI; j++) head = max(head, key[j]);
+    uint32_t reach = 0;
+    for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+        const int n = __popcll(__ballot(head >= (reach | bit)));
+        if (n >= need) {
+            reach |= bit;
+            if (n <= need + kMoreHeads) break;
+        }
+    }
+    if (reach == 0) return false;
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < NI; j++) {
+        const uint64_t in = __ballot(key[j] >= reach);
+        const int at = n + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(in >> 32),
+                                                     __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(in), 0));
+        if (key[j] >= reach && at < kWave) {
+            best[at] = Candidate{rev[j], key[j]};
+            if constexpr (FINE) best_fine[at] = fine[j];
+        }
+        n += __popcll(in);
+    }
+    if (n > kWave) return false;
+    wave_sync();
+    const int lane = lane_id();
+    Candidate mine = best[lane];
+    if (lane >= n) mine = Candidate{0, 0};
+    int rank = 0;
+    if constexpr (FINE) {
+        const uint64_t at = best_fine[lane];
+        for (int i = 0; i < n; i++) {
+            const uint64_t o = best_fine[i];
+            const uint32_t r = best[i].rev;
+            rank += o > at || (o == at && r > mine.rev);
+        }
+    } else {
+        const uint64_t at = static_cast<uint64_t>(mine.key) << 32 | mine.rev;
+        for (int i = 0; i < n; i++) {
+            const uint64_t o = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(mine.key), i))) << 32 |
+                               static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(mine.rev), i));
+            rank += o > at;
+        }
+    }
+    if (lane < n && rank < need) chosen[rank] = Chosen{256 - static_cast<int>(mine.rev), mine.key};
+    return true;
 }
 
 // The choice in 64 bits throughout, for the tokens whose choice 32 bits cannot
-// tell: s_ids and s_v, the k chosen experts and their logits in order.
-template <int L, int NI, bool GROUPS>
-__device__ __forceinline__ void choose64(const ScoreArgs &a, const Experts<NI> &x,
-                                                   TokenLds<L, NI> &lds, int *s_ids, float *s_v) {
-    const int l = threadIdx.x % L, Ne = a.Ne, n = a.tab.n, Nd = a.tab.Nd;
+// tell: the k chosen experts in order, by all lanes of a wave.  A call of its
+// own, which loads its row anew.  Few tokens take it, but a launch ends with the
+// last of them.
+struct Choice {
+    const float *row, *bias;
+    const uint8_t *place;  // LDS: expert at each place
+    int Ne, k, n, Nd, sigmoid, top_groups, group_best;
+};
+template <int NI, bool GROUPS>
+__device__ __attribute__((noinline)) void choose64(Choice a, ChoiceLds *lds, Candidate *best, Chosen *chosen) {
+    constexpr int L = kWave;
+    const int l = lane_id(), Ne = a.Ne, n = a.n, Nd = a.Nd;
+    const float *row = a.row;
+    struct {
+        int e[NI];
+        float v[NI], b[NI];
+    } x;
+#pragma unroll
+    for (int j = 0; j < NI; j++) {
+        const int p = min(l + L * j, Ne - 1);
+        x.e[j] = GROUPS ? a.place[p] : p;
+        x.v[j] = row[x.e[j]];
+        x.b[j] = a.bias ? a.bias[x.e[j]] : 0.f;
+        if (!(l + L * j < Ne) || x.v[j] != x.v[j]) x.v[j] = -INFINITY;
+    }
     double c[NI];
     if (a.sigmoid) {
 #pragma unroll
@@ -165,7 +280,7 @@ __device__ __forceinline__ void choose64(const ScoreArgs &a, const Experts<NI> &
         }
         sum = team_reduce<L>(sum, [](double p, double q) { return p + q; });
 #pragma unroll
-        for (int j = 0; j < NI; j++) c[j] = sum > 0. ? c[j] / sum : 0.;
+        for (int j = 0; j < NI; j++) c[j] = sum > 0. ? c[j] * over64(sum) : 0.;
     }
 #pragma unroll
     for (int j = 0; j < NI; j++) c[j] = x.v[j] == -INFINITY ? -INFINITY : c[j] + x.b[j];
@@ -174,238 +289,377 @@ __device__ __forceinline__ void choose64(const ScoreArgs &a, const Experts<NI> &
 #pragma unroll
         for (int j = 0; j < NI; j++) {
             const int p = l + L * j;
-            if (p < Ne) lds.choice[p + p / n] = c[j];
+            if (p < Ne) lds->choice[p + p / n] = c[j];
         }
         wave_sync();
-        group_scores<L>(lds.choice, Nd, n, a.group_best, [&](int g, double v) {
-            if (g < Nd) lds.group[g] = v;
+        group_scores<L>(lds->choice, Nd, n, a.group_best, [&](int g, double v) {
+            if (g < Nd) lds->group[g] = v;
         });
         wave_sync();
         allowed = 0;
         for (int g = l; g < Nd; g += L) {
-            const double v = lds.group[g];
+            const double v = lds->group[g];
             int ahead = 0;
             for (int o = 0; o < Nd; o++) {
-                const double y = lds.group[o];
+                const double y = lds->group[o];
                 ahead += y > v || (y == v && o < g);
             }
             if (ahead < a.top_groups) allowed |= 1ull << g;
         }
         allowed = team_reduce<L>(allowed, [](uint64_t p, uint64_t q) { return p | q; });
     }
-    uint64_t key[NI];
+    uint64_t fine[NI];
+    uint32_t key[NI], rev[NI];
 #pragma unroll
     for (int j = 0; j < NI; j++) {
         const int p = l + L * j;
         bool ok = p < Ne;
         if constexpr (GROUPS) ok = ok && allowed >> (p / n) & 1;
-        key[j] = ok ? order_key(a.bias ? c[j] : static_cast<double>(x.v[j])) : 0;
+        const double o = a.bias ? c[j] : static_cast<double>(x.v[j]);
+        fine[j] = ok ? order_key(o) : 0;
+        key[j] = ok ? order_key(static_cast<float>(o)) : 0;  // (rounding keeps the order but for ties)
+        rev[j] = ok ? 256u - x.e[j] : 0;
     }
-    for (int i = 0; i < a.k; i++) {
-        uint64_t best = 0;
-        int who = 0x7fffffff;
+    if (few_best<NI, true>(key, rev, fine, a.k, best, reinterpret_cast<uint64_t *>(lds->choice), chosen)) {
+        wave_sync();
+        return;
+    }
+    for (int i = 0; i < a.k; i++) {  // one after another
+        uint64_t most = 0;
+        uint32_t low = 0;
 #pragma unroll
         for (int j = 0; j < NI; j++)
-            if (key[j] > best || (key[j] == best && x.e[j] < who)) {
-                best = key[j];
-                who = x.e[j];
+            if (fine[j] > most || (fine[j] == most && rev[j] > low)) {
+                most = fine[j];
+                low = rev[j];
             }
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) {
-            const uint64_t ob = __shfl_xor(best, o);
-            const int ow = __shfl_xor(who, o);
-            if (ob > best || (ob == best && ow < who)) {
-                best = ob;
-                who = ow;
+            const uint64_t om = __shfl_xor(most, o);
+            const uint32_t ow = __shfl_xor(low, o);
+            if (om > most || (om == most && ow > low)) {
+                most = om;
+                low = ow;
             }
         }
 #pragma unroll
         for (int j = 0; j < NI; j++)
-            if (key[j] && x.e[j] == who) {
-                key[j] = 0;
-                s_ids[i] = who;
-                s_v[i] = x.v[j];
+            if (fine[j] && rev[j] == low) {
+                fine[j] = 0;
+                chosen[i] = Chosen{256 - static_cast<int>(low), 0};
             }
     }
     wave_sync();
 }
 
+// The groups' scores from the order keys of c in LDS (as group_scores), and of
+// the kept groups: bit g << shift of the result; `sure` is whether the scores
+// at the border lie far enough apart.  Scores and their margins as floats.
+template <int L>
+__device__ __forceinline__ uint64_t keep_groups(const uint32_t *key, float *s_group, const ScoreArgs &a,
+                                                float margin, int &shift, bool &sure) {
+    const GroupWalk<L> walk(a.tab.Nd);
+    const int l = threadIdx.x % L, Nd = a.tab.Nd, n = a.tab.n, GL = 1 << walk.shift;
+    const int i = l & (GL - 1);
+    const auto score = [&](int g) {
+        uint32_t top = 0, next = 0;
+        const uint32_t *at = key + min(g, Nd - 1) * (n + 1);
+        for (int j0 = 0; j0 < n; j0 += 4 * GL) {
+            uint32_t k[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) k[j] = at[min(j0 + GL * j + i, n - 1)];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t one = g < Nd && j0 + GL * j + i < n ? k[j] : 0;
+                next = max(next, min(top, one));
+                top = max(top, one);
+            }
+        }
+        const auto join = [&](uint32_t ot, uint32_t on) {
+            next = max(max(next, on), min(top, ot));
+            top = max(top, ot);
+        };
+        if (GL >= 2) join(dpp_partner<kDppXor1>(top), dpp_partner<kDppXor1>(next));
+        if (GL >= 4) join(dpp_partner<kDppXor2>(top), dpp_partner<kDppXor2>(next));
+        if (GL >= 8) join(dpp_partner<kDppHalfMirror>(top), dpp_partner<kDppHalfMirror>(next));
+        if (GL >= 16) join(dpp_partner<kDppMirror>(top), dpp_partner<kDppMirror>(next));
+        if (GL >= 32) join(__shfl_xor(top, 16), __shfl_xor(next, 16));
+        if (GL >= 64) join(__shfl_xor(top, 32), __shfl_xor(next, 32));
+        // none left: -inf; one: no second
+        const float ft = top ? from_key(top) : -INFINITY, fn = next ? from_key(next) : -INFINITY;
+        return a.group_best > 1 && fn > -INFINITY ? ft + fn : ft;
+    };
+    uint64_t kept = 0;
+    shift = 0;
+    if (GL >= Nd) {  // (all groups at once) a group's lane i compares it with group i
+        const int g = l >> walk.shift;
+        const float v = score(g), y = __shfl(v, i << walk.shift, L);
+        const float off = 2.f * margin * (1.f + fabsf(v));
+        const bool other = i < Nd && g < Nd && i != g;
+        const uint64_t fields = GL >= 64 ? ~0ull : (1ull << GL) - 1;
+        const int ahead = __popcll(team_ballot<L>(other && y - v > off) >> (g << walk.shift) & fields);
+        const int near = __popcll(team_ballot<L>(other && !(v - y > off)) >> (g << walk.shift) & fields);
+        const bool in = near < a.top_groups, out = ahead >= a.top_groups;
+        sure = team_ballot<L>(g < Nd && !in && !out) == 0;
+        kept = team_ballot<L>(g < Nd && in && i == 0);
+        shift = walk.shift;
+        return kept;
+    }
+    for (int g0 = 0; g0 < Nd; g0 += walk.per) {
+        const int g = g0 + (l >> walk.shift);
+        const float v = score(g);
+        if (g < Nd && i == 0) s_group[g] = v;
+    }
+    wave_sync();
+    for (int g0 = 0; g0 < Nd; g0 += L) {
+        const int g = g0 + l;
+        const float v = g < Nd ? s_group[g] : -INFINITY, off = 2.f * margin * (1.f + fabsf(v));
+        int ahead = 0, near = 0;
+        for (int o = 0; o < Nd; o++) {
+            const float y = s_group[o];
+            ahead += y - v > off;
+            near += !(v - y > off) && o != g;
+        }
+        const bool in = near < a.top_groups, out = ahead >= a.top_groups;
+        sure = sure && team_ballot<L>(g < Nd && !in && !out) == 0;
+        kept |= team_ballot<L>(g < Nd && in) << g0;
+    }
+    return kept;
+}
+
 // A team of L lanes a token, NI experts a lane.  A choice is a border, and near
 // ties would fall differently in 32 bits than in 64 for a token in some
-// thousands.  Scores in 32 bits are off by less than half of margin(c), so a
+// thousands.  Scores in 32 bits are off by less than half of a margin, so a
 // choice whose neighbours (the chosen, the first not chosen, the groups at
 // their border) lie further apart is the one that 64 bits make; logits alone
 // order without an error, and experts of equal logit and bias tie in both.  The
-// tokens that are left take choose64.  The chosen experts' scores and the
-// weights are formed in 64 bits, a lane an expert.
-constexpr float kMargin = 0x1p-18f;
-template <int L, int NI, bool GROUPS>
-__global__ __launch_bounds__(kScoreThreads) void k_route_scored(ScoreArgs a) {
-    constexpr int TOK = kScoreThreads / L, KPL = L == 64 ? 1 : kMaxK / L;
-    __shared__ TokenLds<L, NI> s_lds[GROUPS ? TOK : 1];
-    __shared__ float s_v[TOK][kMaxK + 1], s_b[TOK][kMaxK + 1], s_c[TOK][kMaxK + 1];
-    __shared__ int s_ids[TOK][kMaxK + 1];
-    const int l = threadIdx.x % L, q = threadIdx.x / L;
-    const int Ne = a.Ne, k = a.k, n = a.tab.n, Nd = a.tab.Nd;
-    const bool biased = a.bias != nullptr;
-    for (size_t t0 = static_cast<size_t>(blockIdx.x) * TOK; t0 < static_cast<size_t>(a.T);
-         t0 += static_cast<size_t>(gridDim.x) * TOK) {
-        const size_t t = t0 + q;
-        const bool live = t < static_cast<size_t>(a.T);
-        const float *row = a.logits + (live ? t : a.T - 1) * Ne;
-        Experts<NI> x;
+// tokens that are left take choose64.
+//
+// Bound by instructions.  With 16 lanes a token a lane sorts its experts once,
+// and a round is the team's largest head and the winner's next one; all lanes
+// of a wave take few_best.  A wave makes the choice of four tokens (16 lanes
+// each, or all lanes one token after another) and then forms their weights in
+// 64 bits, 16 lanes a token.
+template <int L, int NI, bool GROUPS, bool BIASED>
+__global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) {
+    constexpr int TEAMS = kWave / L, WAVES = kScoreThreads / kWave, TOK = 4, W = 16, KPL = kMaxK / W;
+    constexpr bool DOUBT = GROUPS || BIASED || L == 64;  // (logits alone order for sure)
+    __shared__ Candidate s_best[DOUBT ? WAVES : 1][kWave];
+    __shared__ union {
+        GroupLds<L, NI> team[GROUPS ? TEAMS : 1];
+        ChoiceLds all;
+    } s_lds[DOUBT ? WAVES : 1];
+    __shared__ Chosen s_chosen[WAVES][TOK][kMaxK + 1];
+    __shared__ double s_sum[WAVES][TOK];
+    __shared__ float s_top[WAVES][TOK], s_margin[WAVES][TOK];  // INFINITY: not sure already
+    __shared__ uint8_t s_place[GROUPS ? kMaxNe : 1];
+    if constexpr (GROUPS) {
+        for (int p = threadIdx.x; p < a.Ne; p += kScoreThreads) s_place[p] = a.in_order ? p : a.tab.expert[p];
+        __syncthreads();
+    }
+    const int lane = lane_id(), wv = threadIdx.x / kWave, l = lane % L, team = lane / L;
+    const int Ne = a.Ne, k = a.k;
+    const bool full = !a.sigmoid && !a.renormalise;
+    int e_of[NI], g_of[NI];  // the lane's experts: at places l + L j of the placement where groups
+    float bias[NI];          // matter (which puts a group's together), of 0..Ne-1 otherwise
 #pragma unroll
-        for (int j = 0; j < NI; j++) {
-            const int p = min(l + L * j, Ne - 1);
-            x.e[j] = GROUPS && !a.in_order ? a.tab.expert[p] : p;
-            x.v[j] = row[x.e[j]];
-            x.b[j] = biased ? a.bias[x.e[j]] : 0.f;
-        }
+    for (int j = 0; j < NI; j++) {
+        const int p = min(l + L * j, Ne - 1);
+        e_of[j] = GROUPS ? s_place[p] : p;
+        bias[j] = BIASED ? a.bias[e_of[j]] : 0.f;
+        g_of[j] = GROUPS ? (l + L * j) * a.over_n >> 16 : 0;
+    }
+    const size_t T = a.T, step = static_cast<size_t>(gridDim.x) * WAVES * a.per_wave;
+    for (size_t t0 = (static_cast<size_t>(blockIdx.x) * WAVES + wv) * a.per_wave; t0 < T; t0 += step) {
+        for (int it = 0; it < a.per_wave; it += TEAMS) {
+            const int q = it + team;
+            const size_t t = min(t0 + q, T - 1);  // (behind the last one: again, and not written)
+            const float *row = a.logits + t * Ne;
+            Chosen *chosen = s_chosen[wv][q];
+            float v[NI];
 #pragma unroll
-        for (int j = 0; j < NI; j++)
-            if (!(l + L * j < Ne) || x.v[j] != x.v[j]) x.v[j] = -INFINITY;
-        float top = 0.f;  // the largest logit, for a softmax
-        if (!a.sigmoid) {
-            uint32_t m = 0;
+            for (int j = 0; j < NI; j++) v[j] = row[e_of[j]];
 #pragma unroll
-            for (int j = 0; j < NI; j++) m = max(m, order_key(x.v[j]));
-            top = from_key(team_max<L>(m));
-        }
-        float c[NI];
-        bool sure = true;
-        if (GROUPS || biased) {
-            if (a.sigmoid) {
+            for (int j = 0; j < NI; j++)
+                if (!(l + L * j < Ne) || v[j] != v[j]) v[j] = -INFINITY;
+            float top = 0.f;  // the largest logit, for a softmax
+            if (!a.sigmoid && (GROUPS || BIASED || full)) {
+                uint32_t m = 0;
 #pragma unroll
-                for (int j = 0; j < NI; j++) {
-                    const float e = __expf(-fabsf(x.v[j]));
-                    c[j] = (x.v[j] < 0.f ? e : 1.f) * __builtin_amdgcn_rcpf(1.f + e);
-                }
-            } else {
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < NI; j++) {
-                    c[j] = x.v[j] == -INFINITY ? 0.f : x.v[j] == top ? 1.f : __expf(x.v[j] - top);
-                    sum += c[j];
-                }
-                sum = team_sum<L>(sum);
-                const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
-#pragma unroll
-                for (int j = 0; j < NI; j++) c[j] *= inv;
+                for (int j = 0; j < NI; j++) m = max(m, order_key(v[j]));
+                top = from_key(team_max<L>(m));
             }
+            // How far apart two choices in 32 bits must be, over 1 + |c|, to be
+            // sure: twice the error of one.  A sigmoid's is below 2^-22 (2^-23
+            // for the reciprocal, 2^-24 for the sum in it, 0.42 2^-23 for the
+            // exponential, whose own is 2^-23 + 1.5 |v| 2^-24) and 2^-24 |c| for
+            // the bias; a softmax's below 2^-19 of the largest p (the terms'
+            // exponentials, their sum and its reciprocal) besides.
+            float margin = 0x1p-21f;
+            float c[NI];
+            bool sure = true;
+            if constexpr (GROUPS || BIASED) {
+                if (a.sigmoid) {
 #pragma unroll
-            for (int j = 0; j < NI; j++) c[j] = x.v[j] == -INFINITY ? -INFINITY : c[j] + x.b[j];
-        }
-        uint32_t key[NI];
+                    for (int j = 0; j < NI; j++) {
+                        c[j] = __builtin_amdgcn_rcpf(1.f + __expf(-v[j]));
+                    }
+                } else {
+                    float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < NI; j++) key[j] = l + L * j < Ne ? order_key(biased ? c[j] : x.v[j]) : 0u;
-        if constexpr (GROUPS) {
-            float *choice = reinterpret_cast<float *>(s_lds[q].choice), *group = reinterpret_cast<float *>(s_lds[q].group);
-            int g_of[NI];
+                    for (int j = 0; j < NI; j++) {
+                        c[j] = v[j] == -INFINITY ? 0.f : v[j] == top ? 1.f : __expf(v[j] - top);
+                        sum += c[j];
+                    }
+                    sum = team_sum<L>(sum);
+                    const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
+#pragma unroll
+                    for (int j = 0; j < NI; j++) c[j] *= inv;
+                    margin += 0x1p-18f * inv;
+                }
+#pragma unroll
+                for (int j = 0; j < NI; j++) c[j] = v[j] == -INFINITY ? -INFINITY : c[j] + bias[j];
+            }
+            uint32_t key[NI], rev[NI];  // rev: 256 - e, larger for the lower index
 #pragma unroll
             for (int j = 0; j < NI; j++) {
-                const int p = l + L * j;
-                g_of[j] = p * a.over_n >> 16;
-                if (p < Ne) choice[p + g_of[j]] = c[j];
+                const bool in = l + L * j < Ne;
+                key[j] = in ? order_key(BIASED ? c[j] : v[j]) : 0u;
+                rev[j] = in ? 256u - e_of[j] : 0u;
             }
-            wave_sync();
-            group_scores<L>(choice, Nd, n, a.group_best, [&](int g, float v) {
-                if (g < Nd) group[g] = v;
-            });
-            wave_sync();
-            uint64_t allowed = 0;
-            for (int g0 = 0; g0 < Nd; g0 += L) {
-                const float v = g0 + l < Nd ? group[g0 + l] : -INFINITY;
-                const float off = 2.f * kMargin * (1.f + fabsf(v));
-                int ahead = 0, near = 0;  // surely; perhaps
-                for (int o = 0; o < Nd; o++) {
-                    const float y = group[o];
-                    ahead += y - v > off;
-                    near += !(v - y > off) && o != g0 + l;
+            if constexpr (GROUPS) {
+                GroupLds<L, NI> &lds = s_lds[wv].team[team];
+#pragma unroll
+                for (int j = 0; j < NI; j++) {
+                    const int p = l + L * j;
+                    if (p < Ne) lds.key[p + g_of[j]] = BIASED ? key[j] : order_key(c[j]);
                 }
-                const bool in = near < a.top_groups, out = ahead >= a.top_groups;
-                sure = sure && (g0 + l >= Nd || in || out);
-                allowed |= team_ballot<L>(in && g0 + l < Nd) << g0;
+                wave_sync();
+                int shift;
+                const uint64_t kept = keep_groups<L>(lds.key, lds.group, a, margin, shift, sure);
+#pragma unroll
+                for (int j = 0; j < NI; j++)
+                    if (!(kept >> (g_of[j] << shift) & 1)) key[j] = 0;
             }
-            sure = team_ballot<L>(!sure) == 0;
-#pragma unroll
-            for (int j = 0; j < NI; j++)
-                if (!(allowed >> g_of[j] & 1)) key[j] = 0;
-        }
-        // one more than k where the choice's border has to be looked at
-        const int rounds = biased ? k + 1 : k;
-        for (int i = 0; i < rounds; i++) {
-            uint32_t best = key[0];
-#pragma unroll
-            for (int j = 1; j < NI; j++) best = max(best, key[j]);
-            best = team_max<L>(best);
-            uint32_t low = 0;  // the lowest expert that has it, as 256 - e
-#pragma unroll
-            for (int j = NI - 1; j >= 0; j--) low = key[j] == best ? max(low, 256u - x.e[j]) : low;
-            const uint64_t with = team_ballot<L>(low != 0);
-            // (wave-uniform: a lane alone has it in every team, as nearly always)
-            if (__ballot((with & (with - 1)) != 0)) low = low == team_max<L>(low) ? low : 0;
-#pragma unroll
-            for (int j = 0; j < NI; j++)
-                if (low && key[j] == best && 256u - x.e[j] == low) {
-                    key[j] = 0;
-                    s_ids[q][i] = x.e[j];
-                    s_v[q][i] = x.v[j];
-                    if (biased) {
-                        s_b[q][i] = x.b[j];
-                        s_c[q][i] = best ? c[j] : -INFINITY;
+            // one more than k where the choice's border has to be looked at
+            const int rounds = BIASED ? k + 1 : k;
+            if constexpr (L == 64) {
+                sure = few_best<NI, false>(key, rev, nullptr, rounds, s_best[wv], nullptr, chosen) && sure;
+            } else {
+                // the lane's experts, the best first
+                const auto order = [&](int i, int j) {
+                    const bool swap = key[j] > key[i] || (key[j] == key[i] && rev[j] > rev[i]);
+                    const uint32_t k0 = key[i], r0 = rev[i];
+                    key[i] = swap ? key[j] : k0;
+                    rev[i] = swap ? rev[j] : r0;
+                    key[j] = swap ? k0 : key[j];
+                    rev[j] = swap ? r0 : rev[j];
+                };
+                if constexpr (NI == 2) order(0, 1);
+                if constexpr (NI == 4) {
+                    order(0, 1);
+                    order(2, 3);
+                    order(0, 2);
+                    order(1, 3);
+                    order(1, 2);
+                }
+                for (int i = 0; i < rounds; i++) {
+                    const uint32_t best = team_max<L>(key[0]);
+                    bool has = key[0] == best;
+                    const uint64_t with = team_ballot<L>(has);
+                    if (__ballot((with & (with - 1)) != 0)) {  // ties, in any team of the wave
+                        const uint32_t low = team_max<L>(has ? rev[0] : 0u);
+                        has = has && rev[0] == low;
                     }
+                    if (has) chosen[i] = Chosen{256 - static_cast<int>(rev[0]), best};
+#pragma unroll
+                    for (int j = 0; j + 1 < NI; j++) {
+                        key[j] = has ? key[j + 1] : key[j];
+                        rev[j] = has ? rev[j + 1] : rev[j];
+                    }
+                    key[NI - 1] = has ? 0u : key[NI - 1];
                 }
+            }
+            if (DOUBT && l == 0) s_margin[wv][q] = sure ? margin : INFINITY;
+            if (full) {
+                double sum = 0.;
+#pragma unroll
+                for (int j = 0; j < NI; j++) sum += exp_over(v[j], top);
+                sum = team_reduce<L>(sum, [](double y, double z) { return y + z; });
+                if (l == 0) {
+                    s_sum[wv][q] = sum;
+                    s_top[wv][q] = top;
+                }
+            }
         }
         wave_sync();
-        if (biased) {
+        const int r = lane % W, q = lane / W;
+        const size_t t = t0 + q;
+        const bool live = q < a.per_wave && t < T;
+        // The choices that are not sure, found 16 lanes a token.
+        if constexpr (DOUBT) {
+            const float margin = live ? s_margin[wv][q] : 0.f;
+            bool sure = margin < INFINITY;
+            if (BIASED && sure && live) {
 #pragma unroll
-            for (int i = 0; i < KPL; i++) {
-                const int o = l + L * i + 1;  // against the one in front
-                if (o <= k) {
-                    const float c0 = s_c[q][o - 1], c1 = s_c[q][o];
-                    const bool same = s_v[q][o - 1] == s_v[q][o] && s_b[q][o - 1] == s_b[q][o];
-                    if (c0 - c1 <= kMargin * (1.f + fabsf(c0)) && !same) sure = false;
+                for (int i = 0; i < KPL; i++) {
+                    const int o = r + W * i + 1;  // against the one in front
+                    if (o <= k) {
+                        const Chosen y = s_chosen[wv][q][o - 1], z = s_chosen[wv][q][o];
+                        const float cy = from_key(y.key), cz = z.key ? from_key(z.key) : -INFINITY;
+                        if (cy - cz <= margin * (1.f + fabsf(cy)))
+                            sure = sure && a.logits[t * Ne + y.e] == a.logits[t * Ne + z.e] && a.bias[y.e] == a.bias[z.e];
+                    }
                 }
             }
-        }
-        if (__ballot(!sure)) {
-            wave_sync();
-            choose64<L, NI, GROUPS>(a, x, s_lds[GROUPS ? q : 0], s_ids[q], s_v[q]);
-        }
-        // Renormalised, scores are taken over the largest that was chosen, so
-        // that none of them vanishes in the sum: softmax terms over its logit;
-        // sigmoids as they are but where all of them are below e^-600.
-        double s[KPL], sum = 0.;
-        float m = top;
-        if (a.renormalise) {
-            m = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < KPL; i++)
-                if (l + L * i < k) m = fmaxf(m, s_v[q][l + L * i]);
-            m = from_key(team_max<L>(order_key(m)));
-        }
-        const bool deep = a.sigmoid && a.renormalise && m < -600.f;
-#pragma unroll
-        for (int i = 0; i < KPL; i++) {
-            const float v = l + L * i < k ? s_v[q][l + L * i] : -INFINITY;
-            s[i] = a.sigmoid && !deep ? sigmoid64(v) : exp_over(v, m);
-            sum += s[i];
-        }
-        if (!a.renormalise) {
-            sum = 0.;
-            if (!a.sigmoid) {
-#pragma unroll
-                for (int j = 0; j < NI; j++) sum += exp_over(x.v[j], top);
+            if (const uint64_t unsure = __ballot(!sure)) {
+                wave_sync();
+                for (int i = 0; i < a.per_wave; i++)
+                    if (unsure >> (W * i) & 0xffff)
+                        choose64<(L * NI + kWave - 1) / kWave, GROUPS>(
+                            Choice{a.logits + (t0 + i) * Ne, a.bias, s_place, Ne, k, a.tab.n, a.tab.Nd, a.sigmoid, a.top_groups,
+                                   a.group_best},
+                            &s_lds[wv].all, s_best[wv], s_chosen[wv][i]);
             }
         }
-        if (a.renormalise || !a.sigmoid) sum = team_reduce<L>(sum, [](double y, double z) { return y + z; });
-        else sum = 1.;
-        const double over = sum > 0. ? sum : INFINITY;
+        // The weights.  Renormalised, scores are taken over the largest that
+        // was chosen, so that none of them vanishes in the sum: softmax terms
+        // over its logit; sigmoids as they are but where all of them are below
+        // e^-600.
+        float v[KPL], m = -INFINITY;
+        int e[KPL];
+#pragma unroll
+        for (int i = 0; i < KPL; i++) {
+            const int j = r + W * i;
+            e[i] = live && j < k ? s_chosen[wv][q][j].e : 0;
+            v[i] = live && j < k ? a.logits[t * Ne + e[i]] : -INFINITY;
+            if (v[i] != v[i]) v[i] = -INFINITY;
+        }
+        if (a.renormalise) {
+#pragma unroll
+            for (int i = 0; i < KPL; i++) m = fmaxf(m, v[i]);
+            m = group_max<W>(m);
+        } else if (full && live) {
+            m = s_top[wv][q];
+        }
+        const bool deep = a.sigmoid && a.renormalise && m < -600.f;
+        double s[KPL], sum = 0.;
+#pragma unroll
+        for (int i = 0; i < KPL; i++) {
+            s[i] = 0.;
+            if (i * W < k) {  // (wave-uniform)
+                s[i] = a.sigmoid && !deep ? sigmoid64(v[i]) : exp_over(v[i], m);
+                sum += s[i];
+            }
+        }
+        if (a.renormalise) sum = team_reduce<W>(sum, [](double y, double z) { return y + z; });
+        else sum = full && live ? s_sum[wv][q] : 1.;
+        const double over = sum > 0. ? a.scale * over64(sum) : 0.;
 #pragma unroll
         for (int i = 0; i < KPL; i++)
-            if (live && l + L * i < k) {
-                a.ids[t * k + l + L * i] = s_ids[q][l + L * i];
-                a.w[t * k + l + L * i] = static_cast<float>(a.scale * (s[i] / over));
+            if (live && r + W * i < k) {
+                a.ids[t * k + r + W * i] = e[i];
+                a.w[t * k + r + W * i] = static_cast<float>(over * s[i]);
             }
         wave_sync();
     }
@@ -599,9 +853,12 @@ hipError_t launch_route_scored(const ScoreArgs &a, hipStream_t s) {
     for (int p = 0; groups && p < a.Ne; p++) b.in_order = b.in_order && a.tab.expert[p] == p;
 #define OCC_SCORED(L, NI)                                                              \
     do {                                                                               \
-        const unsigned grid = std::min(ceil_div(a.T, kScoreThreads / L), kScoreGrid);   \
-        if (groups) k_route_scored<L, NI, true><<<grid, kScoreThreads, 0, s>>>(b);     \
-        else k_route_scored<L, NI, false><<<grid, kScoreThreads, 0, s>>>(b);           \
+        b.per_wave = L == 16 || a.T >= kScoreSerial ? 4 : 1;                            \
+        const unsigned grid = std::min(ceil_div(a.T, kScoreThreads / kWave * b.per_wave), kScoreGrid); \
+        if (groups && a.bias) k_route_scored<L, NI, true, true><<<grid, kScoreThreads, 0, s>>>(b);  \
+        else if (groups) k_route_scored<L, NI, true, false><<<grid, kScoreThreads, 0, s>>>(b);      \
+        else if (a.bias) k_route_scored<L, NI, false, true><<<grid, kScoreThreads, 0, s>>>(b);      \
+        else k_route_scored<L, NI, false, false><<<grid, kScoreThreads, 0, s>>>(b);                 \
     } while (0)
     if (a.Ne <= 16) OCC_SCORED(16, 1);
     else if (a.Ne <= 32) OCC_SCORED(16, 2);
