@@ -23,14 +23,15 @@ constexpr int kPlaceThreads = 256;
 
 // A token's experts, safe: one that is out of range or repeats an earlier one
 // becomes the lowest not yet used, with weight 0 (as launch_sanitize_ids).
-// f(j, expert, weight) for each slot; kAhead entries are loaded at once.
+// f(j, expert, weight) for each slot; kAhead entries are loaded at once.  ONCE:
+// there are no more (k <= kAhead), so that j is a constant where f is inlined.
 constexpr int kAhead = 8;
-template <typename F>
+template <bool ONCE = false, typename F>
 __device__ __forceinline__ void for_slots(const int32_t *__restrict__ ids, const float *__restrict__ w,
                                           size_t t, int k, int Ne, F f) {
     const size_t o = t * k;
     uint64_t u0 = 0, u1 = 0, u2 = 0, u3 = 0;
-    for (int j0 = 0; j0 < k; j0 += kAhead) {
+    for (int j0 = 0; j0 < (ONCE ? 1 : k); j0 += kAhead) {
         int e_in[kAhead];
         float w_in[kAhead];
 #pragma unroll
@@ -54,7 +55,7 @@ __device__ __forceinline__ void for_slots(const int32_t *__restrict__ ids, const
             u1 |= to >> 6 == 1 ? bit : 0;
             u2 |= to >> 6 == 2 ? bit : 0;
             u3 |= to >> 6 == 3 ? bit : 0;
-            if (j0 + j < k) f(j0 + j, to, good ? w_in[j] : 0.f);
+            if (j0 + j < k) f(ONCE ? j : j0 + j, to, good ? w_in[j] : 0.f);
         }
     }
 }
@@ -123,12 +124,37 @@ __global__ __launch_bounds__(kSlotsSmall) void k_slots_small(SlotArgs a) {
     load_places(a.tab, s_pos);
     __syncthreads();
     const int t = threadIdx.x;
-    if (t < a.T)
-        for_slots(a.ids, nullptr, t, a.k, a.tab.Ne, [&](int, int e, float) { atomicAdd(s_rows + s_pos[e], 1); });
+    // Up to kAhead slots a token stay in registers, each with its position in
+    // the placement and its count so far, its row's place in the segment.
+    const bool held = a.k <= kAhead;
+    int pos[kAhead], rank[kAhead];
+    float w[kAhead];
+    if (t < a.T) {
+        if (held)
+            for_slots<true>(a.ids, a.w, t, a.k, a.tab.Ne, [&](int j, int e, float wj) {
+                pos[j] = s_pos[e];
+                rank[j] = atomicAdd(s_rows + pos[j], 1);
+                w[j] = wj;
+            });
+        else
+            for_slots(a.ids, nullptr, t, a.k, a.tab.Ne, [&](int, int e, float) { atomicAdd(s_rows + s_pos[e], 1); });
+    }
     __syncthreads();
     if (threadIdx.x < kWave) segments(s_rows, s_tiles, a, s_next, true);
     __syncthreads();
-    if (t < a.T) place_token(a, t, s_pos, s_next);
+    if (t >= a.T) return;
+    if (!held) {
+        place_token(a, t, s_pos, s_next);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; j++) {
+        if (j >= a.k) continue;
+        const int row = s_next[pos[j]] + rank[j];
+        a.tok_epd[static_cast<size_t>(t) * a.k + j] = row;
+        a.epd_tok[row] = t;
+        a.epd_w[row] = w[j];
+    }
 }
 
 template <int NV>
