@@ -47,12 +47,6 @@ __device__ __forceinline__ float from_key(uint32_t k) {
     return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);
 }
 
-// LDS written by some lanes of a wave and read by others of it.
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 template <int L>
 __device__ __forceinline__ uint32_t team_max(uint32_t v) {
     const auto larger = [](uint32_t x, uint32_t y) { return max(x, y); };
@@ -283,7 +277,10 @@ __device__ __attribute__((noinline)) void choose64(Choice a, ChoiceLds *lds, Can
         for (int j = 0; j < NI; j++) c[j] = sum > 0. ? c[j] * over64(sum) : 0.;
     }
 #pragma unroll
-    for (int j = 0; j < NI; j++) c[j] = x.v[j] == -INFINITY ? -INFINITY : c[j] + x.b[j];
+    for (int j = 0; j < NI; j++) {
+        c[j] += x.b[j];
+        if (x.v[j] == -INFINITY || c[j] != c[j]) c[j] = -INFINITY;
+    }
     uint64_t allowed = ~0ull;
     if constexpr (GROUPS) {
 #pragma unroll
@@ -467,7 +464,7 @@ __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) 
         const int p = min(l + L * j, Ne - 1);
         e_of[j] = GROUPS ? s_place[p] : p;
         bias[j] = BIASED ? a.bias[e_of[j]] : 0.f;
-        g_of[j] = GROUPS ? (l + L * j) * a.over_n >> 16 : 0;
+        g_of[j] = GROUPS ? p * a.over_n >> 16 : 0;
     }
     const size_t T = a.T, step = static_cast<size_t>(gridDim.x) * WAVES * a.per_wave;
     for (size_t t0 = (static_cast<size_t>(blockIdx.x) * WAVES + wv) * a.per_wave; t0 < T; t0 += step) {
@@ -606,8 +603,9 @@ __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) 
                     const int o = r + W * i + 1;  // against the one in front
                     if (o <= k) {
                         const Chosen y = s_chosen[wv][q][o - 1], z = s_chosen[wv][q][o];
-                        const float cy = from_key(y.key), cz = z.key ? from_key(z.key) : -INFINITY;
-                        if (cy - cz <= margin * (1.f + fabsf(cy)))
+                        const float cy = from_key(y.key), cz = from_key(z.key);
+                        // (the k-th may be the last: key 0 and no expert behind it)
+                        if (z.key != 0 && cy - cz <= margin * (1.f + fabsf(cy)))
                             sure = sure && a.logits[t * Ne + y.e] == a.logits[t * Ne + z.e] && a.bias[y.e] == a.bias[z.e];
                     }
                 }

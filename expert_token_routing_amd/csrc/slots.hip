@@ -67,9 +67,9 @@ __device__ void segments(const int *rows, int *tiles, const SlotArgs &a, int *st
     const int lane = lane_id(), Ne = a.tab.Ne;
     if (schedule) {
         for (int p = lane; p < Ne; p += kWave) tiles[p] = (rows[p] + a.tile_rows - 1) / a.tile_rows;
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (a.fill_cols > 0) fill_rounds(rows, tiles, Ne, a.fill_cols, a.cus, kBrimMaxFill);
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
     }
     int run = 0, run_t = 0;
     for (int p0 = 0; p0 < Ne; p0 += kWave) {

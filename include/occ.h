@@ -654,7 +654,9 @@ typedef struct occ_score_desc {
  *              and it comes behind every other one (the ids stay distinct); a
  *              group is scored by the experts that are not left out.  A token
  *              whose chosen experts are all left out has weights of 0.
- *   bias       Ne fp32, or NULL.
+ *   bias       Ne fp32, or NULL.  -inf or NaN: the expert is chosen behind every
+ *              other one and scores for no group, as one that is left out, but
+ *              its weight is its score's.
  *   placement_host  as for occ_route; may be NULL when top_groups is Nd.
  *   ids (out)  T x k int32.   w (out)  T x k fp32. */
 occ_status occ_route_scored(const occ_layer_desc *desc, const occ_score_desc *opt,

@@ -144,6 +144,32 @@ def test_route_masked_experts_and_empty_rows(kind, Ne, Nd):
 
 
 @pytest.mark.parametrize("kind", [ref.SOFTMAX, ref.SIGMOID], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("Ne,Nd,k,top", [(8, 2, 8, 2), (64, 8, 8, 1), (64, 8, 16, 2), (16, 1, 16, 1),
+                                         (192, 8, 24, 1), (192, 8, 6, 3), (256, 8, 32, 1)])
+def test_route_biases_that_are_not_finite(Ne, Nd, k, top, kind):
+    """Infinite biases tie by index, also where the chosen are all that there are and nothing
+    stands behind the last; -inf and NaN come last and score for no group."""
+    g = torch.Generator().manual_seed(11)
+    logits = torch.randn(20, Ne, generator=g)
+    logits[3, ::2] = -INF
+    place = placement(Ne, Nd, seed=12)
+    bias = torch.full((Ne,), INF)
+    check_route(logits, bias, place, k, options(kind, top))
+    check_route(logits, -bias, place, k, options(kind, Nd))
+    logits = torch.randn(20, Ne, generator=g)
+    bias = torch.randn(Ne, generator=g) * 0.1
+    for row in place:  # one of each in a group
+        bias[int(row[0])], bias[int(row[1])], bias[int(row[2])] = INF, -INF, NAN
+    # the reference sums a group's best two over every expert that is not left out: at least two
+    # are finite or +inf, so that a -inf never enters
+    seen = torch.where(bias == bias, bias, torch.full_like(bias, -INF))
+    for best in (1, 2):
+        got = run_route(logits, bias, place, k, options(kind, top, best), Nd)
+        want = check_route(logits, seen, place, k, options(kind, top, best))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("kind", [ref.SOFTMAX, ref.SIGMOID], ids=["softmax", "sigmoid"])
 def test_route_saturated_and_vanishing_scores(kind):
     """Without a bias the logits order experts whose scores are equal in 64 bits; scores down to
     e^-700 still share out their weights."""
