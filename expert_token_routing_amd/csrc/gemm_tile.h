@@ -72,7 +72,7 @@ constexpr int CHUNKS = BK / 8;           // 16-byte chunks per LDS row
 constexpr int ROWS_PER_PASS = NT / CHUNKS;  // rows one pass of the workgroup moves
 constexpr int A_LD = (BM + ROWS_PER_PASS - 1) / ROWS_PER_PASS;
 constexpr int B_LD = BN / ROWS_PER_PASS;
-constexpr int STAGE = (BM + BN) * BK;    // bf16 elements per LDS buffer
+constexpr int STAGE = (BM + BN) * BK;    // 2-byte units per LDS buffer
 #ifndef OCC_GEMM_NSTAGE
 #define OCC_GEMM_NSTAGE 2
 #endif

