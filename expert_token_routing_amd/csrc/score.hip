@@ -28,6 +28,13 @@ constexpr int kScoreThreads = 256;
 // 19.4 / 21.0 / 26.3 / 76 against 15.4 / 21.9 / 35.7 / 117; a single token 5.9
 // against 3.2.
 constexpr int kScoreSerial = 8192;
+// Tokens up to which 33 to 64 experts with groups or a bias take a wave a token,
+// one expert a lane: its steps are fewer where one token's chain is what a
+// launch waits for.  64 experts, top 8, in groups with a bias: 1 / 64 / 512 /
+// 2048 tokens 4.4 / 4.8 / 5.4 / 6.5 us against 5.8 / 6.3 / 7.0 / 7.8 with 16
+// lanes, 4096 even, 8192 15.4 against 9.1 to 11.  Without either, or with fewer
+// experts, within a tenth on both sides.
+constexpr int kScoreWide = 2048;
 constexpr unsigned kScoreGrid = 1 << 20;  // workgroups; more tokens loop
 
 // A double's place in the order of the doubles, above 0; NaN reads as -inf.
@@ -447,10 +454,10 @@ __device__ __forceinline__ uint64_t keep_groups(const uint32_t *key, float *s_gr
 // and a round is the team's largest head and the winner's next one; all lanes
 // of a wave take few_best.  A wave makes the choice of four tokens (16 lanes
 // each, or all lanes one token after another) and then forms their weights in
-// 64 bits, 16 lanes a token.  Up to 64 experts 16 lanes a token: at 512 / 8192
-// / 65536 tokens of 60 experts, top 4, 3.5 / 3.8 / 10.9 us against 3.7 / 7.0 /
-// 29.5 with 64, of 64 in groups with a bias, top 8, 6.3 / 9.1 / 32 against 8.6
-// / 15.4 / 58; a single token of the latter 5.7 against 4.4.  The 65536 tokens
+// 64 bits, 16 lanes a token.  Up to 64 experts 16 lanes a token (but see
+// kScoreWide): at 512 / 8192 / 65536 tokens of 60 experts, top 4, 3.5 / 3.8 /
+// 10.9 us against 3.7 / 7.0 / 29.5 with 64, 65536 of 64 in groups with a bias,
+// top 8, 32 against 58.  The 65536 tokens
 // of 60 experts read and write 18 MB (1.7 TB/s), 32768 of 256 in groups 36 MB
 // in 43 us (0.8 TB/s).
 template <int L, int NI, bool GROUPS, bool BIASED>
@@ -882,7 +889,13 @@ hipError_t launch_route_scored(const ScoreArgs &a, hipStream_t s) {
     } while (0)
     if (a.Ne <= 16) OCC_SCORED(16, 1);
     else if (a.Ne <= 32) OCC_SCORED(16, 2);
-    else if (a.Ne <= 64) OCC_SCORED(16, 4);
+    else if (a.Ne <= 64 && a.T <= kScoreWide && (groups || a.bias)) {
+        b.per_wave = 1;
+        const unsigned grid = std::min(ceil_div(a.T, kScoreThreads / kWave), kScoreGrid);
+        if (groups && a.bias) k_route_scored<64, 1, true, true><<<grid, kScoreThreads, 0, s>>>(b);
+        else if (groups) k_route_scored<64, 1, true, false><<<grid, kScoreThreads, 0, s>>>(b);
+        else k_route_scored<64, 1, false, true><<<grid, kScoreThreads, 0, s>>>(b);
+    } else if (a.Ne <= 64) OCC_SCORED(16, 4);
     else if (a.Ne <= 128) OCC_SCORED(64, 2);
     else OCC_SCORED(64, 4);
 #undef OCC_SCORED

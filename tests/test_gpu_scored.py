@@ -180,6 +180,28 @@ def test_route_saturated_and_vanishing_scores(kind):
     assert torch.allclose(w.sum(1), torch.ones(3), atol=1e-6)
 
 
+@pytest.mark.parametrize("kind", [ref.SOFTMAX, ref.SIGMOID], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "biased"])
+@pytest.mark.parametrize("Ne,Nd,top", [(16, 4, 2), (48, 4, 4), (64, 8, 3), (120, 5, 5), (192, 8, 4)])
+def test_route_of_a_token_does_not_depend_on_its_batch(Ne, Nd, top, biased, kind):
+    """The same rows (of a normal, near ties, ties, masked, empty) in batches from one token to
+    those in which a wave takes several: the reference's choice and the same bits in each."""
+    g = torch.Generator().manual_seed(Ne)
+    n, k = 60, 4
+    rows = torch.randn(n, Ne, generator=g) * 2
+    rows[20:35] = 2 + torch.arange(Ne)[torch.randperm(Ne, generator=g)] * 2.0 ** -22
+    rows[35:45] = torch.randint(-1, 2, (10, Ne), generator=g).float()
+    rows[45:55][torch.rand(10, Ne, generator=g) < 0.5] = -INF
+    rows[55] = NAN
+    bias = 1 + torch.arange(Ne).float() * 2.0 ** -23 if biased else None
+    place, opt = placement(Ne, Nd, seed=1), options(kind, top, min(2, top), scale=1.5)
+    ids, w = check_route(rows, bias, place, k, opt)
+    for T in (1, 7, 2048, 2049, 8191, 8192, 8195):
+        at = torch.arange(T) % n
+        got_ids, got_w = run_route(rows[at], bias, place, k, opt, Nd)
+        assert torch.equal(got_ids, ids[at]) and torch.equal(got_w, w[at]), T
+
+
 def test_route_without_groups_needs_no_placement_and_repeats_bitwise():
     g = torch.Generator(device="cuda").manual_seed(5)
     T, Ne, k = 5000, 128, 8
