@@ -491,14 +491,22 @@ __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) 
     }
     const size_t T = a.T, step = static_cast<size_t>(gridDim.x) * WAVES * a.per_wave;
     for (size_t t0 = (static_cast<size_t>(blockIdx.x) * WAVES + wv) * a.per_wave; t0 < T; t0 += step) {
+        float ahead[NI];  // the token's row; where a wave takes several, loaded while the
+                          // one before is in work (4 to 6% from 32768 tokens on)
+        const auto load = [&](int q) {
+            const float *row = a.logits + min(t0 + q, T - 1) * Ne;  // (behind the last one: again, and not written)
+#pragma unroll
+            for (int j = 0; j < NI; j++) ahead[j] = row[e_of[j]];
+        };
+        if constexpr (L == kWave) load(0);
         for (int it = 0; it < a.per_wave; it += TEAMS) {
             const int q = it + team;
-            const size_t t = min(t0 + q, T - 1);  // (behind the last one: again, and not written)
-            const float *row = a.logits + t * Ne;
+            if constexpr (L < kWave) load(q);
             Chosen *chosen = s_chosen[wv][q];
             float v[NI];
 #pragma unroll
-            for (int j = 0; j < NI; j++) v[j] = row[e_of[j]];
+            for (int j = 0; j < NI; j++) v[j] = ahead[j];
+            if (L == kWave && it + 1 < a.per_wave) load(it + 1);
 #pragma unroll
             for (int j = 0; j < NI; j++)
                 if (!(l + L * j < Ne) || v[j] != v[j]) v[j] = -INFINITY;
