@@ -13,7 +13,7 @@
 // fragment 16, and the int8 instruction multiplies 64 bytes of K in the
 // cycles that the bf16 one does.  Half the bytes and half the instructions a
 // product.  Measured (d = 2048, 64 experts of F = 1024, top 8, 320-row tiles):
-// 8192 tokens up 291 us, down 187 (1.89 and 1.47 POP/s, against 2.04 of a plain
+// 8192 tokens up 298 us, down 190 (1.84 and 1.45 POP/s, against 2.04 of a plain
 // 8192 x 8192 x 8192 int8 product), bound by the matrix cores and, in the
 // down-projection, the epilogue's stores; 512 tokens on 80-row tiles 64 and 39
 // us for 282 and 141 MB of weights and rows (4.4 and 3.6 TB/s), bound by memory.  K need only be a multiple of 64: rows of codes are padded with

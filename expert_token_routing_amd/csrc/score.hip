@@ -23,9 +23,9 @@ namespace {
 constexpr int kScoreThreads = 256;
 // Tokens from which a wave of 64 lanes a token takes four one after another, so
 // that their weights in 64 bits fill its lanes once: at 4096 / 8192 / 16384 /
-// 65536 tokens of 128 experts (top 8, no bias) 6.7 / 7.5 / 9.6 / 32.7 us
+// 65536 tokens of 128 experts (top 8, no bias) 6.7 / 7.3 / 9.5 / 30.8 us
 // against 5.0 / 8.0 / 13.8 / 50.9 one at a time, of 256 in groups (top 8, bias)
-// 19.4 / 21.0 / 26.3 / 76 against 15.4 / 21.9 / 35.7 / 117; a single token 5.9
+// 19.4 / 20.8 / 26 / 72 against 15.4 / 21.9 / 35.7 / 117; a single token 5.9
 // against 3.2.
 constexpr int kScoreSerial = 8192;
 // Tokens up to which 33 to 64 experts with groups or a bias take a wave a token,
@@ -459,7 +459,7 @@ __device__ __forceinline__ uint64_t keep_groups(const uint32_t *key, float *s_gr
 // 10.9 us against 3.7 / 7.0 / 29.5 with 64, 65536 of 64 in groups with a bias,
 // top 8, 32 against 58.  The 65536 tokens
 // of 60 experts read and write 18 MB (1.7 TB/s), 32768 of 256 in groups 36 MB
-// in 43 us (0.8 TB/s).
+// in 42 us (0.8 TB/s).
 template <int L, int NI, bool GROUPS, bool BIASED>
 __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) {
     constexpr int TEAMS = kWave / L, WAVES = kScoreThreads / kWave, TOK = 4, W = 16, KPL = kMaxK / W;
