@@ -187,14 +187,16 @@ struct Chosen {
 // larger rev = 256 - e).  A key that between `need` and kMoreHeads more lanes'
 // largest ones reach, bit by bit by ballots; then every expert that reaches it,
 // one a lane through LDS, counts those ahead of it.  False where that is more
-// than a wave of experts or the lanes with any are fewer than `need`.
+// than a wave of experts or the lanes with any are fewer than `need`.  `tie`
+// (by key alone, need >= 2): whether the last two have one key.
 constexpr int kMoreHeads = 3;
 struct alignas(8) Candidate {
     uint32_t rev, key;
 };
 template <int NI, bool FINE>
 __device__ __forceinline__ bool few_best(const uint32_t (&key)[NI], const uint32_t (&rev)[NI], const uint64_t *fine,
-                                         int need, Candidate *best, uint64_t *best_fine, Chosen *chosen) {
+                                         int need, Candidate *best, uint64_t *best_fine, Chosen *chosen,
+                                         bool *tie = nullptr) {
     uint32_t head = key[0];
 #pragma unroll
     for (int j = 1; j < NI; j++) head = max(head, key[j]);
@@ -245,7 +247,31 @@ __device__ __forceinline__ bool few_best(const uint32_t (&key)[NI], const uint32
         }
     }
     if (lane < n && rank < need) chosen[rank] = Chosen{256 - static_cast<int>(mine.rev), mine.key};
+    if (tie) {
+        const auto at = [&](int r) { return __builtin_ctzll(__ballot(lane < n && rank == r)); };
+        *tie = __builtin_amdgcn_readlane(static_cast<int>(mine.key), at(need - 1)) ==
+               __builtin_amdgcn_readlane(static_cast<int>(mine.key), at(need - 2));
+    }
     return true;
+}
+
+// Where the first expert that is not chosen (`last`) is an exact tie of the last
+// chosen one, of one logit and bias, that pair is in order but says nothing of
+// what stands behind it: whether an expert that is no such tie lies within the
+// margin of theirs, so that 64 bits may put it in front.  `key` and `rev` hold
+// the experts that are left, or all of them.
+template <int L, int NI>
+__device__ __forceinline__ bool hidden_behind(const uint32_t (&key)[NI], const uint32_t (&rev)[NI], Chosen last,
+                                              const float *row, const float *bias, float margin) {
+    const float c = from_key(last.key), off = margin * (1.f + fabsf(c)), v = row[last.e], b = bias[last.e];
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < NI; j++)
+        if (key[j] != 0 && key[j] <= last.key && c - from_key(key[j]) <= off) {
+            const int e = 256 - static_cast<int>(rev[j]);
+            any = any || row[e] != v || bias[e] != b;
+        }
+    return team_ballot<L>(any) != 0;
 }
 
 // The choice in 64 bits throughout, for the tokens whose choice 32 bits cannot
@@ -446,8 +472,9 @@ __device__ __forceinline__ uint64_t keep_groups(const uint32_t *key, float *s_gr
 // thousands.  Scores in 32 bits are off by less than half of a margin, so a
 // choice whose neighbours (the chosen, the first not chosen, the groups at
 // their border) lie further apart is the one that 64 bits make; logits alone
-// order without an error, and experts of equal logit and bias tie in both.  The
-// tokens that are left take choose64.
+// order without an error, and experts of equal logit and bias tie in both; where
+// they tie across the border of the chosen, the experts behind them count (by
+// hidden_behind).  The tokens that are left take choose64.
 //
 // Bound by instructions, but for few tokens, where the launch and its chain of
 // dependent steps count.  With 16 lanes a token a lane sorts its experts once,
@@ -571,8 +598,16 @@ __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) 
             }
             // one more than k where the choice's border has to be looked at
             const int rounds = BIASED ? k + 1 : k;
+            const auto hidden = [&] {
+                return hidden_behind<L, NI>(key, rev, chosen[k], a.logits + min(t0 + q, T - 1) * Ne, a.bias, margin);
+            };
             if constexpr (L == 64) {
-                sure = few_best<NI, false>(key, rev, nullptr, rounds, s_best[wv], nullptr, chosen) && sure;
+                bool tie = false;
+                sure = few_best<NI, false>(key, rev, nullptr, rounds, s_best[wv], nullptr, chosen, BIASED ? &tie : nullptr) && sure;
+                if (BIASED && tie) {
+                    wave_sync();
+                    sure = !hidden() && sure;
+                }
             } else {
                 // the lane's experts, the best first
                 const auto order = [&](int i, int j) {
@@ -606,6 +641,14 @@ __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) 
                         rev[j] = has ? rev[j + 1] : rev[j];
                     }
                     key[NI - 1] = has ? 0u : key[NI - 1];
+                }
+                if constexpr (BIASED) {
+                    wave_sync();
+                    const bool tie = chosen[k].key == chosen[k - 1].key && chosen[k].key != 0;
+                    if (__ballot(tie)) {
+                        const bool h = hidden();
+                        sure = sure && !(tie && h);
+                    }
                 }
             }
             if (DOUBT && l == 0) s_margin[wv][q] = sure ? margin : INFINITY;

@@ -230,6 +230,52 @@ def test_route_softmax_is_the_layers_own_route_when_plain():
     assert torch.equal(a, b) and ((wa - wb).abs() <= 1e-6 * wb + 2.0 ** -149).all()
 
 
+# ----------------------------------------------- borders that 32 bits cannot tell
+
+# experts, groups, kept groups, tokens: 16 lanes with 1, 2 and 4 experts each, a wave with 1, 2 and 4
+BORDERS = [(3, 1, 1, 40), (4, 2, 2, 40), (16, 4, 2, 40), (32, 4, 4, 40), (32, 8, 3, 40),
+           (64, 8, 8, 2100), (64, 8, 3, 2100), (64, 8, 8, 40), (64, 8, 3, 40), (128, 8, 8, 40),
+           (128, 8, 3, 40), (256, 16, 16, 40), (256, 16, 4, 40), (256, 16, 4, 8200)]
+
+
+def border_rows(Ne, seed):
+    """Exact ties beside neighbours that 32 bits place level with them: saturated sigmoids, terms of
+    a peaked softmax, neighbours of a few steps of fp32, logits rounded to bf16.  None above 28, where
+    a sigmoid's own 64 bits still tell a step of bf16 apart (e^-28 / 8 is a hundred of their steps)."""
+    g = torch.Generator().manual_seed(seed)
+    rows = []
+    for head in ([20., 20., 21.], [18., 18., 18.125], [0., -110., -110., -105.], [25., 24.75, 24.75, 25.]):
+        for low in (-30., -120.):
+            row = torch.full((Ne,), low)
+            row[:min(len(head), Ne)] = torch.tensor(head[:Ne])
+            rows += [row, row[torch.randperm(Ne, generator=g)], row.flip(0)]
+    for _ in range(8):
+        near = 2 + torch.randint(0, 8, (Ne,), generator=g) * 2.0 ** -22
+        rows += [near, near - 3, torch.randint(128, 161, (Ne,), generator=g) / 8.0]
+    for size in (1.0, 4.0, 8.0, 8.0):
+        rows += list((torch.randn(8, Ne, generator=g) * size).to(BF16).float().clamp(max=28))
+    return torch.stack(rows)
+
+
+@pytest.mark.parametrize("kind", [ref.SOFTMAX, ref.SIGMOID], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("Ne,Nd,top,T", BORDERS)
+def test_route_ties_at_the_border_hide_no_better_expert(Ne, Nd, top, T, kind):
+    rows = border_rows(Ne, Ne + top)
+    at = torch.arange(max(T, rows.shape[0])) % rows.shape[0]
+    place = placement(Ne, Nd, seed=2)
+    for bias in (torch.zeros(Ne), torch.full((Ne,), 0.5), (torch.arange(Ne) % 3) * 2.0 ** -23):
+        for k in (1, 2, 3, 8):
+            if k > top * (Ne // Nd):
+                continue
+            opt = options(kind, top, 1)
+            ids, w = ref.route(rows, bias, place, k, kind, top, 1, 1, 1.0)
+            got_ids, got_w = run_route(rows[at], bias, place, k, opt, Nd)
+            wrong = (got_ids != ids[at]).any(1)
+            assert not wrong.any(), (k, int(wrong.sum()), rows[at][wrong][0], got_ids[wrong][0],
+                                     ids[at][wrong][0])
+            assert ((got_w - w[at]).abs() <= half_step(F32) * w[at].abs() * (1 + 1e-6) + 2.0 ** -149).all()
+
+
 # ------------------------------------------------------------------- gradient
 
 def run_back(logits, ids, dw, dlogits_in, opt, alias=None):
