@@ -98,15 +98,18 @@ struct GroupWalk {
 
 // LDS of a wave in choose64: the choice by place (a group's places together,
 // groups n + 1 apart: other banks) and the groups' scores; of a team in
-// keep_groups the same in 32 bits.
+// keep_groups the same in 32 bits, with how far off a score may be.
 struct ChoiceLds {
     double choice[kMaxNe + kMaxNd];
     double group[kMaxNd];
 };
+struct alignas(8) GroupScore {
+    float v, err;
+};
 template <int L, int NI>
 struct GroupLds {
     uint32_t key[L * NI + kMaxNd];
-    float group[kMaxNd];
+    GroupScore group[kMaxNd];
 };
 
 // The best two of two pairs.
@@ -394,14 +397,17 @@ __device__ __attribute__((noinline)) void choose64(Choice a, ChoiceLds *lds, Can
 
 // The groups' scores from the order keys of c in LDS (as group_scores), and of
 // the kept groups: bit g << shift of the result; `sure` is whether the scores
-// at the border lie far enough apart.  Scores and their margins as floats.
+// at the border lie further apart than both may be off.  A sum's error goes by
+// its terms, which may cancel: margin / 2 (1 + |c|) of each, 2^-24 of the sum
+// besides, below margin (1 + |c1| + |c2|) together.  A group without an expert
+// is -inf exactly.
 template <int L>
-__device__ __forceinline__ uint64_t keep_groups(const uint32_t *key, float *s_group, const ScoreArgs &a,
+__device__ __forceinline__ uint64_t keep_groups(const uint32_t *key, GroupScore *s_group, const ScoreArgs &a,
                                                 float margin, int &shift, bool &sure) {
     const GroupWalk<L> walk(a.tab.Nd);
     const int l = threadIdx.x % L, Nd = a.tab.Nd, n = a.tab.n, GL = 1 << walk.shift;
     const int i = l & (GL - 1);
-    const auto score = [&](int g) {
+    const auto score = [&](int g) -> GroupScore {
         uint32_t top = 0, next = 0;
         const uint32_t *at = key + min(g, Nd - 1) * (n + 1);
         for (int j0 = 0; j0 < n; j0 += 4 * GL) {
@@ -427,14 +433,17 @@ __device__ __forceinline__ uint64_t keep_groups(const uint32_t *key, float *s_gr
         if (GL >= 64) join(__shfl_xor(top, 32), __shfl_xor(next, 32));
         // none left: -inf; one: no second
         const float ft = top ? from_key(top) : -INFINITY, fn = next ? from_key(next) : -INFINITY;
-        return a.group_best > 1 && fn > -INFINITY ? ft + fn : ft;
+        const bool both = a.group_best > 1 && fn > -INFINITY;
+        const float size = fabsf(ft) + (both ? fabsf(fn) : 0.f);
+        return GroupScore{both ? ft + fn : ft, ft > -INFINITY ? margin * (1.f + size) : 0.f};
     };
     uint64_t kept = 0;
     shift = 0;
     if (GL >= Nd) {  // (all groups at once) a group's lane i compares it with group i
         const int g = l >> walk.shift;
-        const float v = score(g), y = __shfl(v, i << walk.shift, L);
-        const float off = 2.f * margin * (1.f + fabsf(v));
+        const GroupScore own = score(g);
+        const float v = own.v, y = __shfl(v, i << walk.shift, L);
+        const float off = own.err + __shfl(own.err, i << walk.shift, L);
         const bool other = i < Nd && g < Nd && i != g;
         const uint64_t fields = GL >= 64 ? ~0ull : (1ull << GL) - 1;
         const int ahead = __popcll(team_ballot<L>(other && y - v > off) >> (g << walk.shift) & fields);
@@ -447,18 +456,19 @@ __device__ __forceinline__ uint64_t keep_groups(const uint32_t *key, float *s_gr
     }
     for (int g0 = 0; g0 < Nd; g0 += walk.per) {
         const int g = g0 + (l >> walk.shift);
-        const float v = score(g);
-        if (g < Nd && i == 0) s_group[g] = v;
+        const GroupScore own = score(g);
+        if (g < Nd && i == 0) s_group[g] = own;
     }
     wave_sync();
     for (int g0 = 0; g0 < Nd; g0 += L) {
         const int g = g0 + l;
-        const float v = g < Nd ? s_group[g] : -INFINITY, off = 2.f * margin * (1.f + fabsf(v));
+        const GroupScore own = s_group[min(g, Nd - 1)];
         int ahead = 0, near = 0;
         for (int o = 0; o < Nd; o++) {
-            const float y = s_group[o];
-            ahead += y - v > off;
-            near += !(v - y > off) && o != g;
+            const GroupScore y = s_group[o];
+            const float off = own.err + y.err;
+            ahead += y.v - own.v > off;
+            near += !(own.v - y.v > off) && o != g;
         }
         const bool in = near < a.top_groups, out = ahead >= a.top_groups;
         sure = sure && team_ballot<L>(g < Nd && !in && !out) == 0;

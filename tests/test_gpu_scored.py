@@ -276,6 +276,43 @@ def test_route_ties_at_the_border_hide_no_better_expert(Ne, Nd, top, T, kind):
             assert ((got_w - w[at]).abs() <= half_step(F32) * w[at].abs() * (1 + 1e-6) + 2.0 ** -149).all()
 
 
+@pytest.mark.parametrize("kind", [ref.SOFTMAX, ref.SIGMOID], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("Ne,Nd,top,T", [(16, 4, 2, 300), (16, 8, 3, 300), (32, 4, 1, 300),
+                                         (64, 8, 4, 300), (64, 8, 4, 2100), (64, 32, 9, 300),
+                                         (64, 32, 9, 2100), (128, 8, 4, 300), (128, 64, 20, 300),
+                                         (256, 8, 3, 300), (256, 64, 20, 300)])
+def test_route_groups_whose_best_two_cancel(Ne, Nd, top, T, kind):
+    """One expert of a group with a bias of B or more, the others with as much less: the sum of the
+    best two is near 0, its error is of B's size.  The groups lie some steps of B's fp32 apart."""
+    g = torch.Generator().manual_seed(Nd + top)
+    n, rows = Ne // Nd, 300
+    place = placement(Ne, Nd, seed=6)
+    for B in (1.0, 16.0, 64.0, 256.0, 1024.0, 65536.0):
+        # one row of logits in every group, each shifted by some 2^-23 B to 2^-17 B either way: a
+        # sum in fp32 may step up where its terms' rounded parts say down
+        base = torch.randn(rows, 1, n, generator=g)
+        size = B * 2.0 ** (torch.arange(rows) % 7 - 23)
+        shift = (torch.rand(rows, Nd, n, generator=g).double() * 2 - 1) * size[:, None, None]
+        logits, bias = torch.empty(rows, Ne), torch.empty(Ne)
+        logits[:, place.flatten()] = (base.double() + shift).float().reshape(rows, Ne)
+        # (of another size in each group: the chosen lie far apart, only the groups near)
+        of_group = B * (1 + torch.arange(Nd) / Nd)[:, None] * torch.tensor([1.0] + [-1.0] * (n - 1))
+        bias[place.flatten()] = of_group.flatten()
+        k = top
+        ids, w = ref.route(logits, bias, place, k, kind, top, 2, 1, 1.0)
+        at = torch.arange(T) % rows
+        got_ids, _ = run_route(logits[at], bias, place, k, options(kind, top, 2), Nd)
+        # Groups whose logits came out equal tie but for the roundings of s + bias, which 64 bits do
+        # not settle: scores within 2^-50 here and 2^-51 there, a sum rounded by 2^-53 (1 + 2 B), and
+        # four such sums at a border: below 2^-46 (1 + 2 B) together
+        c = (ref.scores(logits, kind) + bias.double())[:, place.flatten()].view(rows, Nd, n)
+        ranked = c.topk(2, dim=2).values.sum(2).sort(1, descending=True).values
+        told = ranked[:, top - 1] - ranked[:, top] > 2.0 ** -46 * (1 + 2 * B)
+        assert told.sum() >= 240
+        wrong = (got_ids != ids[at]).any(1) & told[at]
+        assert not wrong.any(), (B, int(wrong.sum()))
+
+
 # ------------------------------------------------------------------- gradient
 
 def run_back(logits, ids, dw, dlogits_in, opt, alias=None):
