@@ -243,7 +243,7 @@ struct ScoreArgs {
     PlaceTab tab;
     int32_t *ids;
     float *w;
-    int over_n, in_order, per_wave;  // set by the launcher
+    int over_n, in_order, per_wave, rounds;  // set by the launcher
 };
 hipError_t launch_route_scored(const ScoreArgs &a, hipStream_t s);
 hipError_t launch_route_scored_back(const float *logits, const int32_t *ids, const float *dw,

@@ -189,9 +189,10 @@ struct Chosen {
 // experts of one key; the same in all for none), then by the lower index (the
 // larger rev = 256 - e).  A key that between `need` and kMoreHeads more lanes'
 // largest ones reach, bit by bit by ballots; then every expert that reaches it,
-// one a lane through LDS, counts those ahead of it.  False where that is more
-// than a wave of experts or the lanes with any are fewer than `need`.  `tie`
-// (by key alone, need >= 2): whether the last two have one key.
+// one a lane through LDS, counts those ahead of it; all experts with a key where
+// they lie in fewer lanes than `need`.  False where that is more than a wave of
+// experts or fewer than `need`.  `tie` (by key alone): whether the last two have
+// one key.
 constexpr int kMoreHeads = 3;
 struct alignas(8) Candidate {
     uint32_t rev, key;
@@ -211,7 +212,7 @@ __device__ __forceinline__ bool few_best(const uint32_t (&key)[NI], const uint32
             if (n <= need + kMoreHeads) break;
         }
     }
-    if (reach == 0) return false;
+    reach = max(reach, 1u);
     int n = 0;
 #pragma unroll
     for (int j = 0; j < NI; j++) {
@@ -224,7 +225,7 @@ __device__ __forceinline__ bool few_best(const uint32_t (&key)[NI], const uint32
         }
         n += __popcll(in);
     }
-    if (n > kWave) return false;
+    if (n > kWave || n < need) return false;
     wave_sync();
     const int lane = lane_id();
     Candidate mine = best[lane];
@@ -252,8 +253,8 @@ __device__ __forceinline__ bool few_best(const uint32_t (&key)[NI], const uint32
     if (lane < n && rank < need) chosen[rank] = Chosen{256 - static_cast<int>(mine.rev), mine.key};
     if (tie) {
         const auto at = [&](int r) { return __builtin_ctzll(__ballot(lane < n && rank == r)); };
-        *tie = __builtin_amdgcn_readlane(static_cast<int>(mine.key), at(need - 1)) ==
-               __builtin_amdgcn_readlane(static_cast<int>(mine.key), at(need - 2));
+        *tie = need > 1 && __builtin_amdgcn_readlane(static_cast<int>(mine.key), at(need - 1)) ==
+                               __builtin_amdgcn_readlane(static_cast<int>(mine.key), at(need - 2));
     }
     return true;
 }
@@ -606,15 +607,14 @@ __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) 
                 for (int j = 0; j < NI; j++)
                     if (!(kept >> (g_of[j] << shift) & 1)) key[j] = 0;
             }
-            // one more than k where the choice's border has to be looked at
-            const int rounds = BIASED ? k + 1 : k;
+            const bool border = BIASED && a.rounds > k;
             const auto hidden = [&] {
                 return hidden_behind<L, NI>(key, rev, chosen[k], a.logits + min(t0 + q, T - 1) * Ne, a.bias, margin);
             };
             if constexpr (L == 64) {
                 bool tie = false;
-                sure = few_best<NI, false>(key, rev, nullptr, rounds, s_best[wv], nullptr, chosen, BIASED ? &tie : nullptr) && sure;
-                if (BIASED && tie) {
+                sure = few_best<NI, false>(key, rev, nullptr, a.rounds, s_best[wv], nullptr, chosen, BIASED ? &tie : nullptr) && sure;
+                if (border && tie) {
                     wave_sync();
                     sure = !hidden() && sure;
                 }
@@ -636,7 +636,7 @@ __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) 
                     order(1, 3);
                     order(1, 2);
                 }
-                for (int i = 0; i < rounds; i++) {
+                for (int i = 0; i < a.rounds; i++) {
                     const uint32_t best = team_max<L>(key[0]);
                     bool has = key[0] == best;
                     const uint64_t with = team_ballot<L>(has);
@@ -652,7 +652,7 @@ __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) 
                     }
                     key[NI - 1] = has ? 0u : key[NI - 1];
                 }
-                if constexpr (BIASED) {
+                if (border) {
                     wave_sync();
                     const bool tie = chosen[k].key == chosen[k - 1].key && chosen[k].key != 0;
                     if (__ballot(tie)) {
@@ -685,11 +685,10 @@ __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) 
 #pragma unroll
                 for (int i = 0; i < KPL; i++) {
                     const int o = r + W * i + 1;  // against the one in front
-                    if (o <= k) {
+                    if (o < a.rounds) {
                         const Chosen y = s_chosen[wv][q][o - 1], z = s_chosen[wv][q][o];
                         const float cy = from_key(y.key), cz = from_key(z.key);
-                        // (the k-th may be the last: key 0 and no expert behind it)
-                        if (z.key != 0 && cy - cz <= margin * (1.f + fabsf(cy)))
+                        if (cy - cz <= margin * (1.f + fabsf(cy)))
                             sure = sure && a.logits[t * Ne + y.e] == a.logits[t * Ne + z.e] && a.bias[y.e] == a.bias[z.e];
                     }
                 }
@@ -935,7 +934,10 @@ __global__ __launch_bounds__(kBiasThreads) void k_bias_step(const int32_t *__res
 
 hipError_t launch_route_scored(const ScoreArgs &a, hipStream_t s) {
     const bool groups = a.top_groups < a.tab.Nd;
+    const int kept = groups ? a.top_groups * a.tab.n : a.Ne;
     ScoreArgs b = a;
+    // one more than k where the choice has a border and that has to be looked at
+    b.rounds = a.bias ? std::min(a.k + 1, kept) : a.k;
     b.over_n = static_cast<int>(ceil_div(1 << 16, a.tab.n));  // p / n = p over_n >> 16 for p < 256
     b.in_order = 1;
     for (int p = 0; groups && p < a.Ne; p++) b.in_order = b.in_order && a.tab.expert[p] == p;

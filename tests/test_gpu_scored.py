@@ -313,6 +313,33 @@ def test_route_groups_whose_best_two_cancel(Ne, Nd, top, T, kind):
         assert not wrong.any(), (B, int(wrong.sum()))
 
 
+# experts, groups, kept groups, k: the kept groups hold the chosen and no other, or one more, or lie
+# on the lanes of a few (places a wave apart), in every lane layout
+KEPT = [(8, 2, 1, 4), (16, 4, 4, 16), (32, 4, 2, 16), (64, 8, 1, 8), (64, 8, 1, 7), (64, 1, 1, 32),
+        (128, 16, 2, 16), (128, 16, 2, 9), (128, 8, 1, 16), (256, 8, 1, 32), (256, 64, 4, 16),
+        (256, 32, 4, 31), (192, 24, 4, 32)]
+
+
+@pytest.mark.parametrize("kind", [ref.SOFTMAX, ref.SIGMOID], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("Ne,Nd,top,k", KEPT)
+def test_route_of_kept_groups_that_hold_little_more_than_the_chosen(Ne, Nd, top, k, kind):
+    g = torch.Generator().manual_seed(Ne + k)
+    rows = torch.randn(60, Ne, generator=g) * 2
+    rows[20:40] = 2 + torch.randint(0, 6, (20, Ne), generator=g) * 2.0 ** -22
+    rows[40:][torch.rand(20, Ne, generator=g) < 0.5] = -INF
+    place = placement(Ne, Nd, seed=7)
+    n = Ne // Nd
+    # (the best of every group in places 64 apart, so that they are kept together)
+    for shift in (0, 4.0):
+        rows[:, place.flatten()[torch.arange(Ne) % 64 < n]] += shift
+        for bias in (torch.randn(Ne, generator=g) * 0.1, 1 + torch.arange(Ne) * 2.0 ** -23, torch.zeros(Ne)):
+            opt = options(kind, top, min(2, n), scale=1.5)
+            ids, w = check_route(rows, bias, place, k, opt)
+            at = torch.arange(2100) % 60
+            got_ids, got_w = run_route(rows[at], bias, place, k, opt, Nd)
+            assert torch.equal(got_ids, ids[at]) and torch.equal(got_w, w[at])
+
+
 # ------------------------------------------------------------------- gradient
 
 def run_back(logits, ids, dw, dlogits_in, opt, alias=None):
