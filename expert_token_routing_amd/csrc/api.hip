@@ -396,6 +396,13 @@ struct Int8Layout {
 bool small_tiles8(const occ_layer_desc &D) {
     return static_cast<int64_t>(D.T) * D.k < static_cast<int64_t>(kSmallTileRows8) * D.Ne;
 }
+// The shared experts see every token, whatever a routed expert's share of them:
+// their products take the low tiles up to this many.  Layer with few routed
+// rows, 80-row / 320-row tiles (us): two of F_shared = 1408 (d = 2048) 128 / 140
+// at 1024 tokens, 144 / 150 at 1536, 168 / 158 at 2048, 234 / 197 at 4096; one of
+// 5632 94 / 101 at 768, 144 / 144 at 1024, 174 / 162 at 1536, 312 / 269 at 4096; one
+// of 1024 55 / 62, 95 / 101, 104 / 108, 139 / 131.
+constexpr int kSmallTileShared8 = 1536;
 int tile_rows8(const occ_layer_desc &D) { return small_tiles8(D) ? kGemmBmInt8Small : kGemmBmBf16; }
 int fill_cols8(const occ_layer_desc &D) { return small_tiles8(D) ? 0 : static_cast<int>(ceil_div(D.F, 128)); }
 
@@ -1431,9 +1438,11 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
         OCC_HIP(launch_few(f, s));
         return OCC_OK;
     }
-    const bool small = small_tiles8(D);
+    const bool small = small_tiles8(D), small_sh = D.T < kSmallTileShared8;
     const auto gemm_up = small ? launch_gemm_up8_m80 : launch_gemm_up8;
     const auto gemm_down = small ? launch_gemm_down8_m80 : launch_gemm_down8;
+    const auto gemm_up_sh = small_sh ? launch_gemm_up8_m80 : launch_gemm_up8;
+    const auto gemm_down_sh = small_sh ? launch_gemm_down8_m80 : launch_gemm_down8;
     const size_t routed_tiles = most_row_tiles8(D);
 
     // a token's row of codes is kept once and gathered by each of its experts
@@ -1473,7 +1482,7 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
         up.Ne = 1;
         up.lda = static_cast<int>(round_line(d));
         up.tab = tab;
-        OCC_HIP(gemm_up(up, 0, s));
+        OCC_HIP(gemm_up_sh(up, 0, s));
         OCC_HIP(launch_quantize_rows(h, 0, T, D.F_shared, hq, round_line(Fs), hs, s));
         Down8Args dn{};
         dn.A = hq;
@@ -1487,7 +1496,7 @@ occ_status occ_moe_forward_int8(const occ_layer_desc *desc, const void *x, const
         dn.Ne = 1;
         dn.lda = static_cast<int>(round_line(Fs));
         dn.tab = tab;
-        OCC_HIP(gemm_down(dn, 0, s));
+        OCC_HIP(gemm_down_sh(dn, 0, s));
     }
     Up8Args up{};
     up.A = xq;

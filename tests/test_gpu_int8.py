@@ -172,6 +172,22 @@ def test_layer(T, d, Ne, k, F, Nd, n_shared, F_shared):
     assert torch.equal(case.run(desc=desc, place=place), y)
 
 
+# the shared experts' rows by the tokens, the routed ones' by their share: either tile for each
+@pytest.mark.parametrize("T,d,Ne,k,F,Nd,n_shared,F_shared", [
+    (1535, 128, 64, 2, 64, 4, 1, 320), (1536, 128, 64, 2, 64, 4, 1, 320), (2100, 192, 256, 8, 64, 8, 2, 192),
+    (1535, 64, 4, 2, 128, 2, 1, 128), (1600, 64, 4, 2, 128, 2, 2, 64)])
+def test_layer_of_many_tokens_with_shared_experts(T, d, Ne, k, F, Nd, n_shared, F_shared):
+    case = Case(T, d, Ne, k, F, Nd, n_shared, F_shared, seed=T + Ne)
+    y = case.check()
+    # a part of the batch, on the other tiles: the same bits
+    desc = layer(700, d, Ne, k, F, Nd, n_shared, F_shared)
+    x, ids, w = (a[-700:].contiguous().cuda() for a in (case.x, case.ids, case.w))
+    part = torch.empty(700, d, dtype=BF16, device="cuda")
+    occ.occ_moe_forward_int8(desc, x, ids, w, case.place, on_gpu(case.experts), on_gpu(case.shared), part,
+                             occ.alloc_int8_workspace(desc))
+    assert torch.equal(part.cpu(), y[-700:])
+
+
 @pytest.mark.parametrize("T,Ne,k", [(6, 32, 2), (900, 8, 1), (700, 64, 4)])
 def test_layer_uneven_and_empty_experts(T, Ne, k):
     """Every token on the same experts, all others without rows; then half of the tokens."""
