@@ -419,17 +419,24 @@ size_t most_row_tiles8(const occ_layer_desc &D) {
 
 // Whether the layer runs without sorting its slots (int8_few.hip): each slot
 // then reads its expert's weights for itself, so what decides is the bytes that
-// all slots read.  Measured against the general path (us): 64 experts of F =
-// 1024, top 8 (50 MB a token): 1 token 18 / 33, 4 tokens 42 / 48, 5 50 / 52, 6
-// 58 / 53; 60 of F = 1408, top 4, with a shared expert of 5632 (69 MB, shared
-// bytes from the caches): 3 tokens 51 / 75, 6 84 / 90, 7 100 / 89; 128 of F =
-// 768, d = 1024, top 2 (5 MB): 16 tokens 21 / 29.
-constexpr int64_t kFewBytes = 256 << 20;
+// all slots read, and the three launches that the general path spends on each
+// shared expert.  Weights of T tokens where the few-token form stops being the
+// faster one (MiB), and us there, few / general: 64 experts of F = 1024, top 8,
+// 192 to 240 (4 tokens 42 / 45, 5 51 / 47); 60 of 1408, top 4, 165 to 198; 128 of
+// 768, top 8, 216 to 252; with one shared expert 330 (60 of 1408, top 4, one of
+// 5632: 5 tokens 75 / 76, 6 83 / 80; 64 of 1024, top 8, one of 1024: 324, 6 tokens
+// 65 / 66); with two 462 (64 of 1408, top 6, two of 1408: 6 tokens 86 / 92, 7 100 /
+// 103, 8 112 / 106); with four above 768 (64 of 1024, top 4, four of 1024: 16 tokens
+// 119 / 125).  Few tokens of small experts win throughout: 128 of 768, d = 1024,
+// top 2, with a shared one: 16 tokens 27 / 42.
+constexpr int64_t kFewBytes = 200 << 20, kFewSharedBytes = 130 << 20;
 constexpr int kFewTokenSlots = 64;
 bool few_tokens(const occ_layer_desc &D) {
-    const int64_t token = 3ll * D.d * (static_cast<int64_t>(D.k) * D.F + static_cast<int64_t>(D.n_shared) * (D.n_shared > 0 ? D.F_shared : 0));
-    return static_cast<int64_t>(D.T) * D.k <= kFewTokenSlots && D.T * token <= kFewBytes &&
-           few_fits(D.d, D.k, D.F, D.n_shared, D.F_shared);
+    const int64_t shared = D.n_shared > 0 ? static_cast<int64_t>(D.n_shared) * D.F_shared : 0;
+    const int64_t token = 3ll * D.d * (static_cast<int64_t>(D.k) * D.F + shared);
+    return static_cast<int64_t>(D.T) * D.k <= kFewTokenSlots &&
+           few_fits(D.d, D.k, D.F, D.n_shared, D.F_shared) &&
+           D.T * token <= kFewBytes + D.n_shared * kFewSharedBytes;
 }
 
 Int8Layout int8_layout(const occ_layer_desc &D) {

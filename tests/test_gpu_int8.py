@@ -188,6 +188,22 @@ def test_layer_of_many_tokens_with_shared_experts(T, d, Ne, k, F, Nd, n_shared, 
     assert torch.equal(part.cpu(), y[-700:])
 
 
+@pytest.mark.parametrize("k,F,n_shared,F_shared", [(4, 1408, 1, 5632), (6, 1408, 2, 1408), (8, 1024, 0, 0)])
+def test_layer_of_some_tokens_at_the_few_token_forms_end(k, F, n_shared, F_shared):
+    """From three to nine tokens, where the choice of form changes: each token's bits as alone."""
+    case = Case(9, 2048, 10, k, F, 2, n_shared, F_shared, seed=k + n_shared)
+    whole = case.check()
+    ex, sh = on_gpu(case.experts), on_gpu(case.shared)
+    for T in range(1, 9):
+        desc = layer(T, 2048, 10, k, F, 2, n_shared, F_shared)
+        x, ids, w = (a[:T].contiguous().cuda() for a in (case.x, case.ids, case.w))
+        n = occ.occ_int8_workspace_size(desc)
+        ws = torch.full((n + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+        y = torch.empty(T, 2048, dtype=BF16, device="cuda")
+        occ.occ_moe_forward_int8(desc, x, ids, w, case.place, ex, sh, y, ws[:n])
+        assert torch.equal(y.cpu(), whole[:T]) and (ws[n:] == 0xA5).all(), T
+
+
 @pytest.mark.parametrize("T,Ne,k", [(6, 32, 2), (900, 8, 1), (700, 64, 4)])
 def test_layer_uneven_and_empty_experts(T, Ne, k):
     """Every token on the same experts, all others without rows; then half of the tokens."""
