@@ -8,8 +8,8 @@
 //   down  a workgroup takes kFewC columns of a token over all of its slots: it
 //         asks for its weights, quantises the slots' h while they come, and
 //         adds the terms.
-// One token of top 8 (d = 2048, F = 1024): 8.3 + 8.4 us for 33.6 + 16.8 MB (4.0
-// and 2.0 TB/s), where the shortest kernel with one load takes 3 us.
+// One token of top 8 (d = 2048, F = 1024): 8.2 + 8.6 us for 33.6 + 16.8 MB (4.1
+// and 1.9 TB/s), where the shortest kernel with one load takes 3 us.
 // Codes, integer sums, terms and the order of their sum are those of the
 // general path: a token's y does not depend on the batch that it came in.
 #include "int8_rows.h"

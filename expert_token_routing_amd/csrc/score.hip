@@ -23,17 +23,17 @@ namespace {
 constexpr int kScoreThreads = 256;
 // Tokens from which a wave of 64 lanes a token takes four one after another, so
 // that their weights in 64 bits fill its lanes once: at 4096 / 8192 / 16384 /
-// 65536 tokens of 128 experts (top 8, no bias) 6.7 / 7.3 / 9.5 / 30.8 us
-// against 5.0 / 8.0 / 13.8 / 50.9 one at a time, of 256 in groups (top 8, bias)
-// 19.4 / 20.8 / 26 / 72 against 15.4 / 21.9 / 35.7 / 117; a single token 5.9
-// against 3.2.
+// 65536 tokens of 128 experts (top 8, no bias) 6.8 / 7.5 / 9.7 / 30.7 us
+// against 5.2 / 8.4 / 14.7 / 52.6 one at a time, of 256 in groups (top 8, bias)
+// 19.5 / 21.7 / 26.1 / 74 against 16.2 / 22.6 / 36.6 / 116; a single token 6.1
+// against 3.3.
 constexpr int kScoreSerial = 8192;
 // Tokens up to which 33 to 64 experts with groups or a bias take a wave a token,
 // one expert a lane: its steps are fewer where one token's chain is what a
 // launch waits for.  64 experts, top 8, in groups with a bias: 1 / 64 / 512 /
-// 2048 tokens 4.4 / 4.8 / 5.4 / 6.5 us against 5.8 / 6.3 / 7.0 / 7.8 with 16
-// lanes, 4096 even, 8192 15.4 against 9.1 to 11.  Without either, or with fewer
-// experts, within a tenth on both sides.
+// 2048 tokens 4.5 / 5.0 / 5.1 / 6.8 us against 6.1 / 6.5 / 6.7 / 8.1 with 16
+// lanes, 4096 8.0 against 8.2, 8192 13.8 against 11.5.  Without either, or with
+// fewer experts, within a tenth on both sides.
 constexpr int kScoreWide = 2048;
 constexpr unsigned kScoreGrid = 1 << 20;  // workgroups; more tokens loop
 
@@ -493,11 +493,14 @@ __device__ __forceinline__ uint64_t keep_groups(const uint32_t *key, GroupScore 
 // of a wave take few_best.  A wave makes the choice of four tokens (16 lanes
 // each, or all lanes one token after another) and then forms their weights in
 // 64 bits, 16 lanes a token.  Up to 64 experts 16 lanes a token (but see
-// kScoreWide): at 512 / 8192 / 65536 tokens of 60 experts, top 4, 3.5 / 3.8 /
-// 10.9 us against 3.7 / 7.0 / 29.5 with 64, 65536 of 64 in groups with a bias,
-// top 8, 32 against 58.  The 65536 tokens
-// of 60 experts read and write 18 MB (1.7 TB/s), 32768 of 256 in groups 36 MB
-// in 42 us (0.8 TB/s).
+// kScoreWide): at 512 / 8192 / 65536 tokens of 60 experts, top 4, 3.6 / 3.9 /
+// 11.0 us against 3.7 / 7.0 / 29.5 with 64, 65536 of 64 in groups with a bias,
+// top 8, 33 against 78.  The 65536 tokens of 60 experts read and write 18 MB (1.7
+// TB/s) in 93 vector and 38 scalar instructions a token, of 64 in groups with a
+// bias 21 MB (0.6 TB/s) in 246 and 86, 32768 of 256 in groups 36 MB in 43 us (0.8
+// TB/s) in 433 and 308.  choose64 is what they are far from: 65536 tokens of 64
+// experts in groups take 111 us where most of them need it (sigmoids of logits of
+// a deviation of 8, rounded to bf16, a bias of zeros).
 template <int L, int NI, bool GROUPS, bool BIASED>
 __global__ __launch_bounds__(kScoreThreads, 4) void k_route_scored(ScoreArgs a) {
     constexpr int TEAMS = kWave / L, WAVES = kScoreThreads / kWave, TOK = 4, W = 16, KPL = kMaxK / W;
